@@ -23,6 +23,8 @@ FA_DTYPE_F32, FA_DTYPE_BF16 = 0, 1
 
 EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bwd_static_workspace", "fa_fwd_key_major",
            "fa_fwd_key_major_workspace_bytes", "fa_fwd_f32_3xtf32", "fa_fwd_f32_3xtf32_workspace_bytes",
+           "fa_fwd_shared_prefix", "fa_fwd_shared_prefix_workspace_bytes", "fa_fwd_latent_absorbed",
+           "fa_fwd_latent_absorbed_workspace_bytes", "fa_fwd_latent", "fa_bwd_latent", "fa_bwd_latent_workspace_bytes",
            "fa_last_device_status", "fa_set_wait_limit_us", "fa_selftest_wait_timeout", "fa_status_string",
            "fa_version")
 
@@ -55,6 +57,20 @@ def _load() -> ctypes.CDLL:
     L.fa_fwd_f32_3xtf32.restype = i
     L.fa_fwd_f32_3xtf32_workspace_bytes.argtypes = [i, i, i, i]
     L.fa_fwd_f32_3xtf32_workspace_bytes.restype = sz
+    L.fa_fwd_shared_prefix.argtypes = [vp] * 8 + [i] * 7 + [f, i, vp, sz, vp]
+    L.fa_fwd_shared_prefix.restype = i
+    L.fa_fwd_shared_prefix_workspace_bytes.argtypes = [i] * 7
+    L.fa_fwd_shared_prefix_workspace_bytes.restype = sz
+    L.fa_fwd_latent_absorbed.argtypes = [vp] * 6 + [i] * 8 + [f, i, vp, sz, vp]
+    L.fa_fwd_latent_absorbed.restype = i
+    L.fa_fwd_latent_absorbed_workspace_bytes.argtypes = [i] * 6
+    L.fa_fwd_latent_absorbed_workspace_bytes.restype = sz
+    L.fa_fwd_latent.argtypes = [vp] * 6 + [i] * 7 + [f, i, i, vp]
+    L.fa_fwd_latent.restype = i
+    L.fa_bwd_latent.argtypes = [vp] * 11 + [i] * 7 + [f, i, i, vp, sz, vp]
+    L.fa_bwd_latent.restype = i
+    L.fa_bwd_latent_workspace_bytes.argtypes = [i] * 7
+    L.fa_bwd_latent_workspace_bytes.restype = sz
     L.fa_last_device_status.argtypes = [vp]
     L.fa_last_device_status.restype = i
     L.fa_set_wait_limit_us.argtypes = [ctypes.c_longlong]
@@ -295,3 +311,211 @@ def fa_bwd_static_workspace(q, k, v, o, lse, do, dq, dk, dv, scale: float | None
     if st != FA_OK:
         raise FaError(st, "fa_bwd_static_workspace")
     return dq, dk, dv
+
+
+def fa_fwd_shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Np: int, Ns: int, d: int) -> int:
+    return lib.fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d)
+
+
+def fa_fwd_latent_absorbed_workspace_bytes(B: int, H: int, Nq: int, page_size: int, max_pages: int, dc: int) -> int:
+    return lib.fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc)
+
+
+def fa_bwd_latent_workspace_bytes(B: int, H: int, Nq: int, Nk: int, dn: int, dr: int, dv: int) -> int:
+    return lib.fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dv)
+
+
+def _need(name, t, shape, dtype, device):
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {device}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _first(name, t, dims):
+    """The tensor that sets a call's dtype and device: its dtype code."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
+    code = _dtype_code(t)
+    if not t.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return code
+
+
+@contextlib.contextmanager
+def _running_on(device, stream):
+    """The tensors' device made current, and the call's stream on it: the given
+    one, or that device's current stream.  Tensors a call allocates are
+    allocated on that stream (see _alloc_on)."""
+    torch = _torch()
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.device(device), _alloc_on(stream):
+        yield ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+
+
+def _workspace(workspace, need, device):
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(need, device=device, dtype=torch.uint8)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def fa_fwd_shared_prefix(q, k_prefix, v_prefix, k, v, lens, scale: float | None = None, o=None, lse=None,
+                         want_lse: bool = True, workspace=None, stream=None):
+    """Attention of a decoding batch whose sequences share one prefix; returns ``(o, lse)``.
+
+    ``q``: [B, Hq, Nq, d], each sequence's Nq new tokens; ``k_prefix,
+    v_prefix``: [Hkv, Np, d], seen by every row and read once for the batch;
+    ``k, v``: [B, Hkv, Ns, d], each sequence's own keys and values (the new
+    tokens' included), of which ``lens[b]`` (int32 [B]) are valid.  Query
+    token t sees the prefix and its own keys j < lens[b] - (Nq - 1 - t).  bf16
+    (d in {64, 96, 128}) or float32 (d <= 128), contiguous, on one device.
+    ``scale`` defaults to 1/sqrt(d).  ``workspace``: a CUDA uint8 tensor of at
+    least ``fa_fwd_shared_prefix_workspace_bytes`` bytes, or allocated here.
+    """
+    torch = _torch()
+    code = _first("q", q, 4)
+    B, Hq, Nq, d = q.shape
+    if k_prefix.dim() != 3 or k.dim() != 4:
+        raise ValueError("k_prefix must be [Hkv, Np, d] and k [B, Hkv, Ns, d]")
+    Hkv, Np, Ns = k_prefix.shape[0], k_prefix.shape[1], k.shape[2]
+    dev = q.device
+    for name, t, shape in (("k_prefix", k_prefix, (Hkv, Np, d)), ("v_prefix", v_prefix, (Hkv, Np, d)),
+                           ("k", k, (B, Hkv, Ns, d)), ("v", v, (B, Hkv, Ns, d))):
+        _need(name, t, shape, q.dtype, dev)
+    _need("lens", lens, (B,), torch.int32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    with _running_on(dev, stream) as sp:
+        o = torch.empty_like(q) if o is None else _need("o", o, q.shape, q.dtype, dev)
+        if lse is not None:
+            _need("lse", lse, (B, Hq, Nq), torch.float32, dev)
+        elif want_lse:
+            lse = torch.empty((B, Hq, Nq), device=dev, dtype=torch.float32)
+        ws = _workspace(workspace, lib.fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d), dev)
+        st = lib.fa_fwd_shared_prefix(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(lens), _ptr(o),
+                                      _ptr(lse), B, Hq, Hkv, Nq, Np, Ns, d, float(scale), code, _ptr(ws),
+                                      ws.numel() * ws.element_size(), sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_shared_prefix")
+    return o, lse
+
+
+def fa_fwd_latent_absorbed(q, cache, lens, dc: int, scale: float, block_table=None, o=None, lse=None,
+                           want_lse: bool = True, workspace=None, stream=None):
+    """Latent attention, absorbed form, over a paged cache; returns ``(o, lse)``.
+
+    ``q``: [B, H, Nq, dc+dr], each sequence's Nq new tokens; ``cache``:
+    [pages, page_size, dc+dr], one vector a token, whose first ``dc`` entries
+    are also the value; ``block_table``: int32 [B, max_pages], or None when
+    sequence b is page b; ``lens``: int32 [B], tokens in the cache, the new
+    ones included.  ``o`` is [B, H, Nq, dc].  bf16 (dc 256 or 512, dr 64, pages
+    of a multiple of 16 tokens) or float32 (dc <= 512, dr <= 128).  ``scale``
+    is the expanded head's.  ``workspace``: at least
+    ``fa_fwd_latent_absorbed_workspace_bytes`` bytes, or allocated here.
+    """
+    torch = _torch()
+    code = _first("q", q, 4)
+    B, H, Nq, dk = q.shape
+    dr = dk - dc
+    if cache.dim() != 3 or not 0 < dc < dk:
+        raise ValueError("cache must be [pages, page_size, dc + dr], with 0 < dc < dc + dr")
+    pages, page_size = cache.shape[:2]
+    dev = q.device
+    _need("cache", cache, (pages, page_size, dk), q.dtype, dev)
+    _need("lens", lens, (B,), torch.int32, dev)
+    max_pages = 1
+    if block_table is not None:
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_pages]")
+        max_pages = block_table.shape[1]
+        _need("block_table", block_table, (B, max_pages), torch.int32, dev)
+    with _running_on(dev, stream) as sp:
+        o = torch.empty((B, H, Nq, dc), device=dev, dtype=q.dtype) if o is None else \
+            _need("o", o, (B, H, Nq, dc), q.dtype, dev)
+        if lse is not None:
+            _need("lse", lse, (B, H, Nq), torch.float32, dev)
+        elif want_lse:
+            lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
+        ws = _workspace(workspace, lib.fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc), dev)
+        st = lib.fa_fwd_latent_absorbed(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(lens), _ptr(o), _ptr(lse), B, H,
+                                        Nq, pages, page_size, max_pages, dc, dr, float(scale), code, _ptr(ws),
+                                        ws.numel() * ws.element_size(), sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_latent_absorbed")
+    return o, lse
+
+
+def _check_latent(q, k_nope, k_rope, v):
+    code = _first("q", q, 4)
+    if k_nope.dim() != 4 or v.dim() != 4:
+        raise ValueError("k_nope and v must be [B, H, Nk, d]")
+    B, H, Nq, dk = q.shape
+    Nk, dn, dv = k_nope.shape[2], k_nope.shape[3], v.shape[3]
+    if not 0 < dn < dk:
+        raise ValueError("q must be [B, H, Nq, dn + dr]")
+    _need("k_nope", k_nope, (B, H, Nk, dn), q.dtype, q.device)
+    _need("k_rope", k_rope, (B, Nk, dk - dn), q.dtype, q.device)
+    _need("v", v, (B, H, Nk, dv), q.dtype, q.device)
+    return code, (B, H, Nq, Nk, dn, dk - dn, dv)
+
+
+def fa_fwd_latent(q, k_nope, k_rope, v, scale: float | None = None, causal: bool = True, o=None, lse=None,
+                  want_lse: bool = True, stream=None):
+    """Latent attention, expanded form; returns ``(o, lse)``.
+
+    ``q``: [B, H, Nq, dn+dr]; ``k_nope``: [B, H, Nk, dn]; ``k_rope``: [B, Nk,
+    dr], shared by the heads; ``v``: [B, H, Nk, dv]; ``o``: [B, H, Nq, dv].
+    ``causal``: row i sees keys j <= i + Nk - Nq.  bf16 (dn = 128, dr = 64, dv =
+    128) or float32 (dn + dr <= 256, dv <= 128).  ``scale`` defaults to
+    1/sqrt(dn + dr).
+    """
+    torch = _torch()
+    code, (B, H, Nq, Nk, dn, dr, dv) = _check_latent(q, k_nope, k_rope, v)
+    dev = q.device
+    if scale is None:
+        scale = 1.0 / math.sqrt(dn + dr)
+    with _running_on(dev, stream) as sp:
+        o = torch.empty((B, H, Nq, dv), device=dev, dtype=q.dtype) if o is None else \
+            _need("o", o, (B, H, Nq, dv), q.dtype, dev)
+        if lse is not None:
+            _need("lse", lse, (B, H, Nq), torch.float32, dev)
+        elif want_lse:
+            lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
+        st = lib.fa_fwd_latent(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), B, H, Nq, Nk, dn, dr,
+                               dv, float(scale), int(bool(causal)), code, sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_latent")
+    return o, lse
+
+
+def fa_bwd_latent(q, k_nope, k_rope, v, o, lse, do, scale: float | None = None, causal: bool = True, dq=None,
+                  dk_nope=None, dk_rope=None, dv=None, workspace=None, stream=None):
+    """Gradients ``(dq, dk_nope, dk_rope, dv)`` of ``fa_fwd_latent``, by
+    recomputation from its outputs ``o`` and ``lse`` and ``do`` = dL/dO.  The
+    workspace (at least ``fa_bwd_latent_workspace_bytes`` bytes) is taken from
+    ``workspace`` or allocated here."""
+    torch = _torch()
+    code, (B, H, Nq, Nk, dn, dr, dvw) = _check_latent(q, k_nope, k_rope, v)
+    dev = q.device
+    _need("o", o, (B, H, Nq, dvw), q.dtype, dev)
+    _need("do", do, (B, H, Nq, dvw), q.dtype, dev)
+    _need("lse", lse, (B, H, Nq), torch.float32, dev)
+    if scale is None:
+        scale = 1.0 / math.sqrt(dn + dr)
+    with _running_on(dev, stream) as sp:
+        dq, dk_nope, dk_rope, dv = (torch.empty_like(t) if g is None else _need(name, g, t.shape, q.dtype, dev)
+                                    for name, g, t in (("dq", dq, q), ("dk_nope", dk_nope, k_nope),
+                                                       ("dk_rope", dk_rope, k_rope), ("dv", dv, v)))
+        ws = _workspace(workspace, lib.fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dvw), dev)
+        st = lib.fa_bwd_latent(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
+                               _ptr(dk_nope), _ptr(dk_rope), _ptr(dv), B, H, Nq, Nk, dn, dr, dvw, float(scale),
+                               int(bool(causal)), code, _ptr(ws), ws.numel() * ws.element_size(), sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_bwd_latent")
+    return dq, dk_nope, dk_rope, dv

@@ -12,6 +12,7 @@
 
 #include "fa.h"
 #include "kernels.h"
+#include "seq_kernels.h"
 #include "sm103.cuh"
 
 namespace fa {
@@ -156,6 +157,10 @@ __global__ void selftest_wait_kernel(unsigned int* status, unsigned long long li
 }
 
 }  // namespace
+
+cudaError_t device_status_ptr(unsigned int** out) { return status_ptr(out); }
+unsigned long long device_wait_ns() { return wait_ns(); }
+EncodeTiledFnPtr encode_tiled_fn() { return encode_fn(); }
 
 cudaError_t launch_selftest_wait(unsigned int* status, unsigned long long limit_ns, cudaStream_t s) {
   selftest_wait_kernel<<<1, 32, 0, s>>>(status, limit_ns);
@@ -365,6 +370,7 @@ fa_status fa_last_device_status(void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return FA_ERR_CUDA;
   if (host & sm103::kStatusTimeout) return FA_ERR_TIMEOUT;
   if (host & sm103::kStatusLayout) return FA_ERR_CUDA;
+  if (host & sm103::kStatusInput) return FA_ERR_INVALID;
   return FA_OK;
 }
 

@@ -1,0 +1,323 @@
+// seq_api.cu -- the C ABI of the language-model operators declared in
+// include/fa.h: latent attention (expanded forward and backward, absorbed)
+// and shared-prefix attention.  Argument checks, workspace layouts, dispatch.
+// Nothing here allocates device memory or synchronises.
+#include <cmath>
+#include <cstdint>
+
+#include "fa.h"
+#include "seq_kernels.h"
+
+namespace fa {
+namespace {
+
+bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// a * b * ... of positive ints, or -1 past 2^40
+long long product(const int* x, int n) {
+  long long r = 1;
+  for (int i = 0; i < n; ++i) {
+    if (x[i] < 1) return -1;
+    if (r > (1LL << 40) / x[i]) return -1;
+    r *= x[i];
+  }
+  return r;
+}
+template <typename... I>
+bool sizes_ok(I... x) {
+  const int v[] = {x...};
+  return product(v, sizeof...(x)) > 0;
+}
+bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.f; }
+bool dtype_ok(fa_dtype dt) { return dt == FA_DTYPE_F32 || dt == FA_DTYPE_BF16; }
+
+// partial results [splits][rows] of dv entries and their lse
+struct PartLayout {
+  int splits_a, splits_b;
+  size_t off_lse, bytes;
+};
+PartLayout part_layout(int sa, int sb, long long rows, int dv) {
+  PartLayout w{sa, sb, 0, 0};
+  const size_t n = static_cast<size_t>(sa + sb) * rows;
+  w.off_lse = up256(n * dv * 4);
+  w.bytes = w.off_lse + up256(n * 4);
+  return w;
+}
+
+PartLayout prefix_layout(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
+  const int G = Hq / Hkv;
+  const int sp = seq_simt_splits(Hkv, B * G * Nq, Np);
+  const int ss = seq_simt_splits(static_cast<long long>(B) * Hkv, G * Nq, Ns);
+  return part_layout(sp, ss, static_cast<long long>(B) * Hq * Nq, d);
+}
+bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
+  if (Np < 0 || Ns < 0 || Hkv < 1 || Hq % Hkv != 0) return false;
+  return sizes_ok(B, Hq, Nq, d) && sizes_ok(B, Hkv, Ns > 0 ? Ns : 1, d) && sizes_ok(Hkv, Np > 0 ? Np : 1, d) &&
+         static_cast<long long>(B) * Hq * Nq <= 0x7fffffffLL;
+}
+
+PartLayout absorbed_layout(int B, int H, int Nq, int n_keys, int dc) {
+  const int sp = seq_simt_splits(B, H * Nq, n_keys);
+  return part_layout(sp, 0, static_cast<long long>(B) * H * Nq, dc);
+}
+// tokens a sequence can hold, or -1
+long long absorbed_keys(int page_size, int max_pages) {
+  const long long n = static_cast<long long>(page_size) * max_pages;
+  return n <= 0x7fffff00LL ? n : -1;
+}
+
+bool expanded_sizes_ok(int B, int H, int Nq, int Nk, int dn, int dr, int dv) {
+  return sizes_ok(B, H, Nq, dn) && sizes_ok(B, H, Nq, dr) && sizes_ok(B, H, Nq, dv) && sizes_ok(B, H, Nk, dn) &&
+         sizes_ok(B, H, Nk, dr) && sizes_ok(B, H, Nk, dv) && dn <= 4096 && dr <= 4096 && dv <= 4096 &&
+         static_cast<long long>(B) * H <= 0x7fffffffLL && Nq <= 0x3fffffff && Nk <= 0x3fffffff;
+}
+fa_status expanded_check(int B, int H, int Nq, int Nk, int dn, int dr, int dv, float scale, int causal, fa_dtype dt) {
+  if (!expanded_sizes_ok(B, H, Nq, Nk, dn, dr, dv)) return FA_ERR_INVALID;
+  if (!scale_ok(scale) || !dtype_ok(dt) || (causal != 0 && causal != 1)) return FA_ERR_INVALID;
+  if (dt == FA_DTYPE_BF16 && !(dn == 128 && dr == 64 && dv == 128)) return FA_ERR_UNSUPPORTED;
+  if (dt == FA_DTYPE_F32 && (dn + dr > 256 || dv > 128)) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+fa_status of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
+  if (!prefix_sizes_ok(B, Hq, Hkv, Nq, Np, Ns, d)) return 0;
+  return prefix_layout(B, Hq, Hkv, Nq, Np, Ns, d).bytes;
+}
+
+fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
+                               const int* lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int Np, int Ns,
+                               int d, float scale, fa_dtype dt, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  if (!prefix_sizes_ok(B, Hq, Hkv, Nq, Np, Ns, d)) return FA_ERR_INVALID;
+  if (!q || !o || !lens || !workspace || (Np > 0 && (!k_prefix || !v_prefix)) || (Ns > 0 && (!k || !v)))
+    return FA_ERR_INVALID;
+  const void* ptrs[] = {q, o, k_prefix, v_prefix, k, v};
+  for (const void* x : ptrs)
+    if (!aligned(x, 16)) return FA_ERR_INVALID;
+  if (!aligned(lse, 4) || !aligned(lens, 4) || !aligned(workspace, 256)) return FA_ERR_INVALID;
+  if (!scale_ok(scale) || !dtype_ok(dt)) return FA_ERR_INVALID;
+  if (dt == FA_DTYPE_BF16 && d != 64 && d != 96 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (dt == FA_DTYPE_F32 && d > 128) return FA_ERR_UNSUPPORTED;
+  const PartLayout w = prefix_layout(B, Hq, Hkv, Nq, Np, Ns, d);
+  if (workspace_bytes < w.bytes) return FA_ERR_INVALID;
+
+  const int G = Hq / Hkv;
+  SeqAttn p{};
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.n_new = Nq;
+  p.d1 = d;
+  p.dv = d;
+  p.v_stride = d;
+  p.k2_div = 1;
+  p.lens_div = 1;
+  p.scale = scale;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.off_lse);
+  p.total = static_cast<long long>(B) * Hq * Nq;
+  p.wait_ns = device_wait_ns();
+  if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  // the prefix: one group per key/value head, the rows of every sequence
+  SeqAttn a = p;
+  a.groups = Hkv;
+  a.rows = B * G * Nq;
+  a.group_div = Hkv;
+  a.row_block = G * Nq;
+  a.q_s2 = G * Nq;
+  a.q_s3 = static_cast<long long>(Hq) * Nq;
+  a.k1 = k_prefix;
+  a.v = v_prefix;
+  a.n_keys = Np;
+  a.splits = w.splits_a;
+  a.part0 = 0;
+  cudaError_t e = launch_seq_simt(a, dt, s);
+  if (e != cudaSuccess) return FA_ERR_CUDA;
+
+  // the sequences' own keys: one group per sequence and key/value head
+  SeqAttn b = p;
+  b.groups = B * Hkv;
+  b.rows = G * Nq;
+  b.group_div = Hkv;
+  b.row_block = kAllRows;
+  b.q_s1 = static_cast<long long>(Hq) * Nq;
+  b.q_s2 = G * Nq;
+  b.k1 = k;
+  b.v = v;
+  b.n_keys = Ns;
+  b.lens = lens;
+  b.lens_div = Hkv;
+  b.causal = 1;
+  b.splits = w.splits_b;
+  b.part0 = w.splits_a;
+  e = launch_seq_simt(b, dt, s);
+  if (e != cudaSuccess) return FA_ERR_CUDA;
+  return of(launch_seq_combine(p.part_o, p.part_lse, w.splits_a + w.splits_b, p.total, d, o, lse, dt, s));
+}
+
+size_t fa_fwd_latent_absorbed_workspace_bytes(int B, int H, int Nq, int page_size, int max_pages, int dc) {
+  if (!sizes_ok(B, H, Nq, dc) || page_size < 1 || max_pages < 1 || absorbed_keys(page_size, max_pages) < 0) return 0;
+  return absorbed_layout(B, H, Nq, static_cast<int>(absorbed_keys(page_size, max_pages)), dc).bytes;
+}
+
+fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* block_table, const int* lens, void* o,
+                                 float* lse, int B, int H, int Nq, int n_pages, int page_size, int max_pages, int dc,
+                                 int dr, float scale, fa_dtype dt, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  if (!q || !cache || !lens || !o || !workspace) return FA_ERR_INVALID;
+  if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16) || !aligned(workspace, 256)) return FA_ERR_INVALID;
+  if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(lse, 4)) return FA_ERR_INVALID;
+  if (!sizes_ok(B, H, Nq, dc) || !sizes_ok(B, H, Nq, dr) || dc > 4096 || dr > 4096) return FA_ERR_INVALID;
+  if (!sizes_ok(n_pages, page_size, dc + dr) || !sizes_ok(B, max_pages)) return FA_ERR_INVALID;
+  if (static_cast<long long>(B) * H * Nq > 0x7fffffffLL || absorbed_keys(page_size, max_pages) < 0)
+    return FA_ERR_INVALID;
+  if (!block_table && (max_pages != 1 || n_pages < B)) return FA_ERR_INVALID;
+  if (!scale_ok(scale) || !dtype_ok(dt)) return FA_ERR_INVALID;
+  if (dt == FA_DTYPE_BF16 && !((dc == 256 || dc == 512) && dr == 64)) return FA_ERR_UNSUPPORTED;
+  if (dt == FA_DTYPE_BF16 && block_table && page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (dt == FA_DTYPE_F32 && (dc > 512 || dr > 128)) return FA_ERR_UNSUPPORTED;
+  const int n_keys = static_cast<int>(absorbed_keys(page_size, max_pages));
+  const PartLayout w = absorbed_layout(B, H, Nq, n_keys, dc);
+  if (workspace_bytes < w.bytes) return FA_ERR_INVALID;
+
+  SeqAttn p{};
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.groups = B;
+  p.rows = H * Nq;
+  p.group_div = 1;
+  p.row_block = kAllRows;
+  p.n_new = Nq;
+  p.q_s1 = static_cast<long long>(H) * Nq;
+  p.k1 = cache;
+  p.v = cache;
+  p.d1 = dc + dr;
+  p.dv = dc;
+  p.v_stride = dc + dr;
+  p.n_keys = n_keys;
+  p.k2_div = 1;
+  p.lens = lens;
+  p.lens_div = 1;
+  p.table = block_table;
+  p.page_size = page_size;
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.causal = 1;
+  p.scale = scale;
+  p.splits = w.splits_a;
+  p.total = static_cast<long long>(B) * H * Nq;
+  if (w.splits_a > 1) {
+    p.part_o = static_cast<float*>(workspace);
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.off_lse);
+  }
+  p.wait_ns = device_wait_ns();
+  if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_seq_simt(p, dt, s);
+  if (e != cudaSuccess || w.splits_a == 1) return of(e);
+  return of(launch_seq_combine(p.part_o, p.part_lse, w.splits_a, p.total, dc, o, lse, dt, s));
+}
+
+fa_status fa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, void* o, float* lse,
+                        int B, int H, int Nq, int Nk, int dn, int dr, int dv, float scale, int causal, fa_dtype dt,
+                        void* stream) {
+  const void* ptrs[] = {q, k_nope, k_rope, v, o};
+  for (const void* x : ptrs)
+    if (!x || !aligned(x, 16)) return FA_ERR_INVALID;
+  if (!aligned(lse, 4)) return FA_ERR_INVALID;
+  const fa_status c = expanded_check(B, H, Nq, Nk, dn, dr, dv, scale, causal, dt);
+  if (c != FA_OK) return c;
+  SeqAttn p{};
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.groups = B * H;
+  p.rows = Nq;
+  p.group_div = 1;
+  p.row_block = kAllRows;
+  p.n_new = Nq;
+  p.q_s1 = Nq;
+  p.k1 = k_nope;
+  p.k2 = k_rope;
+  p.v = v;
+  p.d1 = dn;
+  p.d2 = dr;
+  p.dv = dv;
+  p.v_stride = dv;
+  p.n_keys = Nk;
+  p.k2_div = H;
+  p.lens_div = 1;
+  p.causal = causal;
+  p.scale = scale;
+  p.splits = 1;
+  p.total = static_cast<long long>(B) * H * Nq;
+  p.wait_ns = device_wait_ns();
+  if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+  return of(launch_seq_simt(p, dt, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_bwd_latent_workspace_bytes(int B, int H, int Nq, int Nk, int dn, int dr, int dv) {
+  if (!expanded_sizes_ok(B, H, Nq, Nk, dn, dr, dv)) return 0;
+  return latent_bwd_workspace_layout(B, H, Nq, Nk, dr, nullptr, nullptr);
+}
+
+fa_status fa_bwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, const void* o,
+                        const float* lse, const void* dO, void* dq, void* dk_nope, void* dk_rope, void* dv_out, int B,
+                        int H, int Nq, int Nk, int dn, int dr, int dv, float scale, int causal, fa_dtype dt,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  const void* ptrs[] = {q, k_nope, k_rope, v, o, dO, dq, dk_nope, dk_rope, dv_out};
+  for (const void* x : ptrs)
+    if (!x || !aligned(x, 16)) return FA_ERR_INVALID;
+  if (!lse || !aligned(lse, 4) || !workspace || !aligned(workspace, 256)) return FA_ERR_INVALID;
+  const fa_status c = expanded_check(B, H, Nq, Nk, dn, dr, dv, scale, causal, dt);
+  if (c != FA_OK) return c;
+  if (workspace_bytes < fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dv)) return FA_ERR_INVALID;
+  LatentBwd p{};
+  p.q = q;
+  p.kn = k_nope;
+  p.kr = k_rope;
+  p.v = v;
+  p.o = o;
+  p.dO = dO;
+  p.lse = lse;
+  p.dq = dq;
+  p.dkn = dk_nope;
+  p.dkr = dk_rope;
+  p.dv_out = dv_out;
+  p.B = B;
+  p.H = H;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.dn = dn;
+  p.dr = dr;
+  p.dv = dv;
+  p.causal = causal;
+  p.scale = scale;
+  size_t off_dsum = 0, off_part = 0;
+  latent_bwd_workspace_layout(B, H, Nq, Nk, dr, &off_dsum, &off_part);
+  p.lse2 = static_cast<float*>(workspace);
+  p.dsum = reinterpret_cast<float*>(static_cast<char*>(workspace) + off_dsum);
+  p.dkr_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + off_part);
+  p.wait_ns = device_wait_ns();
+  if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_latent_bwd_prep(p, dt, s);
+  if (e == cudaSuccess) e = launch_latent_bwd_simt(p, dt, s);
+  if (e == cudaSuccess) e = launch_latent_bwd_dkr(p, dt, s);
+  return of(e);
+}
+
+}  // extern "C"

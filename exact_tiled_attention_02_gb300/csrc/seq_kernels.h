@@ -1,0 +1,99 @@
+// seq_kernels.h -- internal interface between the C-ABI layer (seq_api.cu)
+// and the kernels of the language-model operators: latent attention
+// (expanded and absorbed) and shared-prefix attention.  Not part of the
+// public ABI.
+#pragma once
+
+#include "kernels.h"
+
+namespace fa {
+
+constexpr int kAllRows = 0x7fffffff;  // SeqAttn::row_block of a problem whose rows are one block
+
+// One attention problem family: groups of query rows, each group against its
+// own keys.  Every index is in rows (tokens), never in bytes.
+struct SeqAttn {
+  // query row r of group g is row
+  //   (g / group_div) * q_s1 + (g % group_div) * q_s2 + (r / row_block) * q_s3 + r % row_block
+  // of q, o and lse (q rows have dk = d1 + d2 entries, o rows dv), and token
+  // r % n_new of its sequence's n_new new ones
+  const void* q;
+  void* o;
+  float* lse;  // may be null
+  int groups, rows;
+  int group_div, row_block, n_new;
+  long long q_s1, q_s2, q_s3;
+  // keys j < nk: nk = n_keys, or lens[g / lens_div] where lens is given
+  // (clamped to 0 .. n_keys).  A key's entries are k1 row (g * n_keys + j) and
+  // k2 row ((g / k2_div) * n_keys + j); its value is v row (g * n_keys + j).
+  // With page_size > 0 the k1 and v row is page * page_size + j % page_size
+  // instead, page = table[g * max_pages + j / page_size], or g without a table.
+  const void* k1;
+  const void* k2;
+  const void* v;
+  int d1, d2, dv, v_stride;  // v rows are v_stride entries apart
+  int n_keys, k2_div;
+  const int* lens;
+  int lens_div;
+  const int* table;
+  int page_size, max_pages, n_pages;
+  // a row sees keys j < nk - (causal ? n_new - 1 - r % n_new : 0)
+  int causal;
+  float scale;
+  // splits > 1 or part_o given: results go to part_o [part0 + split][total][dv]
+  // and part_lse [part0 + split][total] (fp32) instead of o and lse
+  int splits;
+  float* part_o;
+  float* part_lse;
+  int part0;
+  long long total;  // rows of o
+  unsigned int* status;
+  unsigned long long wait_ns;
+};
+
+// fp32 on CUDA cores (seq_fwd_simt.cu).
+cudaError_t launch_seq_simt(const SeqAttn& p, fa_dtype dt, cudaStream_t s);
+// Splits of the keys that give the launch enough blocks.
+int seq_simt_splits(long long groups, int rows, int max_keys);
+
+// o, lse = the merged partial results [splits][total] (seq_combine.cu).
+cudaError_t launch_seq_combine(const float* part_o, const float* part_lse, int splits, long long total, int dv,
+                               void* o, float* lse, fa_dtype dt, cudaStream_t s);
+
+// Expanded latent attention's backward.
+struct LatentBwd {
+  const void* q;   // [B,H,Nq,dn+dr]
+  const void* kn;  // [B,H,Nk,dn]
+  const void* kr;  // [B,Nk,dr]
+  const void* v;   // [B,H,Nk,dv]
+  const void* o;
+  const void* dO;  // [B,H,Nq,dv]
+  const float* lse;
+  void* dq;
+  void* dkn;
+  void* dkr;
+  void* dv_out;
+  int B, H, Nq, Nk, dn, dr, dv;
+  int causal;
+  float scale;
+  // workspace: lse2 and dsum [B*H][Nq rounded up to 128] fp32 (-lse log2 e and
+  // -D; rows past Nq: -inf and 0), dkr_part [B*H][Nk][dr] fp32
+  float* lse2;
+  float* dsum;
+  float* dkr_part;
+  unsigned int* status;
+  unsigned long long wait_ns;
+};
+size_t latent_bwd_workspace_layout(int B, int H, int Nq, int Nk, int dr, size_t* off_dsum, size_t* off_part);
+cudaError_t launch_latent_bwd_prep(const LatentBwd& p, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_latent_bwd_simt(const LatentBwd& p, fa_dtype dt, cudaStream_t s);
+// dkr = the sum over heads of dkr_part
+cudaError_t launch_latent_bwd_dkr(const LatentBwd& p, fa_dtype dt, cudaStream_t s);
+
+// From fa_api.cu: the device status word of the current device, the time
+// limit of device-side waits, cuTensorMapEncodeTiled.
+cudaError_t device_status_ptr(unsigned int** out);
+unsigned long long device_wait_ns();
+EncodeTiledFnPtr encode_tiled_fn();
+
+}  // namespace fa

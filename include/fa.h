@@ -190,10 +190,126 @@ fa_status fa_bwd_static_workspace(const void* q, const void* k, const void* v, c
                                   void* stream);
 
 /*
+ * Attention for language models: shared prefix, latent keys and values
+ * -------------------------------------------------------------------
+ * The calls below compute the same softmax attention with the head layouts,
+ * caches and masks of a language model.  The pages describe none of them;
+ * they are written from the formulas given here.  Common to all:
+ *   - bf16 runs on the tensor cores (fp32 accumulation, P rounded to bf16
+ *     before it multiplies V), float32 on CUDA cores in plain fp32.
+ *   - "New tokens": a sequence's Nq query tokens are its last ones, so query
+ *     token t sees the keys j < n - (Nq - 1 - t) of its n keys.  A query row
+ *     that sees no key (t too early, or an empty sequence) gets O = 0 and
+ *     lse = -inf, and adds nothing to any gradient.
+ *   - lens and block_table are int32 arrays in device memory, read when the
+ *     kernels run (a captured graph sees their contents at replay).  A length
+ *     below 0 counts as 0, one above the capacity as the capacity, a page
+ *     index outside the cache as a page of zeros; each is reported by
+ *     fa_last_device_status() as FA_ERR_INVALID.  Nothing out of range is read.
+ *   - Entries of K, V and the cache at positions a sequence's length does not
+ *     cover may hold anything (NaN included); those within it must be finite.
+ *   - Outputs must not overlap inputs, nor the workspace anything.
+ *   - The order of every sum is fixed by the shapes, the lengths and the
+ *     number of SMs: results repeat bit for bit.
+ */
+
+/*
+ * Attention of a decoding batch whose sequences begin with one shared prefix.
+ * The prefix's keys and values are stored, and read, once for the whole
+ * batch.  Query head h uses key/value head h / (Hq / Hkv).
+ *   q            [B,Hq,Nq,d], a sequence's Nq new tokens.
+ *   k_prefix, v_prefix  [Hkv,Np,d]: seen by every query row.  Np may be 0
+ *                (then both may be NULL).
+ *   k, v         [B,Hkv,Ns,d]: each sequence's own keys and values after the
+ *                prefix, those of the new tokens included; positions
+ *                j < lens[b] are valid.  Ns may be 0 (then both may be NULL).
+ *   lens         int32 [B], 0 <= lens[b] <= Ns.
+ *   o, lse       [B,Hq,Nq,d] and float32 [B,Hq,Nq] (or NULL), over the
+ *                prefix's and the sequence's own keys together.
+ *   workspace    at least fa_fwd_shared_prefix_workspace_bytes() bytes,
+ *                256-byte aligned; contents on entry do not matter and are
+ *                undefined on return.
+ * Hq must be a multiple of Hkv.  bf16 with d = 64, 96 or 128; float32 with
+ * 1 <= d <= 128; others return FA_ERR_UNSUPPORTED.  Forward only: a serving
+ * call.
+ */
+fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                               const void* v, const int* lens, void* o, float* lse,
+                               int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d, float scale, fa_dtype dt,
+                               void* workspace, size_t workspace_bytes, void* stream);
+size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d);
+
+/*
+ * Latent attention, absorbed form (serving): every head attends to one shared
+ * vector per token, c = [latent | rotary] of dc + dr entries, as the key, and
+ * to its first dc entries as the value:
+ *     S_ij = scale q_i . c_j,  O_i = sum_j softmax_j(S_i) c_j[:dc]
+ * (the per-head up-projections are folded into q before, and applied to O
+ * after, the call).
+ *   q            [B,H,Nq,dc+dr], a sequence's Nq new tokens.
+ *   cache        [n_pages,page_size,dc+dr].
+ *   block_table  int32 [B,max_pages]: page of the sequence's tokens
+ *                p * page_size ...; entries past its length are not read.
+ *                NULL: sequence b is page b (then max_pages must be 1 and
+ *                n_pages >= B).
+ *   lens         int32 [B], tokens in the cache, the new ones included,
+ *                0 <= lens[b] <= max_pages * page_size.
+ *   o, lse       [B,H,Nq,dc] and float32 [B,H,Nq] (or NULL).
+ *   scale        of the expanded head, usually 1/sqrt(its q and k width).
+ *   workspace    at least fa_fwd_latent_absorbed_workspace_bytes() bytes,
+ *                256-byte aligned, as above.
+ * bf16 with dc = 256 or 512, dr = 64 and, with a table, page_size a multiple
+ * of 16; float32 with dc <= 512, dr <= 128; others return
+ * FA_ERR_UNSUPPORTED.  Forward only: training uses the expanded form.
+ */
+fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* block_table, const int* lens,
+                                 void* o, float* lse, int B, int H, int Nq, int n_pages, int page_size,
+                                 int max_pages, int dc, int dr, float scale, fa_dtype dt,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+size_t fa_fwd_latent_absorbed_workspace_bytes(int B, int H, int Nq, int page_size, int max_pages, int dc);
+
+/*
+ * Latent attention, expanded form (training and prefill): each head's keys
+ * are [k_nope | k_rope], the rotary part shared by the heads of a token, and
+ * its values have a width of their own:
+ *     S_ij = scale (q_i[:dn] . k_nope_j + q_i[dn:] . k_rope_j)
+ *   q            [B,H,Nq,dn+dr].
+ *   k_nope, v    [B,H,Nk,dn], [B,H,Nk,dv].     k_rope  [B,Nk,dr].
+ *   o, lse       [B,H,Nq,dv] and float32 [B,H,Nq] (or NULL).
+ *   causal       1: query row i sees keys j <= i + Nk - Nq (rows are the last
+ *                Nq of Nk tokens; with Nq > Nk the first Nq - Nk rows see
+ *                none); 0: every key.
+ * A batch of unequal lengths is padded on the right: with causal = 1 no real
+ * token sees the padding behind it.
+ * bf16 with dn = 128, dr = 64, dv = 128; float32 with dn + dr <= 256,
+ * dv <= 128; others return FA_ERR_UNSUPPORTED.
+ */
+fa_status fa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, void* o, float* lse,
+                        int B, int H, int Nq, int Nk, int dn, int dr, int dv, float scale, int causal, fa_dtype dt,
+                        void* stream);
+
+/*
+ * Its backward, by recomputation from the forward's o and lse:
+ *     dV = P^T dO, dS = P o (dO V^T - D), D_i = dO_i . O_i,
+ *     dq = scale dS [k_nope | k_rope], dk_nope = scale dS^T q[:dn],
+ *     dk_rope = scale (sum over heads) dS^T q[dn:].
+ *   dq, dk_nope, dk_rope, dv_out   shapes and dtype of q, k_nope, k_rope, v.
+ *   workspace    at least fa_bwd_latent_workspace_bytes() bytes, 256-byte
+ *                aligned, as above.
+ * No atomics: gradients repeat bit for bit.  Other arguments as fa_fwd_latent.
+ */
+fa_status fa_bwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, const void* o,
+                        const float* lse, const void* dO, void* dq, void* dk_nope, void* dk_rope, void* dv_out,
+                        int B, int H, int Nq, int Nk, int dn, int dr, int dv, float scale, int causal, fa_dtype dt,
+                        void* workspace, size_t workspace_bytes, void* stream);
+size_t fa_bwd_latent_workspace_bytes(int B, int H, int Nq, int Nk, int dn, int dr, int dv);
+
+/*
  * Synchronises `stream` (as void* cudaStream_t), then reads and clears the
  * device status word that the kernels set when a bounded wait runs out.
- * Returns FA_OK, FA_ERR_TIMEOUT, or FA_ERR_CUDA if synchronising failed or a
- * kernel refused to run on the device (a layout check failed).
+ * Returns FA_OK, FA_ERR_TIMEOUT, FA_ERR_INVALID (a length or page index in
+ * device memory was out of range), or FA_ERR_CUDA if synchronising failed or
+ * a kernel refused to run on the device (a layout check failed).
  */
 fa_status fa_last_device_status(void* stream);
 

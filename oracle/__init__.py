@@ -36,3 +36,9 @@ from .attention import (  # noqa: F401
     tiled_forward,
     dense_backward,
 )
+from .sequence import (  # noqa: F401
+    new_token_mask,
+    masked_probabilities,
+    masked_forward,
+    masked_backward,
+)
