@@ -266,7 +266,8 @@ fa_status fa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, c
   p.total = static_cast<long long>(B) * H * Nq;
   p.wait_ns = device_wait_ns();
   if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
-  return of(launch_seq_simt(p, dt, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return of(dt == FA_DTYPE_BF16 ? launch_seq_rows(p, s) : launch_seq_simt(p, dt, s));
 }
 
 size_t fa_bwd_latent_workspace_bytes(int B, int H, int Nq, int Nk, int dn, int dr, int dv) {
@@ -315,7 +316,7 @@ fa_status fa_bwd_latent(const void* q, const void* k_nope, const void* k_rope, c
   if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_latent_bwd_prep(p, dt, s);
-  if (e == cudaSuccess) e = launch_latent_bwd_simt(p, dt, s);
+  if (e == cudaSuccess) e = dt == FA_DTYPE_BF16 ? launch_latent_bwd_sm103(p, s) : launch_latent_bwd_simt(p, dt, s);
   if (e == cudaSuccess) e = launch_latent_bwd_dkr(p, dt, s);
   return of(e);
 }

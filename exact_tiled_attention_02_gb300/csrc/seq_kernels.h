@@ -56,6 +56,10 @@ cudaError_t launch_seq_simt(const SeqAttn& p, fa_dtype dt, cudaStream_t s);
 // Splits of the keys that give the launch enough blocks.
 int seq_simt_splits(long long groups, int rows, int max_keys);
 
+// bf16 on the tensor cores, many rows a group (seq_rows_sm103.cu): no lens, no
+// pages; the expanded latent shape.
+cudaError_t launch_seq_rows(const SeqAttn& p, cudaStream_t s);
+
 // o, lse = the merged partial results [splits][total] (seq_combine.cu).
 cudaError_t launch_seq_combine(const float* part_o, const float* part_lse, int splits, long long total, int dv,
                                void* o, float* lse, fa_dtype dt, cudaStream_t s);
@@ -86,6 +90,8 @@ struct LatentBwd {
 };
 size_t latent_bwd_workspace_layout(int B, int H, int Nq, int Nk, int dr, size_t* off_dsum, size_t* off_part);
 cudaError_t launch_latent_bwd_prep(const LatentBwd& p, fa_dtype dt, cudaStream_t s);
+// bf16 on the tensor cores (latent_bwd_sm103.cu)
+cudaError_t launch_latent_bwd_sm103(const LatentBwd& p, cudaStream_t s);
 cudaError_t launch_latent_bwd_simt(const LatentBwd& p, fa_dtype dt, cudaStream_t s);
 // dkr = the sum over heads of dkr_part
 cudaError_t launch_latent_bwd_dkr(const LatentBwd& p, fa_dtype dt, cudaStream_t s);

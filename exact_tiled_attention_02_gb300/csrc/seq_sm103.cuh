@@ -1,0 +1,107 @@
+// seq_sm103.cuh -- what the language-model kernels share on top of
+// sm103.cuh: split shared-memory descriptors, 4-D TMA loads, host-side tensor
+// maps and per-device launch state.
+#pragma once
+
+#include <atomic>
+
+#include "seq_kernels.h"
+#include "sm103.cuh"
+
+namespace fa {
+namespace seq {
+
+using namespace sm103;
+
+// Shared-memory descriptor in its two 32-bit words: the start address (bits
+// 0-13, 16-byte units) lives in the low word, so stepping through a tile is
+// one 32-bit add (every address is below 256 KB, so the field never carries).
+struct Desc2 {
+  uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc2 desc_sw128(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes) {
+  const uint64_t d = sdesc_sw128(saddr, lbo_bytes, sbo_bytes);
+  return Desc2{static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
+}
+__device__ __forceinline__ void mma_ss2(uint32_t d_tmem, Desc2 a, uint32_t a_off, Desc2 b, uint32_t b_off,
+                                        uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 da, db;\n"
+      "mov.b64 da, {%1, %2};\nmov.b64 db, {%3, %4};\n"
+      "setp.ne.b32 p, %6, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d_tmem),
+      "r"(a.lo + a_off), "r"(a.hi), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts2(uint32_t d_tmem, uint32_t a_tmem, Desc2 b, uint32_t b_off, uint32_t idesc,
+                                        uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 db;\n"
+      "mov.b64 db, {%2, %3};\n"
+      "setp.ne.b32 p, %5, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+// A bf16 map of up to four dimensions, innermost first (dims[0] contiguous),
+// rows packed; box of 64 columns, 128-byte swizzle, zeros outside.
+inline bool make_map(CUtensorMap* m, const void* base, int rank, const long long* dims, const int* box) {
+  const EncodeTiledFnPtr fn = encode_tiled_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t d[4], st[3];
+  cuuint32_t b[4];
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  unsigned long long bytes = 2;
+  for (int i = 0; i < rank; ++i) {
+    d[i] = static_cast<cuuint64_t>(dims[i]);
+    b[i] = static_cast<cuuint32_t>(box[i]);
+    bytes *= static_cast<unsigned long long>(dims[i]);
+    if (i + 1 < rank) st[i] = bytes;
+  }
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), d, st, b, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool make_map3(CUtensorMap* m, const void* base, long long d0, long long d1, long long d2, int box1) {
+  const long long dims[3] = {d0, d1, d2};
+  const int box[3] = {64, box1, 1};
+  return make_map(m, base, 3, dims, box);
+}
+
+// Raises a kernel's dynamic shared memory limit once per device.
+struct SmemOnce {
+  std::atomic<unsigned long long> done{0};
+  template <typename F>
+  cudaError_t operator()(F kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev, std::memory_order_release);
+    return e;
+  }
+};
+
+inline int sm_count() {
+  static std::atomic<int> cached[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = cached[dev].load()) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < 64) cached[dev].store(n);
+  return n;
+}
+
+}  // namespace seq
+}  // namespace fa
