@@ -51,6 +51,25 @@ PartLayout prefix_layout(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) 
   const int ss = seq_simt_splits(static_cast<long long>(B) * Hkv, G * Nq, Ns);
   return part_layout(sp, ss, static_cast<long long>(B) * Hq * Nq, d);
 }
+// bf16: the prefix's splits [splits][rows], then the pieces of the sequences
+struct PrefixLayout {
+  int splits;
+  DecodePlan plan;
+  size_t off_pre_lse, off_o, off_lse, bytes;
+};
+PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
+  PrefixLayout w{};
+  const int G = Hq / Hkv;
+  const size_t rows = static_cast<size_t>(B) * Hq * Nq;
+  w.splits = Np > 0 ? seq_rows_splits(Hkv, B * G * Nq, G * Nq, Np) : 0;
+  w.plan = decode_plan(B, Hkv, G * Nq, false, 64);
+  const size_t slots = Ns > 0 ? decode_slots(w.plan) : 0;
+  w.off_pre_lse = up256(w.splits * rows * d * 4);
+  w.off_o = w.off_pre_lse + up256(w.splits * rows * 4);
+  w.off_lse = w.off_o + up256(slots * d * 4);
+  w.bytes = w.off_lse + up256(slots * 4);
+  return w;
+}
 bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   if (Np < 0 || Ns < 0 || Hkv < 1 || Hq % Hkv != 0) return false;
   return sizes_ok(B, Hq, Nq, d) && sizes_ok(B, Hkv, Ns > 0 ? Ns : 1, d) && sizes_ok(Hkv, Np > 0 ? Np : 1, d) &&
@@ -60,6 +79,14 @@ bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
 PartLayout absorbed_layout(int B, int H, int Nq, int n_keys, int dc) {
   const int sp = seq_simt_splits(B, H * Nq, n_keys);
   return part_layout(sp, 0, static_cast<long long>(B) * H * Nq, dc);
+}
+// bf16: the pieces of sequences that several CTAs share
+PartLayout absorbed_layout_bf16(const DecodePlan& plan, int dc) {
+  return part_layout(1, 0, static_cast<long long>(decode_slots(plan)), dc);
+}
+DecodePlan absorbed_plan(int B, int H, int Nq, int page_size, bool table) {
+  const int box = !table || page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+  return decode_plan(B, 1, H * Nq, true, box);
 }
 // tokens a sequence can hold, or -1
 long long absorbed_keys(int page_size, int max_pages) {
@@ -91,7 +118,9 @@ extern "C" {
 
 size_t fa_fwd_shared_prefix_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   if (!prefix_sizes_ok(B, Hq, Hkv, Nq, Np, Ns, d)) return 0;
-  return prefix_layout(B, Hq, Hkv, Nq, Np, Ns, d).bytes;
+  const size_t f32 = prefix_layout(B, Hq, Hkv, Nq, Np, Ns, d).bytes;
+  const size_t bf16 = prefix_layout_bf16(B, Hq, Hkv, Nq, Np, Ns, d).bytes;
+  return f32 > bf16 ? f32 : bf16;
 }
 
 fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k, const void* v,
@@ -108,8 +137,7 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
   if (!scale_ok(scale) || !dtype_ok(dt)) return FA_ERR_INVALID;
   if (dt == FA_DTYPE_BF16 && d != 64 && d != 96 && d != 128) return FA_ERR_UNSUPPORTED;
   if (dt == FA_DTYPE_F32 && d > 128) return FA_ERR_UNSUPPORTED;
-  const PartLayout w = prefix_layout(B, Hq, Hkv, Nq, Np, Ns, d);
-  if (workspace_bytes < w.bytes) return FA_ERR_INVALID;
+  if (workspace_bytes < fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d)) return FA_ERR_INVALID;
 
   const int G = Hq / Hkv;
   SeqAttn p{};
@@ -123,8 +151,6 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
   p.k2_div = 1;
   p.lens_div = 1;
   p.scale = scale;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.off_lse);
   p.total = static_cast<long long>(B) * Hq * Nq;
   p.wait_ns = device_wait_ns();
   if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
@@ -141,11 +167,6 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
   a.k1 = k_prefix;
   a.v = v_prefix;
   a.n_keys = Np;
-  a.splits = w.splits_a;
-  a.part0 = 0;
-  cudaError_t e = launch_seq_simt(a, dt, s);
-  if (e != cudaSuccess) return FA_ERR_CUDA;
-
   // the sequences' own keys: one group per sequence and key/value head
   SeqAttn b = p;
   b.groups = B * Hkv;
@@ -160,16 +181,39 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
   b.lens = lens;
   b.lens_div = Hkv;
   b.causal = 1;
+  char* base = static_cast<char*>(workspace);
+  if (dt == FA_DTYPE_BF16) {
+    const PrefixLayout w = prefix_layout_bf16(B, Hq, Hkv, Nq, Np, Ns, d);
+    a.part_o = reinterpret_cast<float*>(base);
+    a.part_lse = reinterpret_cast<float*>(base + w.off_pre_lse);
+    a.splits = w.splits;
+    b.part_o = reinterpret_cast<float*>(base + w.off_o);
+    b.part_lse = reinterpret_cast<float*>(base + w.off_lse);
+    cudaError_t e = cudaSuccess;
+    if (Np > 0) e = launch_seq_rows(a, s);
+    if (e == cudaSuccess && Ns > 0) e = launch_seq_decode(b, w.plan, s);
+    if (e == cudaSuccess) e = launch_seq_decode_merge(b, w.plan, a.part_o, a.part_lse, w.splits, s);
+    return of(e);
+  }
+  const PartLayout w = prefix_layout(B, Hq, Hkv, Nq, Np, Ns, d);
+  a.part_o = b.part_o = reinterpret_cast<float*>(base);
+  a.part_lse = b.part_lse = reinterpret_cast<float*>(base + w.off_lse);
+  a.splits = w.splits_a;
+  a.part0 = 0;
   b.splits = w.splits_b;
   b.part0 = w.splits_a;
-  e = launch_seq_simt(b, dt, s);
-  if (e != cudaSuccess) return FA_ERR_CUDA;
-  return of(launch_seq_combine(p.part_o, p.part_lse, w.splits_a + w.splits_b, p.total, d, o, lse, dt, s));
+  cudaError_t e = launch_seq_simt(a, dt, s);
+  if (e == cudaSuccess) e = launch_seq_simt(b, dt, s);
+  if (e == cudaSuccess)
+    e = launch_seq_combine(a.part_o, a.part_lse, w.splits_a + w.splits_b, p.total, d, o, lse, dt, s);
+  return of(e);
 }
 
 size_t fa_fwd_latent_absorbed_workspace_bytes(int B, int H, int Nq, int page_size, int max_pages, int dc) {
   if (!sizes_ok(B, H, Nq, dc) || page_size < 1 || max_pages < 1 || absorbed_keys(page_size, max_pages) < 0) return 0;
-  return absorbed_layout(B, H, Nq, static_cast<int>(absorbed_keys(page_size, max_pages)), dc).bytes;
+  const size_t f32 = absorbed_layout(B, H, Nq, static_cast<int>(absorbed_keys(page_size, max_pages)), dc).bytes;
+  const size_t bf16 = absorbed_layout_bf16(absorbed_plan(B, H, Nq, page_size, true), dc).bytes;
+  return f32 > bf16 ? f32 : bf16;
 }
 
 fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* block_table, const int* lens, void* o,
@@ -189,8 +233,8 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
   if (dt == FA_DTYPE_BF16 && block_table && page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
   if (dt == FA_DTYPE_F32 && (dc > 512 || dr > 128)) return FA_ERR_UNSUPPORTED;
   const int n_keys = static_cast<int>(absorbed_keys(page_size, max_pages));
-  const PartLayout w = absorbed_layout(B, H, Nq, n_keys, dc);
-  if (workspace_bytes < w.bytes) return FA_ERR_INVALID;
+  if (workspace_bytes < fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc))
+    return FA_ERR_INVALID;
 
   SeqAttn p{};
   p.q = q;
@@ -217,15 +261,22 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
   p.n_pages = n_pages;
   p.causal = 1;
   p.scale = scale;
-  p.splits = w.splits_a;
   p.total = static_cast<long long>(B) * H * Nq;
-  if (w.splits_a > 1) {
-    p.part_o = static_cast<float*>(workspace);
-    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.off_lse);
-  }
   p.wait_ns = device_wait_ns();
   if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  p.part_o = static_cast<float*>(workspace);
+  if (dt == FA_DTYPE_BF16) {
+    const DecodePlan plan = absorbed_plan(B, H, Nq, page_size, block_table != nullptr);
+    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + absorbed_layout_bf16(plan, dc).off_lse);
+    cudaError_t e = launch_seq_decode(p, plan, s);
+    if (e == cudaSuccess) e = launch_seq_decode_merge(p, plan, nullptr, nullptr, 0, s);
+    return of(e);
+  }
+  const PartLayout w = absorbed_layout(B, H, Nq, n_keys, dc);
+  p.splits = w.splits_a;
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.off_lse);
+  if (w.splits_a == 1) p.part_o = p.part_lse = nullptr;
   const cudaError_t e = launch_seq_simt(p, dt, s);
   if (e != cudaSuccess || w.splits_a == 1) return of(e);
   return of(launch_seq_combine(p.part_o, p.part_lse, w.splits_a, p.total, dc, o, lse, dt, s));

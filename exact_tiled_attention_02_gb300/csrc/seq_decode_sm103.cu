@@ -1,0 +1,809 @@
+// seq_decode_sm103.cu -- attention of few query rows over long caches, bf16 in
+// / fp32 accumulate, on the tensor cores of GB300 (sm_103a): the absorbed
+// latent form over a paged cache (one 576- or 320-wide vector a token, whose
+// first 512 or 256 entries are also the value), and the sequences' own part
+// of shared-prefix attention (separate keys and values).
+//
+//   S_ij = scale q_i . k_j over the keys j < nk - lag(i),  O_i = sum_j softmax_j v_j
+//
+// Every token's vector is read once for up to NR = 64 query rows, so the
+// bound is the cache's bytes until the rows fill the tensor core.  The
+// products are taken transposed, keys and value dimensions as the long (M)
+// side and query rows as the short (N) side, which may be as small as 16:
+//   S^T [64 keys x NR]          = K Q^T    (A = the tile as loaded, K-major)
+//   O^T [128 dims x NR] per 128 value dimensions += V^T P^T
+//                                           (A = the same tile, MN-major)
+// so one copy of a tile in shared memory serves both products, and O takes
+// NR columns of tensor memory per 128 dimensions (4 x 64 at 512).
+//
+// A sequence's softmax statistics run down the columns here, across lanes.
+// Per tile a thread (one key) only checks whether any of its scores exceeds
+// its column's reference by 2^8; if none of the 64 keys' does (one barrier
+// with an OR) the tile is exponentiated as it is.  Otherwise the column
+// maxima are reduced across lanes and warps and O is rescaled.  Row sums stay
+// per thread until a piece ends.
+//
+// Work: the tiles of all sequences, laid end to end, are cut into equal
+// ranges, one a CTA (per group of rows: heads beyond 64, key/value heads), so
+// ragged batches and single long sequences both fill the GPU, and the cut
+// depends on the lengths alone.  A CTA's share of one sequence is a piece; a
+// sequence that is one whole piece is written out directly where the caller
+// asked for that, others as fp32 partial results that a second kernel merges
+// in a fixed order.
+//
+// 192 threads: warps 0-3 softmax (a 64-row accumulator occupies lanes 0-15 of
+// each warp's quarter of tensor memory: lane l < 16 of warp w holds key 16 w +
+// l), warp 4 MMA issuer and TMEM owner, warp 5 TMA producer.
+// Shared memory: Q, P, a ring of M units (64 tokens x 128 dimensions; shared
+// form: key and value, otherwise values) and one of X units (shared form: the
+// rotary part; otherwise keys).
+#include <cmath>
+
+#include "seq_sm103.cuh"
+
+namespace fa {
+namespace {
+
+using namespace seq;
+
+constexpr int BC = 64;            // keys per tile
+constexpr int CB = BC * 128;      // bytes of a chunk: 64 tokens x 64 entries
+constexpr int kThreads = 192;
+constexpr float kUnset = 3e38f;   // negated reference of a row that has seen no key
+constexpr float kRescaleThreshold = 8.0f;
+
+// DM: entries of an M part; DX: of an X part; SHARED: keys are [M | X] and values M.
+template <int DM, int DX, bool SHARED, int NR>
+struct Cfg {
+  static constexpr int UC = DM >= 128 ? 2 : (DM + 63) / 64;    // chunks of an M unit
+  static constexpr int UM = SHARED ? DM / 128 : 1;             // M units of a tile
+  static constexpr int XC = (DX + 63) / 64;                    // chunks of an X unit
+  static constexpr int QC = SHARED ? UM * UC + XC : XC;        // chunks of a query row
+  static constexpr int UDIM = UC * 64;                         // value dimensions of an M unit: the M of its product
+  static constexpr int Q_BYTES = QC * NR * 128;
+  static constexpr int P_BYTES = NR * 128;
+  static constexpr int M_BYTES = UC * CB, X_BYTES = XC * CB;
+  static constexpr int CTAS = SHARED || NR == 64 ? 1 : 2;  // a SM
+  static constexpr int BUDGET = CTAS == 1 ? 227 * 1024 : 113 * 1024;
+  static constexpr int BARS = DM == 512 && NR == 64 ? 27 : 40;
+  static constexpr int MISC = 3 * NR * 4 + 4 * NR * 4 + 8 * BARS + 24;  // stats, warp scratch, barriers, start
+  static constexpr int FREE = BUDGET - 1024 - Q_BYTES - P_BYTES - MISC;
+  static constexpr int TILE = UM * M_BYTES + X_BYTES;
+  // rings: as many whole tiles as fit (at most four), then M units into what is left
+  static constexpr int NT = FREE / TILE < 4 ? FREE / TILE : 4;
+  static constexpr int NX = NT + (SHARED && FREE - NT * TILE >= X_BYTES + M_BYTES && NT < 4 ? 1 : 0);
+  static constexpr int LEFT = FREE - NT * UM * M_BYTES - NX * X_BYTES;
+  static constexpr int EXTRA = SHARED && NT < 4 ? LEFT / M_BYTES : 0;
+  static constexpr int NM = NT * UM + EXTRA;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_P = OFF_Q + Q_BYTES;
+  static constexpr int OFF_M = OFF_P + P_BYTES;
+  static constexpr int OFF_X = OFF_M + NM * M_BYTES;
+  static constexpr int OFF_STAT = OFF_X + NX * X_BYTES;  // nref, alpha (or 1/l), lag: [NR] each
+  static constexpr int OFF_RED = OFF_STAT + 3 * NR * 4;  // [4][NR]
+  static constexpr int OFF_BAR = OFF_RED + 4 * NR * 4;
+  static constexpr int NBAR = 2 * NM + 2 * NX + 7;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM_USED = OFF_MISC + 24;
+  static constexpr int SMEM_BYTES = SMEM_USED + 1024;
+  static constexpr int TM_S = UM * NR;
+  static constexpr int TM_NEED = UM * NR + 2 * NR;
+  static constexpr int TM_COLS = TM_NEED <= 32 ? 32 : TM_NEED <= 64 ? 64 : TM_NEED <= 128 ? 128 : TM_NEED <= 256 ? 256 : 512;
+  static_assert(NT >= 2, "two tiles in flight");
+  static_assert(SMEM_BYTES <= BUDGET, "shared memory budget");
+  static_assert(NBAR <= BARS, "barriers fit in MISC");
+  static_assert(!SHARED || DM % 128 == 0, "whole M units");
+};
+
+template <int NM, int NX>
+struct Bars {
+  uint32_t base;
+  __device__ uint32_t m_full(int s) const { return base + 8 * s; }
+  __device__ uint32_t m_free(int s) const { return base + 8 * (NM + s); }
+  __device__ uint32_t x_full(int s) const { return base + 8 * (2 * NM + s); }
+  __device__ uint32_t x_free(int s) const { return base + 8 * (2 * NM + NX + s); }
+  __device__ uint32_t q_full() const { return base + 8 * (2 * NM + 2 * NX); }
+  __device__ uint32_t q_free() const { return base + 8 * (2 * NM + 2 * NX + 1); }
+  __device__ uint32_t s_full(int b) const { return base + 8 * (2 * NM + 2 * NX + 2 + b); }
+  __device__ uint32_t p_full() const { return base + 8 * (2 * NM + 2 * NX + 4); }
+  __device__ uint32_t o_done() const { return base + 8 * (2 * NM + 2 * NX + 5); }
+  __device__ uint32_t drain() const { return base + 8 * (2 * NM + 2 * NX + 6); }
+};
+
+struct DecodeMaps {
+  CUtensorMap q, m, x;
+};
+
+__device__ __forceinline__ int seq_len(const SeqAttn& p, int b, bool report) {
+  const int n = p.lens[b];
+  const int nk = min(max(n, 0), p.n_keys);
+  if (report && n != nk) atomicOr(p.status, kStatusInput);
+  return nk;
+}
+__device__ __forceinline__ int tiles_of(int nk) { return (nk + BC - 1) / BC; }
+
+// Whole warp: the sum over sequences before `b` of their tiles, and over all.
+__device__ __forceinline__ void tile_sums(const SeqAttn& p, int n_seq, int b, long long& before, long long& total) {
+  const int lane = threadIdx.x & 31;
+  long long x = 0, y = 0;
+  for (int i = lane; i < n_seq; i += 32) {
+    const int t = tiles_of(seq_len(p, i, false));
+    y += t;
+    if (i < b) x += t;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  before = x;
+  total = y;
+}
+// ranges of `total` tiles that `cuts` CTAs take: none of them empty
+__device__ __forceinline__ int range_count(long long total, int cuts) {
+  return total < cuts ? static_cast<int>(total) : cuts;
+}
+// first tile of range c of n
+__device__ __forceinline__ long long range_start(long long total, int c, int n) { return total * c / n; }
+// the range that holds tile x
+__device__ __forceinline__ int owner(long long total, long long x, int n) {
+  return static_cast<int>(((x + 1) * n - 1) / total);
+}
+
+// Columns v[0..N) of 16 lanes reduced over the lanes: afterwards lane l holds
+// columns N / 16 (its bits, high first) ... in v[0 .. N/16).  Lanes 16-31 mirror.
+template <int H, int BIT, int N, typename Op>
+__device__ __forceinline__ void reduce_step(float (&v)[N], Op op) {
+  if constexpr (BIT >= 1) {
+    const bool up = (threadIdx.x & BIT) != 0;
+#pragma unroll
+    for (int i = 0; i < H; ++i) {
+      const float send = up ? v[i] : v[i + H];
+      const float keep = up ? v[i + H] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, BIT));
+    }
+    reduce_step<H / 2, BIT / 2>(v, op);
+  }
+}
+template <int N, typename Op>
+__device__ __forceinline__ void reduce16(float (&v)[N], Op op) {
+  reduce_step<N / 2, 8>(v, op);
+}
+
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n.reg .pred p, q;\n"
+      "setp.ne.u32 p, %1, 0;\n"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n"
+      "selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+template <int DM, int DX, bool SHARED, int NR>
+__global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
+    fa_seq_decode_sm103_kernel(const __grid_constant__ DecodeMaps maps, const __grid_constant__ SeqAttn p,
+                               const DecodePlan plan) {
+  using C = Cfg<DM, DX, SHARED, NR>;
+  constexpr int UM = C::UM, UC = C::UC, XC = C::XC, NM = C::NM, NX = C::NX, DV = DM;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  if (pad + C::SMEM_USED > static_cast<uint32_t>(C::SMEM_BYTES)) {
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusLayout);
+    return;
+  }
+  uint8_t* smem = smem_raw + pad;
+  const uint32_t sb = raw + pad;
+  const uint32_t sQ = sb + C::OFF_Q, sP = sb + C::OFF_P, sM = sb + C::OFF_M, sX = sb + C::OFF_X;
+  const Bars<NM, NX> bar{sb + C::OFF_BAR};
+  float* s_nref = reinterpret_cast<float*>(smem + C::OFF_STAT);
+  float* s_alpha = s_nref + NR;
+  int* s_lag = reinterpret_cast<int*>(s_alpha + NR);
+  float* s_red = reinterpret_cast<float*>(smem + C::OFF_RED);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  int* s_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // first sequence, its first tile, tiles of this CTA
+  const WaitCtl wc{p.status, abort_flag, p.wait_ns};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // this CTA: rows r0 .. of head `head` of every sequence (group b * heads + head), range `cut` of `cuts`
+  const int grp = blockIdx.x / plan.cuts, cut = blockIdx.x % plan.cuts;
+  const int head = grp / plan.row_groups, r0 = (grp % plan.row_groups) * NR;
+  const int n_rows = min(NR, p.rows - r0);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NM; ++s) {
+      mbar_init(bar.m_full(s), 1);
+      mbar_init(bar.m_free(s), 1);
+    }
+    for (int s = 0; s < NX; ++s) {
+      mbar_init(bar.x_full(s), 1);
+      mbar_init(bar.x_free(s), 1);
+    }
+    mbar_init(bar.q_full(), 1);
+    mbar_init(bar.q_free(), 1);
+    mbar_init(bar.s_full(0), 1);
+    mbar_init(bar.s_full(1), 1);
+    mbar_init(bar.p_full(), 4);
+    mbar_init(bar.o_done(), 1);
+    mbar_init(bar.drain(), 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 4) {
+    tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 5) {
+    // where this CTA's range of the tiles, laid end to end, begins
+    long long before, total;
+    tile_sums(p, plan.n_seq, 0, before, total);
+    const int ranges = range_count(total, plan.cuts);
+    const long long t0 = cut < ranges ? range_start(total, cut, ranges) : total;
+    const long long t1 = cut < ranges ? range_start(total, cut + 1, ranges) : total;
+    long long base = 0;
+    int b0 = 0, first = 0;
+    bool found = false;
+    for (int i0 = 0; i0 < plan.n_seq && !found; i0 += 32) {
+      const int i = i0 + lane;
+      const int t = i < plan.n_seq ? tiles_of(seq_len(p, i, true)) : 0;
+      int inc = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const long long end = base + inc;
+      const unsigned hit = __ballot_sync(0xffffffffu, end > t0);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        const long long beg = __shfl_sync(0xffffffffu, end - t, l);
+        b0 = i0 + l;
+        first = static_cast<int>(t0 - beg);
+        found = true;
+      }
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      s_start[0] = b0;
+      s_start[1] = first;
+      s_start[2] = found ? static_cast<int>(t1 - t0) : 0;
+    }
+  } else if (threadIdx.x < NR) {
+    s_lag[threadIdx.x] = p.n_new - 1 - (r0 + static_cast<int>(threadIdx.x)) % p.n_new;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int start_b = s_start[0], start_t = s_start[1], n_tiles = s_start[2];
+
+  // walks the pieces: f(sequence, its keys, first tile, tiles) until it returns false
+  auto pieces = [&](auto f) {
+    int b = start_b, t = start_t, left = n_tiles;
+    while (left > 0) {
+      const int nk = seq_len(p, b, false);
+      const int take = min(left, tiles_of(nk) - t);
+      if (take > 0) {
+        if (!f(b, nk, t, take)) return;
+        left -= take;
+      }
+      ++b;
+      t = 0;
+    }
+  };
+
+  if (warp == 5) {
+    // ------------------------------------------------------------------ TMA
+    // The whole warp walks; lane i < boxes issues the loads of box i of a tile
+    // (64 tokens, or fewer where pages are not whole tiles).
+    const int box = plan.box, per = BC / box;
+    int g = 0, nq = 0;  // tiles and pieces issued
+    bool ok = true;
+    auto wait = [&](uint32_t bar_addr, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait_backoff(bar_addr, parity, wc));
+      return ok;
+    };
+    pieces([&](int b, int nk, int t0, int n) -> bool {
+      const int group = b * plan.heads + head;
+      if (nq > 0 && !wait(bar.q_free(), (nq - 1) & 1)) return false;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar.q_full(), C::Q_BYTES);
+        for (int c = 0; c < C::QC; ++c) tma_load_3d(sQ + c * NR * 128, &maps.q, bar.q_full(), c * 64, r0, group);
+      }
+      ++nq;
+      // row coordinates of this lane's box: token within the page, page
+      auto place = [&](int tile, int& tok, int& page) {
+        const int j = tile * BC + lane * box;
+        tok = 0;
+        page = 0;
+        if (lane >= per || j >= nk) return;
+        tok = p.page_size > 0 ? j % p.page_size : j;
+        page = group;
+        if (p.table != nullptr) {
+          page = p.table[static_cast<long long>(b) * p.max_pages + j / p.page_size];
+          if (page < 0 || page >= p.n_pages) {
+            atomicOr(p.status, kStatusInput);
+            page = p.n_pages;  // outside: reads as zeros
+          }
+        }
+      };
+      int tok, page;
+      place(t0, tok, page);
+      for (int i = 0; i < n; ++i, ++g) {
+        const int valid = min(BC, nk - (t0 + i) * BC);
+        const int boxes = (valid + box - 1) / box;
+        int tok1 = 0, page1 = 0;
+        if (i + 1 < n) place(t0 + i + 1, tok1, page1);  // the next tile's pages, while this one loads
+        auto load_x = [&]() -> bool {
+          const int s = g % NX;
+          if (g >= NX && !wait(bar.x_free(s), (g / NX - 1) & 1)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(bar.x_full(s), boxes * box * 128 * XC);
+          __syncwarp();
+          if (lane < boxes)
+            for (int c = 0; c < XC; ++c)
+              tma_load_3d(sX + s * C::X_BYTES + c * CB + lane * box * 128, &maps.x, bar.x_full(s),
+                          (SHARED ? DM : 0) + c * 64, tok, page);
+          return true;
+        };
+        if (!SHARED && !load_x()) return false;
+        for (int u = 0; u < UM; ++u) {
+          const int k = g * UM + u, s = k % NM;
+          if (k >= NM && !wait(bar.m_free(s), (k / NM - 1) & 1)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(bar.m_full(s), boxes * box * 128 * UC);
+          __syncwarp();
+          if (lane < boxes)
+            for (int c = 0; c < UC; ++c)
+              tma_load_3d(sM + s * C::M_BYTES + c * CB + lane * box * 128, &maps.m, bar.m_full(s),
+                          (u * UC + c) * 64, tok, page);
+        }
+        if (SHARED && !load_x()) return false;
+        tok = tok1;
+        page = page1;
+      }
+      return true;
+    });
+    if (*abort_flag && lane == 0) {
+      // let copies already in flight land before the CTA's shared memory is
+      // released; a wait for copies that were never issued just runs out
+      WaitCtl drain{nullptr, nullptr, wc.limit_ns};
+      if (nq > 0) mbar_wait(bar.q_full(), (nq - 1) & 1, drain);
+      for (int k = max(0, (g + 1) * UM - NM); k < (g + 1) * UM; ++k) mbar_wait(bar.m_full(k % NM), (k / NM) & 1, drain);
+      for (int k = max(0, g + 1 - NX); k < g + 1; ++k) mbar_wait(bar.x_full(k % NX), (k / NX) & 1, drain);
+    }
+    __syncwarp();
+  } else if (warp == 4) {
+    // ------------------------------------------------------------------ MMA
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(BC, NR, 0, 0);
+      constexpr uint32_t idesc_o = idesc_bf16_f32(C::UDIM, NR, 1, 0);
+      const Desc2 dq = desc_sw128(sQ, 16, 1024), dp = desc_sw128(sP, 16, 1024);
+      bool ok = true;
+      int g = 0, nq = 0;
+      auto issue_s = [&](int k) -> bool {  // S^T of the k-th tile, into buffer k % 2
+        const uint32_t dt = tmem + C::TM_S + NR * (k & 1);
+        uint32_t acc = 0;
+        if (SHARED) {
+          for (int u = 0; u < UM; ++u) {
+            const int m = k * UM + u;
+            if (!mbar_wait(bar.m_full(m % NM), (m / NM) & 1, wc)) return false;
+            tc_fence_after();
+            const Desc2 da = desc_sw128(sM + (m % NM) * C::M_BYTES, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < UC * 4; ++kk) {
+              mma_ss2(dt, da, ((kk >> 2) * CB + (kk & 3) * 32) >> 4, dq,
+                      ((u * UC + (kk >> 2)) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, acc);
+              acc = 1;
+            }
+          }
+        }
+        if (!mbar_wait(bar.x_full(k % NX), (k / NX) & 1, wc)) return false;
+        tc_fence_after();
+        const Desc2 da = desc_sw128(sX + (k % NX) * C::X_BYTES, 16, 1024);
+        constexpr int QX = SHARED ? UM * UC : 0;
+#pragma unroll
+        for (int kk = 0; kk < DX / 16; ++kk) {
+          mma_ss2(dt, da, ((kk >> 2) * CB + (kk & 3) * 32) >> 4, dq, ((QX + (kk >> 2)) * NR * 128 + (kk & 3) * 32) >> 4,
+                  idesc_s, acc);
+          acc = 1;
+        }
+        mma_commit(bar.x_free(k % NX));
+        mma_commit(bar.s_full(k & 1));
+        return true;
+      };
+      pieces([&](int, int, int, int n) -> bool {
+        ok = mbar_wait(bar.q_full(), nq & 1, wc);
+        if (!ok) return false;
+        tc_fence_after();
+        if (!(ok = issue_s(g))) return false;
+        if (n == 1) mma_commit(bar.q_free());
+        for (int i = 0; i < n; ++i, ++g) {
+          if (i + 1 < n) {
+            if (!(ok = issue_s(g + 1))) return false;
+            if (i + 2 == n) mma_commit(bar.q_free());  // no later product of this piece reads Q
+          }
+          if (!(ok = mbar_wait(bar.p_full(), g & 1, wc))) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int u = 0; u < UM; ++u) {
+            const int m = g * UM + u;
+            if (!SHARED) {
+              if (!(ok = mbar_wait(bar.m_full(m % NM), (m / NM) & 1, wc))) return false;
+              tc_fence_after();
+            }
+            const Desc2 da = desc_sw128(sM + (m % NM) * C::M_BYTES, CB, 1024);
+#pragma unroll
+            for (int kk = 0; kk < BC / 16; ++kk)
+              mma_ss2(tmem + u * NR, da, (kk * 16 * 128) >> 4, dp, (kk * 32) >> 4, idesc_o, i > 0 || kk > 0);
+            mma_commit(bar.m_free(m % NM));
+          }
+          mma_commit(bar.o_done());
+        }
+        ++nq;
+        return true;
+      });
+      // every MMA this thread issued must finish before tensor memory is freed
+      mma_commit(bar.drain());
+      WaitCtl drain{nullptr, nullptr, wc.limit_ns};
+      mbar_wait(bar.drain(), 0, drain);
+    }
+    __syncwarp();
+  } else {
+    // -------------------------------------------------------------- softmax
+    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int key = warp * 16 + lane;  // this thread's key of a tile (lane < 16)
+    const bool live = lane < 16;
+    const float sl = p.scale * 1.4426950408889634f;
+    constexpr int LW = NR < 32 ? 16 : 32;  // columns per tensor-memory access
+    // own entry of row c of P: K-major, 128-byte swizzle
+    const uint32_t p_at = sP + (key & 7) * 2;
+    int g = 0;
+    bool ok = true;
+    auto warp_wait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
+    };
+    // all four warps give up together: a barrier's count must be met on every path
+    auto wait_all = [&](uint32_t bar_addr, uint32_t parity) -> bool {
+      ok = !bar_any(1, 128, !warp_wait(bar_addr, parity));
+      return ok;
+    };
+    // columns this lane owns after reduce16
+    int col0 = 0;
+#pragma unroll
+    for (int h = NR / 2, bit = 8; bit >= 1; h /= 2, bit /= 2)
+      if (lane & bit) col0 += h;
+
+    pieces([&](int b, int nk, int t0, int n) -> bool {
+      const int group = b * plan.heads + head;
+      float l[NR], lr[NR];  // this key's share of the row sums: of P, and of P rounded to bf16 (what multiplies V)
+#pragma unroll
+      for (int c = 0; c < NR; ++c) l[c] = lr[c] = 0.f;
+      if (threadIdx.x < NR) s_nref[threadIdx.x] = kUnset;
+      named_bar_sync(1, 128);
+      for (int i = 0; i < n; ++i, ++g) {
+        if (!wait_all(bar.s_full(g & 1), (g >> 1) & 1)) return false;
+        tc_fence_after();
+        float s[NR];
+        {
+          uint32_t r[NR];
+#pragma unroll
+          for (int c = 0; c < NR; c += LW)
+            if constexpr (LW == 16)
+              tmem_ld_32x32b_x16(tl + C::TM_S + NR * (g & 1) + c, r + c);
+            else
+              tmem_ld_32x32b_x32(tl + C::TM_S + NR * (g & 1) + c, r + c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < NR; ++c) s[c] = __uint_as_float(r[c]);
+        }
+        const int j0 = (t0 + i) * BC;
+        if (j0 + BC > nk - (p.n_new - 1)) {
+          const int room = nk - (j0 + key);  // > lag: the row sees this key
+#pragma unroll
+          for (int c = 0; c < NR; ++c) s[c] = s_lag[c] < room ? s[c] : -INFINITY;
+        }
+        if (!live) {
+#pragma unroll
+          for (int c = 0; c < NR; ++c) s[c] = -INFINITY;
+        }
+        // values past the sequence's end multiply zero probabilities: they must be finite
+        const int valid = min(BC, nk - j0);
+        if (valid < BC) {
+          if (!SHARED && !wait_all(bar.m_full(g % NM), (g / NM) & 1)) return false;
+          const int rows = BC - valid;
+          for (int x = threadIdx.x; x < rows * UM * UC * 8; x += 128) {
+            const int row = valid + x / (UM * UC * 8), y = x % (UM * UC * 8);
+            const int u = y / (UC * 8), z = y % (UC * 8);
+            st_shared_v4(sM + ((g * UM + u) % NM) * C::M_BYTES + (z >> 3) * CB + row * 128 + (z & 7) * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+        }
+        float over = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < NR; c += 4) {
+          const float4 nr = *reinterpret_cast<const float4*>(s_nref + c);
+          over = fmax3(over, fmaf(s[c], sl, nr.x), fmaf(s[c + 1], sl, nr.y));
+          over = fmax3(over, fmaf(s[c + 2], sl, nr.z), fmaf(s[c + 3], sl, nr.w));
+        }
+        if (bar_any(1, 128, over > kRescaleThreshold)) {
+          // some row's reference rises: column maxima over the 64 keys
+          {
+            float v[NR];
+#pragma unroll
+            for (int c = 0; c < NR; ++c) v[c] = s[c] * sl;
+            reduce16<NR>(v, [](float a, float c) { return fmaxf(a, c); });
+            if (live) {
+#pragma unroll
+              for (int e = 0; e < NR / 16; ++e) s_red[warp * NR + col0 + e] = v[e];
+            }
+          }
+          named_bar_sync(1, 128);
+          if (threadIdx.x < NR) {
+            const int c = threadIdx.x;
+            const float mx = fmaxf(fmaxf(s_red[c], s_red[NR + c]), fmaxf(s_red[2 * NR + c], s_red[3 * NR + c]));
+            const float old = s_nref[c];
+            float alpha = 1.f;
+            if (mx + old > kRescaleThreshold) {  // old = kUnset: the first key that the row sees
+              alpha = old == kUnset ? 0.f : ex2_approx(-old - mx);
+              s_nref[c] = -mx;
+            }
+            s_alpha[c] = alpha;
+          }
+          named_bar_sync(1, 128);
+#pragma unroll
+          for (int c = 0; c < NR; ++c) {
+            const float a = s_alpha[c];
+            l[c] *= a;
+            lr[c] *= a;
+          }
+          if (i > 0) {
+            if (!wait_all(bar.o_done(), (g - 1) & 1)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < UM * NR; c += LW) {
+              uint32_t o[LW];
+              if constexpr (LW == 16)
+                tmem_ld_32x32b_x16(tl + c, o);
+              else
+                tmem_ld_32x32b_x32(tl + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < LW; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_alpha[c % NR + e]);
+              if constexpr (LW == 16)
+                tmem_st_32x32b_x16(tl + c, o);
+              else
+                tmem_st_32x32b_x32(tl + c, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        // P_{g-1} has been read once its P V has completed
+        if (g > 0 && !wait_all(bar.o_done(), (g - 1) & 1)) return false;
+#pragma unroll
+        for (int c = 0; c < NR; c += 4) {
+          const float4 nr = *reinterpret_cast<const float4*>(s_nref + c);
+          const float nv[4] = {nr.x, nr.y, nr.z, nr.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float pv = ex2_approx(fmaf(s[c + e], sl, nv[e]));
+            const __nv_bfloat16 ph = __float2bfloat16_rn(pv);
+            l[c + e] += pv;
+            lr[c + e] += __bfloat162float(ph);
+            if (live)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(p_at + (c + e) * 128 + ((((key >> 3) ^ (c + e)) & 7) << 4)),
+                           "h"(__bfloat16_as_ushort(ph))
+                           : "memory");
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar.p_full());
+      }
+      // ------------------------------------------------------------ output
+      float ref = 0.f, sum = 0.f, sum_r = 0.f;  // of row threadIdx.x
+      reduce16<NR>(l, [](float a, float c) { return a + c; });
+      reduce16<NR>(lr, [](float a, float c) { return a + c; });
+      if (live) {
+#pragma unroll
+        for (int e = 0; e < NR / 16; ++e) s_red[warp * NR + col0 + e] = l[e];
+      }
+      named_bar_sync(1, 128);
+      if (threadIdx.x < NR) {
+        const int c = threadIdx.x;
+        sum = (s_red[c] + s_red[NR + c]) + (s_red[2 * NR + c] + s_red[3 * NR + c]);
+        ref = s_nref[c] == kUnset ? 0.f : -s_nref[c];
+      }
+      named_bar_sync(1, 128);
+      if (live) {
+#pragma unroll
+        for (int e = 0; e < NR / 16; ++e) s_red[warp * NR + col0 + e] = lr[e];
+      }
+      named_bar_sync(1, 128);
+      const bool whole = p.part_o == nullptr || (plan.direct && t0 == 0 && n == tiles_of(nk));
+      const long long slot = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + cut + b;
+      const long long orow0 = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r0;
+      if (threadIdx.x < NR) {
+        const int c = threadIdx.x;
+        sum_r = (s_red[c] + s_red[NR + c]) + (s_red[2 * NR + c] + s_red[3 * NR + c]);
+        s_alpha[c] = sum_r == 0.f ? 0.f : 1.f / sum_r;
+        const float lse = (ref + __log2f(sum)) * 0.69314718055994531f;  // -inf where no key was seen
+        if (c < n_rows) {
+          if (!whole)
+            p.part_lse[slot * NR + c] = lse;
+          else if (p.lse != nullptr)
+            p.lse[orow0 + c] = lse;
+        }
+      }
+      if (!wait_all(bar.o_done(), (g - 1) & 1)) return false;  // also orders s_alpha
+      tc_fence_after();
+      const int d0 = C::UDIM == 128 ? warp * 32 + lane : warp * 16 + lane;  // this lane's dimension of an M unit
+      const bool has_dim = (C::UDIM == 128 || live) && d0 < DV;
+#pragma unroll 1
+      for (int c = 0; c < UM * NR; c += LW) {
+        uint32_t o[LW];
+        if constexpr (LW == 16)
+          tmem_ld_32x32b_x16(tl + c, o);
+        else
+          tmem_ld_32x32b_x32(tl + c, o);
+        tmem_wait_ld();
+        const int d = (c / NR) * 128 + d0, row = c % NR;
+        if (!has_dim || *abort_flag) continue;
+#pragma unroll
+        for (int e = 0; e < LW; ++e) {
+          if (row + e >= n_rows) break;
+          const float a = s_alpha[row + e];
+          const float v = a == 0.f ? 0.f : __uint_as_float(o[e]) * a;
+          if (whole)
+            static_cast<__nv_bfloat16*>(p.o)[(orow0 + row + e) * DV + d] = __float2bfloat16_rn(v);
+          else
+            p.part_o[(slot * NR + row + e) * DV + d] = v;
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(1, 128);  // the statistics are free for the next piece
+      return true;
+    });
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+// Merges the pieces of each sequence, and the partial results [pre][total] of
+// another set of keys beside them (the prefix), row by row: see
+// seq_combine.cu for the formula.  One warp per row.  Rows of a sequence that
+// was written directly are left alone.
+template <int NR>
+__global__ void __launch_bounds__(128)
+    fa_seq_decode_merge_kernel(const __grid_constant__ SeqAttn p, const DecodePlan plan, const float* __restrict__ pre_o,
+                               const float* __restrict__ pre_lse, int pre) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long idx = static_cast<long long>(blockIdx.x) * 4 + warp;  // (sequence, head, row)
+  if (idx >= static_cast<long long>(plan.n_seq) * plan.heads * p.rows) return;
+  const int r = static_cast<int>(idx % p.rows);
+  const int group = static_cast<int>(idx / p.rows);
+  const int b = group / plan.heads, head = group % plan.heads;
+  long long before, total;
+  tile_sums(p, plan.n_seq, b, before, total);
+  const int nt = tiles_of(seq_len(p, b, true));
+  int c0 = 0, n = 0;
+  if (nt > 0) {
+    const int ranges = range_count(total, plan.cuts);
+    c0 = owner(total, before, ranges);
+    n = owner(total, before + nt - 1, ranges) - c0 + 1;
+  }
+  if (plan.direct && n == 1) return;
+  const int grp = head * plan.row_groups + r / NR;
+  const long long slot0 = (static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + c0 + b) * NR + r % NR;
+  const long long row = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r;
+  auto part = [&](int i) -> long long { return i < pre ? i * p.total + row : slot0 + static_cast<long long>(i - pre) * NR; };
+  auto part_lse = [&](int i) { return i < pre ? pre_lse[part(i)] : p.part_lse[part(i)]; };
+  n += pre;
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, part_lse(i));
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const float ref = m == -INFINITY ? 0.f : m;
+  float sum = 0.f;
+  for (int i = lane; i < n; i += 32) sum += expf(part_lse(i) - ref);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + row * p.dv;
+  for (int c = 4 * lane; c < p.dv; c += 128) {
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; ++i) {
+      const float ls = part_lse(i);
+      if (ls == -INFINITY) continue;
+      const float w = expf(ls - ref) * inv;
+      const float4 v = *reinterpret_cast<const float4*>((i < pre ? pre_o : p.part_o) + part(i) * p.dv + c);
+      acc.x = fmaf(w, v.x, acc.x);
+      acc.y = fmaf(w, v.y, acc.y);
+      acc.z = fmaf(w, v.z, acc.z);
+      acc.w = fmaf(w, v.w, acc.w);
+    }
+    *reinterpret_cast<uint2*>(o + c) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  }
+  if (lane == 0 && p.lse != nullptr) p.lse[row] = m + logf(sum);
+}
+
+template <int DM, int DX, bool SHARED, int NR>
+cudaError_t launch_nr(const SeqAttn& p, const DecodePlan& plan, cudaStream_t s) {
+  using C = Cfg<DM, DX, SHARED, NR>;
+  static SmemOnce once;
+  cudaError_t e = once(fa_seq_decode_sm103_kernel<DM, DX, SHARED, NR>, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  DecodeMaps m;
+  const int width = p.d1;
+  const long long pages = p.page_size > 0 ? p.n_pages : p.groups;
+  const int page = p.page_size > 0 ? p.page_size : p.n_keys;
+  if (!make_map3(&m.q, p.q, width, p.rows, p.groups, NR) || !make_map3(&m.x, p.k1, width, page, pages, plan.box))
+    return cudaErrorInvalidValue;
+  m.m = m.x;
+  if (!SHARED && !make_map3(&m.m, p.v, DM, page, pages, plan.box)) return cudaErrorInvalidValue;
+  fa_seq_decode_sm103_kernel<DM, DX, SHARED, NR>
+      <<<plan.heads * plan.row_groups * plan.cuts, kThreads, C::SMEM_BYTES, s>>>(m, p, plan);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box) {
+  DecodePlan w{};
+  w.n_seq = n_seq;
+  w.heads = heads;
+  w.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  w.row_groups = (rows + w.nr - 1) / w.nr;
+  const int ctas = shared || w.nr == 64 ? 152 : 304;  // one CTA an SM, or two
+  const long long groups = static_cast<long long>(heads) * w.row_groups;
+  w.cuts = groups < ctas ? static_cast<int>(ctas / groups) : 1;
+  w.direct = shared;
+  w.box = box;
+  return w;
+}
+size_t decode_slots(const DecodePlan& w) {
+  return static_cast<size_t>(w.heads) * w.row_groups * (static_cast<size_t>(w.cuts) + w.n_seq) * w.nr;
+}
+
+cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, cudaStream_t s) {
+  if (static_cast<long long>(w.heads) * w.row_groups * w.cuts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+#define FA_DECODE(DM, DX, SH)                                                        \
+  (w.nr == 16 ? launch_nr<DM, DX, SH, 16>(p, w, s)                                   \
+              : w.nr == 32 ? launch_nr<DM, DX, SH, 32>(p, w, s) : launch_nr<DM, DX, SH, 64>(p, w, s))
+  if (w.direct) {
+    if (p.dv == 512) return FA_DECODE(512, 64, true);
+    if (p.dv == 256) return FA_DECODE(256, 64, true);
+  } else {
+    if (p.dv == 64) return FA_DECODE(64, 64, false);
+    if (p.dv == 96) return FA_DECODE(96, 96, false);
+    if (p.dv == 128) return FA_DECODE(128, 128, false);
+  }
+#undef FA_DECODE
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
+                                    int pre, cudaStream_t s) {
+  const long long warps = static_cast<long long>(w.n_seq) * w.heads * p.rows;
+  if ((warps + 3) / 4 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
+  if (w.nr == 16)
+    fa_seq_decode_merge_kernel<16><<<blocks, 128, 0, s>>>(p, w, pre_o, pre_lse, pre);
+  else if (w.nr == 32)
+    fa_seq_decode_merge_kernel<32><<<blocks, 128, 0, s>>>(p, w, pre_o, pre_lse, pre);
+  else
+    fa_seq_decode_merge_kernel<64><<<blocks, 128, 0, s>>>(p, w, pre_o, pre_lse, pre);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -57,8 +57,30 @@ cudaError_t launch_seq_simt(const SeqAttn& p, fa_dtype dt, cudaStream_t s);
 int seq_simt_splits(long long groups, int rows, int max_keys);
 
 // bf16 on the tensor cores, many rows a group (seq_rows_sm103.cu): no lens, no
-// pages; the expanded latent shape.
+// pages; the expanded latent shape to o and lse, or d = 64, 96, 128 to partial
+// results.
 cudaError_t launch_seq_rows(const SeqAttn& p, cudaStream_t s);
+int seq_rows_splits(int groups, int rows, int row_block, int n_keys);
+
+// bf16 on the tensor cores, few rows a group over (paged) caches
+// (seq_decode_sm103.cu).  Groups are (sequence, head) pairs, lens per
+// sequence; the tiles of all sequences are cut into `cuts` ranges per head and
+// group of nr rows.  Pieces go to part_o [slot][dv] and part_lse [slot], slot
+// = ((row group * (cuts + n_seq)) + cut + sequence) * nr + row.
+struct DecodePlan {
+  int n_seq, heads;
+  int nr;          // query rows of a CTA: 16, 32 or 64
+  int row_groups;  // of nr rows each
+  int cuts;
+  int direct;      // keys and values shared (the latent form): whole sequences go straight to o and lse
+  int box;         // tokens of one load: 64, or 32 or 16 where pages are not whole tiles
+};
+DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box);
+size_t decode_slots(const DecodePlan& w);  // rows of part_o
+cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, cudaStream_t s);
+// o, lse = the pieces merged, with the partial results pre_o [pre][total][dv] of other keys
+cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
+                                    int pre, cudaStream_t s);
 
 // o, lse = the merged partial results [splits][total] (seq_combine.cu).
 cudaError_t launch_seq_combine(const float* part_o, const float* part_lse, int splits, long long total, int dv,

@@ -569,21 +569,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+RowsPlan rows_plan(int rows, int row_block, bool causal) {
+  RowsPlan w{};
+  w.block_rows = row_block == kAllRows ? rows : row_block;
+  w.blocks = rows / w.block_rows;
+  w.per_tile = w.block_rows <= BR ? BR / w.block_rows : 1;
+  if (causal) w.per_tile = 1;  // a causal tile lies in one block
+  if (w.per_tile > w.blocks) w.per_tile = w.blocks;
+  w.per_block = (w.block_rows + BR - 1) / BR;
+  w.tiles = w.per_block > 1 ? w.blocks * w.per_block : (w.blocks + w.per_tile - 1) / w.per_tile;
+  w.pairs = (w.tiles + 1) / 2;
+  return w;
+}
+
 template <int DQK, int DV, int D2, bool PART>
 cudaError_t launch_rows(const SeqAttn& p, cudaStream_t s) {
   using C = Cfg<DQK, DV>;
   static SmemOnce once;
   cudaError_t e = once(fa_seq_rows_sm103_kernel<DQK, DV, D2, PART>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  RowsPlan w{};
-  w.block_rows = p.row_block == kAllRows ? p.rows : p.row_block;
-  w.blocks = p.rows / w.block_rows;
-  w.per_tile = w.block_rows <= BR ? BR / w.block_rows : 1;
-  if (p.causal) w.per_tile = 1;  // a causal tile lies in one block
-  if (w.per_tile > w.blocks) w.per_tile = w.blocks;
-  w.per_block = (w.block_rows + BR - 1) / BR;
-  w.tiles = w.per_block > 1 ? w.blocks * w.per_block : (w.blocks + w.per_tile - 1) / w.per_tile;
-  w.pairs = (w.tiles + 1) / 2;
+  RowsPlan w = rows_plan(p.rows, p.row_block, p.causal != 0);
   w.heavy_first = p.causal && p.splits == 1;
   const long long items = static_cast<long long>(w.pairs) * p.groups * p.splits;
   if (items > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
@@ -608,8 +613,32 @@ cudaError_t launch_rows(const SeqAttn& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_seq_rows(const SeqAttn& p, cudaStream_t s) {
-  if (p.d2 == 64 && p.d1 == 128 && p.dv == 128 && p.part_o == nullptr) return launch_rows<192, 128, 64, false>(p, s);
+  if (p.part_o == nullptr)
+    return p.d2 == 64 && p.d1 == 128 && p.dv == 128 ? launch_rows<192, 128, 64, false>(p, s) : cudaErrorInvalidValue;
+  if (p.d1 == 64) return launch_rows<64, 64, 0, true>(p, s);
+  if (p.d1 == 96) return launch_rows<96, 96, 0, true>(p, s);
+  if (p.d1 == 128) return launch_rows<128, 128, 0, true>(p, s);
   return cudaErrorInvalidValue;
+}
+
+int seq_rows_splits(int groups, int rows, int row_block, int n_keys) {
+  const int tiles = (n_keys + BC - 1) / BC;
+  const RowsPlan w = rows_plan(rows, row_block, false);
+  const long long items = static_cast<long long>(w.pairs) * groups;
+  // the share of the SMs' time that whole rounds of items fill, against the
+  // partial results that more splits write and merge (a hundredth each)
+  int best = 1;
+  double top = -1.0;
+  for (int n = 1; n <= tiles && n <= 152; ++n) {
+    const long long all = items * n, rounds = (all + 151) / 152;
+    const double per = static_cast<double>((tiles + n - 1) / n) * n / tiles;  // the longest split over the mean
+    const double score = static_cast<double>(all) / (152.0 * rounds) / per - 0.01 * static_cast<double>(rows) / 1024 * n;
+    if (score > top) {
+      top = score;
+      best = n;
+    }
+  }
+  return best;
 }
 
 }  // namespace fa
