@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   const WaitCtl wc{p.status, abort_flag, p.wait_ns};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   // heads vary fastest, the longest tiles come first
   const int heads = p.B * p.H;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   if (warp == 9) {
     // ------------------------------------------------------------------ TMA
@@ -185,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
+    // The whole warp runs it, converged (see mma_ss_w).
+    {
       constexpr uint32_t idesc_s = idesc_bf16_f32(BR, BC, 0, 0);
       constexpr uint32_t idesc_a2 = idesc_bf16_f32(BR, DQK, 0, 1);
       constexpr uint32_t idesc_a1 = idesc_bf16_f32(BR, DV, 0, 1);
@@ -194,18 +195,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Desc2 bd = desc_sw128(sb + OFF_B + (it % STAGES) * STAGE_BYTES, 16, 1024);
 #pragma unroll
         for (int k = 0; k < DQK / 16; ++k)
-          mma_ss2(tmem + TM_S + 64 * (it & 1), a, ((k >> 2) * A_CHUNK + (k & 3) * 32) >> 4, bd,
+          mma_ss_w(tmem + TM_S + 64 * (it & 1), a, ((k >> 2) * A_CHUNK + (k & 3) * 32) >> 4, bd,
                   ((k >> 2) * B_CHUNK + (k & 3) * 32) >> 4, idesc_s, k > 0);
-        mma_commit(bar.s_full(it & 1));
+        mma_commit_w(bar.s_full(it & 1));
       };
       auto issue_dp = [&](int it) {
         const Desc2 a = desc_sw128(sb + OFF_A2, 16, 1024);
         const Desc2 bd = desc_sw128(sb + OFF_B + (it % STAGES) * STAGE_BYTES + 3 * B_CHUNK, 16, 1024);
 #pragma unroll
         for (int k = 0; k < DV / 16; ++k)
-          mma_ss2(tmem + TM_DP, a, ((k >> 2) * A_CHUNK + (k & 3) * 32) >> 4, bd,
+          mma_ss_w(tmem + TM_DP, a, ((k >> 2) * A_CHUNK + (k & 3) * 32) >> 4, bd,
                   ((k >> 2) * B_CHUNK + (k & 3) * 32) >> 4, idesc_s, k > 0);
-        mma_commit(bar.dp_full());
+        mma_commit_w(bar.dp_full());
       };
       auto issue_acc = [&](int it) {
         const uint32_t t = tmem + TM_S + 64 * (it & 1);
@@ -216,16 +217,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Desc2 b2 = desc_sw128(st + 3 * B_CHUNK, B_CHUNK, 1024);
 #pragma unroll
           for (int k = 0; k < BC / 16; ++k)
-            mma_ts2(tmem + TM_ACC1, t + 32 * (k >> 1) + 8 * (k & 1), b2, (k * 16 * 128) >> 4, idesc_a1, it > 0 || k > 0);
+            mma_ts_w(tmem + TM_ACC1, t + 32 * (k >> 1) + 8 * (k & 1), b2, (k * 16 * 128) >> 4, idesc_a1, it > 0 || k > 0);
         }
         const Desc2 b1 = desc_sw128(st, B_CHUNK, 1024);
 #pragma unroll
         for (int k = 0; k < BC / 16; ++k)
-          mma_ts2(tmem + TM_ACC2, t + 32 * (k >> 1) + 16 + 8 * (k & 1), b1, (k * 16 * 128) >> 4, idesc_a2,
+          mma_ts_w(tmem + TM_ACC2, t + 32 * (k >> 1) + 16 + 8 * (k & 1), b1, (k * 16 * 128) >> 4, idesc_a2,
                   it > 0 || k > 0);
-        mma_commit(bar.st_free(it % STAGES));
+        mma_commit_w(bar.st_free(it % STAGES));
       };
-      bool ok = nsteps > 0 && mbar_wait2(bar.a_full(), 0, bar.st_full(0), 0, wc);
+      bool ok = nsteps > 0 && warp_wait2(bar.a_full(), 0, bar.st_full(0), 0, wc);
       if (ok) {
         tc_fence_after();
         issue_s(0);
@@ -234,19 +235,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; ok && it < nsteps; ++it) {
         const bool more = it + 1 < nsteps;
         if (more) {
-          ok = mbar_wait(bar.st_full((it + 1) % STAGES), ((it + 1) / STAGES) & 1, wc);
+          ok = warp_wait(bar.st_full((it + 1) % STAGES), ((it + 1) / STAGES) & 1, wc);
           if (!ok) break;
           tc_fence_after();
           issue_s(it + 1);
         }
-        ok = mbar_wait(bar.e_full(), it & 1, wc);
+        ok = warp_wait(bar.e_full(), it & 1, wc);
         if (!ok) break;
         tc_fence_after();
         if (more) issue_dp(it + 1);
         issue_acc(it);
       }
       // every MMA this thread issued must finish before tensor memory is read or freed
-      mma_commit(bar.fin());
+      mma_commit_w(bar.fin());
       WaitCtl drain{nullptr, nullptr, wc.limit_ns};
       mbar_wait(bar.fin(), 0, drain);
     }
@@ -263,15 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       row_l2 = p.lse2[bh * npad + r];  // padded to whole tiles
       row_d = p.dsum[bh * npad + r];
     }
-    auto warp_wait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
-    };
     bool ok = true;
     for (int it = 0; it < nsteps; ++it) {
       const uint32_t tS = tl + TM_S + 64 * (it & 1) + 32 * half, tD = tl + TM_DP + 32 * half;
       // (the stage's own barrier too: this thread reads the row terms that it counts)
-      if (!warp_wait(bar.s_full(it & 1), (it >> 1) & 1) ||
-          (KEYS && !warp_wait(bar.st_full(it % STAGES), (it / STAGES) & 1))) {
+      if (!warp_wait(bar.s_full(it & 1), (it >> 1) & 1, wc) ||
+          (KEYS && !warp_wait(bar.st_full(it % STAGES), (it / STAGES) & 1, wc))) {
         ok = false;
         break;
       }
@@ -312,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
         tmem_st_32x32b_x16(tS, pk);
       }
-      if (!warp_wait(bar.dp_full(), it & 1)) {
+      if (!warp_wait(bar.dp_full(), it & 1, wc)) {
         tmem_wait_st();
         ok = false;
         break;
@@ -339,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar.e_full());
     }
     // -------------------------------------------------------------- output
-    const bool have = ok && warp_wait(bar.fin(), 0) && !*abort_flag;
+    const bool have = ok && warp_wait(bar.fin(), 0, wc) && !*abort_flag;
     tc_fence_after();
     // columns [lo, hi) of an accumulator, 32 at a time; zeros where nothing was streamed
     auto load32 = [&](uint32_t col, float mul, float* x) {

@@ -150,17 +150,21 @@ __device__ __forceinline__ int owner(long long total, long long x, int n) {
   return static_cast<int>(((x + 1) * n - 1) / total);
 }
 
-// Columns v[0..N) of 16 lanes reduced over the lanes: afterwards lane l holds
-// columns N / 16 (its bits, high first) ... in v[0 .. N/16).  Lanes 16-31 mirror.
+// Columns v[0..N) of the 16 lanes of a half-warp reduced over them: lane l
+// ends with max(1, N / 16) columns in v[0 ..), from column reduce_col<N>() on.
 template <int H, int BIT, int N, typename Op>
 __device__ __forceinline__ void reduce_step(float (&v)[N], Op op) {
   if constexpr (BIT >= 1) {
     const bool up = (threadIdx.x & BIT) != 0;
+    if constexpr (H >= 1) {
 #pragma unroll
-    for (int i = 0; i < H; ++i) {
-      const float send = up ? v[i] : v[i + H];
-      const float keep = up ? v[i + H] : v[i];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, BIT));
+      for (int i = 0; i < H; ++i) {
+        const float send = up ? v[i] : v[i + H];
+        const float keep = up ? v[i + H] : v[i];
+        v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, BIT));
+      }
+    } else {
+      v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], BIT));
     }
     reduce_step<H / 2, BIT / 2>(v, op);
   }
@@ -168,6 +172,14 @@ __device__ __forceinline__ void reduce_step(float (&v)[N], Op op) {
 template <int N, typename Op>
 __device__ __forceinline__ void reduce16(float (&v)[N], Op op) {
   reduce_step<N / 2, 8>(v, op);
+}
+template <int N>
+__device__ __forceinline__ int reduce_col() {
+  int col = 0;
+#pragma unroll
+  for (int h = N / 2, bit = 8; h >= 1; h /= 2, bit /= 2)
+    if (threadIdx.x & bit) col += h;
+  return col;
 }
 
 __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool x) {
@@ -208,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* s_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // first sequence, its first tile, tiles of this CTA
   const WaitCtl wc{p.status, abort_flag, p.wait_ns};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   // this CTA: rows r0 .. of head `head` of every sequence (group b * heads + head), range `cut` of `cuts`
   const int grp = blockIdx.x / plan.cuts, cut = blockIdx.x % plan.cuts;
@@ -280,14 +292,15 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int start_b = s_start[0], start_t = s_start[1], n_tiles = s_start[2];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const int start_b = __shfl_sync(0xffffffffu, s_start[0], 0), start_t = __shfl_sync(0xffffffffu, s_start[1], 0),
+            n_tiles = __shfl_sync(0xffffffffu, s_start[2], 0);
 
-  // walks the pieces: f(sequence, its keys, first tile, tiles) until it returns false
+  // walks the pieces, a whole warp at a time: f(sequence, its keys, first tile, tiles) until it returns false
   auto pieces = [&](auto f) {
     int b = start_b, t = start_t, left = n_tiles;
     while (left > 0) {
-      const int nk = seq_len(p, b, false);
+      const int nk = __shfl_sync(0xffffffffu, seq_len(p, b, false), 0);
       const int take = min(left, tiles_of(nk) - t);
       if (take > 0) {
         if (!f(b, nk, t, take)) return;
@@ -304,11 +317,9 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
     // (64 tokens, or fewer where pages are not whole tiles).
     const int box = plan.box, per = BC / box;
     int g = 0, nq = 0;  // tiles and pieces issued
-    bool ok = true;
-    auto wait = [&](uint32_t bar_addr, uint32_t parity) {
-      ok = __all_sync(0xffffffffu, mbar_wait_backoff(bar_addr, parity, wc));
-      return ok;
-    };
+    int ms = 0, xs = 0;            // next slots of the rings, and the parity their release completes
+    uint32_t mp = 1, xp = 1;
+    auto wait = [&](uint32_t bar_addr, uint32_t parity) { return warp_wait(bar_addr, parity, wc); };
     pieces([&](int b, int nk, int t0, int n) -> bool {
       const int group = b * plan.heads + head;
       if (nq > 0 && !wait(bar.q_free(), (nq - 1) & 1)) return false;
@@ -317,20 +328,17 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
         for (int c = 0; c < C::QC; ++c) tma_load_3d(sQ + c * NR * 128, &maps.q, bar.q_full(), c * 64, r0, group);
       }
       ++nq;
-      // row coordinates of this lane's box: token within the page, page
+      // this lane's box of a tile: token within its page, page (as the table has it)
       auto place = [&](int tile, int& tok, int& page) {
         const int j = tile * BC + lane * box;
         tok = 0;
-        page = 0;
-        if (lane >= per || j >= nk) return;
-        tok = p.page_size > 0 ? j % p.page_size : j;
         page = group;
+        if (lane >= per || j >= nk) return;
+        tok = j;
         if (p.table != nullptr) {
-          page = p.table[static_cast<long long>(b) * p.max_pages + j / p.page_size];
-          if (page < 0 || page >= p.n_pages) {
-            atomicOr(p.status, kStatusInput);
-            page = p.n_pages;  // outside: reads as zeros
-          }
+          const int q = j / p.page_size;
+          tok = j - q * p.page_size;
+          page = p.table[static_cast<long long>(b) * p.max_pages + q];
         }
       };
       int tok, page;
@@ -340,27 +348,43 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
         const int boxes = (valid + box - 1) / box;
         int tok1 = 0, page1 = 0;
         if (i + 1 < n) place(t0 + i + 1, tok1, page1);  // the next tile's pages, while this one loads
+        if (p.table != nullptr && lane < boxes && (page < 0 || page >= p.n_pages)) {
+          atomicOr(p.status, kStatusInput);
+          page = p.n_pages;  // outside the cache: reads as zeros
+        }
         auto load_x = [&]() -> bool {
-          const int s = g % NX;
-          if (g >= NX && !wait(bar.x_free(s), (g / NX - 1) & 1)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(bar.x_full(s), boxes * box * 128 * XC);
+          if (!wait(bar.x_free(xs), xp)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(bar.x_full(xs), boxes * box * 128 * XC);
           __syncwarp();
-          if (lane < boxes)
+          if (lane < boxes) {
+#pragma unroll
             for (int c = 0; c < XC; ++c)
-              tma_load_3d(sX + s * C::X_BYTES + c * CB + lane * box * 128, &maps.x, bar.x_full(s),
+              tma_load_3d(sX + xs * C::X_BYTES + c * CB + lane * box * 128, &maps.x, bar.x_full(xs),
                           (SHARED ? DM : 0) + c * 64, tok, page);
+          }
+          __syncwarp();
+          if (++xs == NX) {
+            xs = 0;
+            xp ^= 1;
+          }
           return true;
         };
         if (!SHARED && !load_x()) return false;
         for (int u = 0; u < UM; ++u) {
-          const int k = g * UM + u, s = k % NM;
-          if (k >= NM && !wait(bar.m_free(s), (k / NM - 1) & 1)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(bar.m_full(s), boxes * box * 128 * UC);
+          if (!wait(bar.m_free(ms), mp)) return false;
+          if (lane == 0) mbar_arrive_expect_tx(bar.m_full(ms), boxes * box * 128 * UC);
           __syncwarp();
-          if (lane < boxes)
+          if (lane < boxes) {
+#pragma unroll
             for (int c = 0; c < UC; ++c)
-              tma_load_3d(sM + s * C::M_BYTES + c * CB + lane * box * 128, &maps.m, bar.m_full(s),
-                          (u * UC + c) * 64, tok, page);
+              tma_load_3d(sM + ms * C::M_BYTES + c * CB + lane * box * 128, &maps.m, bar.m_full(ms), (u * UC + c) * 64,
+                          tok, page);
+          }
+          __syncwarp();
+          if (++ms == NM) {
+            ms = 0;
+            mp ^= 1;
+          }
         }
         if (SHARED && !load_x()) return false;
         tok = tok1;
@@ -379,116 +403,146 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
     __syncwarp();
   } else if (warp == 4) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(BC, NR, 0, 0);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(C::UDIM, NR, 1, 0);
-      const Desc2 dq = desc_sw128(sQ, 16, 1024), dp = desc_sw128(sP, 16, 1024);
-      bool ok = true;
-      int g = 0, nq = 0;
-      auto issue_s = [&](int k) -> bool {  // S^T of the k-th tile, into buffer k % 2
-        const uint32_t dt = tmem + C::TM_S + NR * (k & 1);
-        uint32_t acc = 0;
-        if (SHARED) {
-          for (int u = 0; u < UM; ++u) {
-            const int m = k * UM + u;
-            if (!mbar_wait(bar.m_full(m % NM), (m / NM) & 1, wc)) return false;
+    // The whole warp runs it, converged (see mma_ss_w).  Two streams of work:
+    // S^T of tile after tile, a ring unit at a time as its loads land, at most
+    // one tile ahead of the values (two S buffers); and O^T of a tile once its
+    // P is published.  Whichever is ready goes first, so that a late load
+    // does not hold up the product that frees ring space for later ones.
+    constexpr uint32_t idesc_s = idesc_bf16_f32(BC, NR, 0, 0);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(C::UDIM, NR, 1, 0);
+    constexpr int UNITS = SHARED ? UM + 1 : 1;  // ring units that S^T of a tile reads
+    const Desc2 dq = desc_sw128(sQ, 16, 1024), dp = desc_sw128(sP, 16, 1024);
+    const Desc2 dm_k = desc_sw128(sM, 16, 1024), dx = desc_sw128(sX, 16, 1024), dm_v = desc_sw128(sM, CB, 1024);
+    bool ok = true;
+    int nq = 0;
+    int ms = 0, xs = 0, vs = 0;  // M and X slots of the next S^T unit, M slot of the next value unit
+    uint32_t mp = 0, xp = 0, vp = 0, sbuf = 0, pp = 0;
+    pieces([&](int, int, int, int n) -> bool {
+      if (!(ok = warp_wait(bar.q_full(), nq & 1, wc))) return false;
+      tc_fence_after();
+      int s_tile = 0, s_unit = 0, o_tile = 0;  // progress within the piece
+      unsigned long long since = 0;
+      while (o_tile < n) {
+        bool moved = false;
+        if (s_tile < n && s_tile <= o_tile + 1) {
+          const bool x_unit = s_unit == UNITS - 1;
+          if (x_unit ? warp_test(bar.x_full(xs), xp) : warp_test(bar.m_full(ms), mp)) {
+            moved = true;
             tc_fence_after();
-            const Desc2 da = desc_sw128(sM + (m % NM) * C::M_BYTES, 16, 1024);
+            const uint32_t dt = tmem + C::TM_S + NR * sbuf;
+            if (x_unit) {
+              constexpr int QX = SHARED ? UM * UC : 0;
+              const uint32_t at = (xs * C::X_BYTES) >> 4;
 #pragma unroll
-            for (int kk = 0; kk < UC * 4; ++kk) {
-              mma_ss2(dt, da, ((kk >> 2) * CB + (kk & 3) * 32) >> 4, dq,
-                      ((u * UC + (kk >> 2)) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, acc);
-              acc = 1;
+              for (int kk = 0; kk < DX / 16; ++kk)
+                mma_ss_w(dt, dx, at + (((kk >> 2) * CB + (kk & 3) * 32) >> 4), dq,
+                         ((QX + (kk >> 2)) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, SHARED || kk > 0);
+              mma_commit_w(bar.x_free(xs));
+              mma_commit_w(bar.s_full(sbuf));
+              if (++xs == NX) {
+                xs = 0;
+                xp ^= 1;
+              }
+              sbuf ^= 1;
+              s_unit = 0;
+              if (++s_tile == n) mma_commit_w(bar.q_free());  // no later product of this piece reads Q
+            } else {
+              const uint32_t at = (ms * C::M_BYTES) >> 4, qo = (s_unit * UC * NR * 128) >> 4;
+#pragma unroll
+              for (int kk = 0; kk < UC * 4; ++kk)
+                mma_ss_w(dt, dm_k, at + (((kk >> 2) * CB + (kk & 3) * 32) >> 4), dq,
+                         qo + (((kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4), idesc_s, s_unit > 0 || kk > 0);
+              ++s_unit;
+              if (++ms == NM) {
+                ms = 0;
+                mp ^= 1;
+              }
             }
           }
         }
-        if (!mbar_wait(bar.x_full(k % NX), (k / NX) & 1, wc)) return false;
-        tc_fence_after();
-        const Desc2 da = desc_sw128(sX + (k % NX) * C::X_BYTES, 16, 1024);
-        constexpr int QX = SHARED ? UM * UC : 0;
+        if (o_tile < s_tile && warp_test(bar.p_full(), pp)) {
+          bool values = true;
+          if (!SHARED) values = warp_test(bar.m_full(vs), vp);
+          if (values) {
+            moved = true;
+            tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < DX / 16; ++kk) {
-          mma_ss2(dt, da, ((kk >> 2) * CB + (kk & 3) * 32) >> 4, dq, ((QX + (kk >> 2)) * NR * 128 + (kk & 3) * 32) >> 4,
-                  idesc_s, acc);
-          acc = 1;
-        }
-        mma_commit(bar.x_free(k % NX));
-        mma_commit(bar.s_full(k & 1));
-        return true;
-      };
-      pieces([&](int, int, int, int n) -> bool {
-        ok = mbar_wait(bar.q_full(), nq & 1, wc);
-        if (!ok) return false;
-        tc_fence_after();
-        if (!(ok = issue_s(g))) return false;
-        if (n == 1) mma_commit(bar.q_free());
-        for (int i = 0; i < n; ++i, ++g) {
-          if (i + 1 < n) {
-            if (!(ok = issue_s(g + 1))) return false;
-            if (i + 2 == n) mma_commit(bar.q_free());  // no later product of this piece reads Q
-          }
-          if (!(ok = mbar_wait(bar.p_full(), g & 1, wc))) return false;
-          tc_fence_after();
+            for (int u = 0; u < UM; ++u) {
+              const uint32_t at = (vs * C::M_BYTES) >> 4;
 #pragma unroll
-          for (int u = 0; u < UM; ++u) {
-            const int m = g * UM + u;
-            if (!SHARED) {
-              if (!(ok = mbar_wait(bar.m_full(m % NM), (m / NM) & 1, wc))) return false;
-              tc_fence_after();
+              for (int kk = 0; kk < BC / 16; ++kk)
+                mma_ss_w(tmem + u * NR, dm_v, at + ((kk * 16 * 128) >> 4), dp, (kk * 32) >> 4, idesc_o,
+                         o_tile > 0 || kk > 0);
+              mma_commit_w(bar.m_free(vs));
+              if (++vs == NM) {
+                vs = 0;
+                vp ^= 1;
+              }
             }
-            const Desc2 da = desc_sw128(sM + (m % NM) * C::M_BYTES, CB, 1024);
-#pragma unroll
-            for (int kk = 0; kk < BC / 16; ++kk)
-              mma_ss2(tmem + u * NR, da, (kk * 16 * 128) >> 4, dp, (kk * 32) >> 4, idesc_o, i > 0 || kk > 0);
-            mma_commit(bar.m_free(m % NM));
+            mma_commit_w(bar.o_done());
+            pp ^= 1;
+            ++o_tile;
           }
-          mma_commit(bar.o_done());
         }
-        ++nq;
-        return true;
-      });
-      // every MMA this thread issued must finish before tensor memory is freed
-      mma_commit(bar.drain());
-      WaitCtl drain{nullptr, nullptr, wc.limit_ns};
-      mbar_wait(bar.drain(), 0, drain);
-    }
+        if (moved) {
+          since = 0;
+        } else if (since == 0) {
+          since = globaltimer_ns();
+        } else {
+          // neither stream has moved: the wait is bounded like every other
+          bool late = globaltimer_ns() - since > wc.limit_ns;
+          late = __any_sync(0xffffffffu, late);
+          if (late) record_timeout(wc);
+          if (__any_sync(0xffffffffu, late || *abort_flag != 0)) return ok = false;
+        }
+      }
+      ++nq;
+      return true;
+    });
+    // every MMA this warp issued must finish before tensor memory is freed
+    mma_commit_w(bar.drain());
+    WaitCtl drain{nullptr, nullptr, wc.limit_ns};
+    mbar_wait(bar.drain(), 0, drain);
     __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
-    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const int key = warp * 16 + lane;  // this thread's key of a tile (lane < 16)
-    const bool live = lane < 16;
-    const float sl = p.scale * 1.4426950408889634f;
+    // Tensor memory hands the scores of key 16 w + l to lane l < 16 of warp w;
+    // lane l + 16 takes half of them over (columns NR / 2 ..), so that every
+    // lane has NH columns of one key.
+    constexpr int NH = NR / 2;
     constexpr int LW = NR < 32 ? 16 : 32;  // columns per tensor-memory access
-    // own entry of row c of P: K-major, 128-byte swizzle
-    const uint32_t p_at = sP + (key & 7) * 2;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    const int key = warp * 16 + (lane & 15), col = lane < 16 ? 0 : NH;
+    const float sl = p.scale * 1.4426950408889634f;
+    // P is [row][64 keys], 128-byte rows, 16-byte chunks swizzled by row % 8.
+    // Lanes of an even and an odd key pair up: the even one writes both keys'
+    // P of an even column, the odd one those of the column after it.
+    const int odd = lane & 1;
+    uint32_t p_at[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      p_at[q] = sP + (col + 2 * q + odd) * 128 + (((key >> 3) ^ (2 * q + odd)) << 4) + (key & 6) * 2;
+    const int my_col = col + reduce_col<NH>();  // first column this lane owns after reduce16
+    constexpr int OWN = NH >= 16 ? NH / 16 : 1;
     int g = 0;
     bool ok = true;
-    auto warp_wait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
-    };
     // all four warps give up together: a barrier's count must be met on every path
     auto wait_all = [&](uint32_t bar_addr, uint32_t parity) -> bool {
-      ok = !bar_any(1, 128, !warp_wait(bar_addr, parity));
+      ok = !bar_any(1, 128, !warp_wait(bar_addr, parity, wc));
       return ok;
     };
-    // columns this lane owns after reduce16
-    int col0 = 0;
-#pragma unroll
-    for (int h = NR / 2, bit = 8; bit >= 1; h /= 2, bit /= 2)
-      if (lane & bit) col0 += h;
 
     pieces([&](int b, int nk, int t0, int n) -> bool {
       const int group = b * plan.heads + head;
-      float l[NR], lr[NR];  // this key's share of the row sums: of P, and of P rounded to bf16 (what multiplies V)
+      float l[NH], lr[NH];  // this key's share of the row sums: of P, and of P rounded to bf16 (what multiplies V)
 #pragma unroll
-      for (int c = 0; c < NR; ++c) l[c] = lr[c] = 0.f;
+      for (int c = 0; c < NH; ++c) l[c] = lr[c] = 0.f;
       if (threadIdx.x < NR) s_nref[threadIdx.x] = kUnset;
       named_bar_sync(1, 128);
       for (int i = 0; i < n; ++i, ++g) {
         if (!wait_all(bar.s_full(g & 1), (g >> 1) & 1)) return false;
         tc_fence_after();
-        float s[NR];
+        float s[NH];
         {
           uint32_t r[NR];
 #pragma unroll
@@ -499,17 +553,16 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
               tmem_ld_32x32b_x32(tl + C::TM_S + NR * (g & 1) + c, r + c);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < NR; ++c) s[c] = __uint_as_float(r[c]);
+          for (int c = 0; c < NH; ++c) {
+            const uint32_t far = __shfl_xor_sync(0xffffffffu, r[c + NH], 16);
+            s[c] = __uint_as_float(lane < 16 ? r[c] : far);
+          }
         }
         const int j0 = (t0 + i) * BC;
         if (j0 + BC > nk - (p.n_new - 1)) {
           const int room = nk - (j0 + key);  // > lag: the row sees this key
 #pragma unroll
-          for (int c = 0; c < NR; ++c) s[c] = s_lag[c] < room ? s[c] : -INFINITY;
-        }
-        if (!live) {
-#pragma unroll
-          for (int c = 0; c < NR; ++c) s[c] = -INFINITY;
+          for (int c = 0; c < NH; ++c) s[c] = s_lag[col + c] < room ? s[c] : -INFINITY;
         }
         // values past the sequence's end multiply zero probabilities: they must be finite
         const int valid = min(BC, nk - j0);
@@ -525,22 +578,20 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
         }
         float over = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NR; c += 4) {
-          const float4 nr = *reinterpret_cast<const float4*>(s_nref + c);
+        for (int c = 0; c < NH; c += 4) {
+          const float4 nr = *reinterpret_cast<const float4*>(s_nref + col + c);
           over = fmax3(over, fmaf(s[c], sl, nr.x), fmaf(s[c + 1], sl, nr.y));
           over = fmax3(over, fmaf(s[c + 2], sl, nr.z), fmaf(s[c + 3], sl, nr.w));
         }
         if (bar_any(1, 128, over > kRescaleThreshold)) {
           // some row's reference rises: column maxima over the 64 keys
           {
-            float v[NR];
+            float v[NH];
 #pragma unroll
-            for (int c = 0; c < NR; ++c) v[c] = s[c] * sl;
-            reduce16<NR>(v, [](float a, float c) { return fmaxf(a, c); });
-            if (live) {
+            for (int c = 0; c < NH; ++c) v[c] = s[c] * sl;
+            reduce16<NH>(v, [](float x, float y) { return fmaxf(x, y); });
 #pragma unroll
-              for (int e = 0; e < NR / 16; ++e) s_red[warp * NR + col0 + e] = v[e];
-            }
+            for (int e = 0; e < OWN; ++e) s_red[warp * NR + my_col + e] = v[e];
           }
           named_bar_sync(1, 128);
           if (threadIdx.x < NR) {
@@ -556,8 +607,8 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
           }
           named_bar_sync(1, 128);
 #pragma unroll
-          for (int c = 0; c < NR; ++c) {
-            const float a = s_alpha[c];
+          for (int c = 0; c < NH; ++c) {
+            const float a = s_alpha[col + c];
             l[c] *= a;
             lr[c] *= a;
           }
@@ -582,24 +633,30 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
             tmem_wait_st();
           }
         }
+        uint32_t pk[NH / 2];
+#pragma unroll
+        for (int c = 0; c < NH; c += 4) {
+          const float4 nr = *reinterpret_cast<const float4*>(s_nref + col + c);
+          const float p0 = ex2_approx(fmaf(s[c], sl, nr.x)), p1 = ex2_approx(fmaf(s[c + 1], sl, nr.y));
+          const float p2 = ex2_approx(fmaf(s[c + 2], sl, nr.z)), p3 = ex2_approx(fmaf(s[c + 3], sl, nr.w));
+          const uint32_t a = pack_bf16x2(p0, p1), bq = pack_bf16x2(p2, p3);
+          l[c] += p0;
+          l[c + 1] += p1;
+          l[c + 2] += p2;
+          l[c + 3] += p3;
+          lr[c] += __uint_as_float(a << 16);
+          lr[c + 1] += __uint_as_float(a & 0xffff0000u);
+          lr[c + 2] += __uint_as_float(bq << 16);
+          lr[c + 3] += __uint_as_float(bq & 0xffff0000u);
+          const uint32_t ya = __shfl_xor_sync(0xffffffffu, a, 1), yb = __shfl_xor_sync(0xffffffffu, bq, 1);
+          pk[c / 2] = odd ? __byte_perm(ya, a, 0x7632) : __byte_perm(a, ya, 0x5410);
+          pk[c / 2 + 1] = odd ? __byte_perm(yb, bq, 0x7632) : __byte_perm(bq, yb, 0x5410);
+        }
         // P_{g-1} has been read once its P V has completed
         if (g > 0 && !wait_all(bar.o_done(), (g - 1) & 1)) return false;
 #pragma unroll
-        for (int c = 0; c < NR; c += 4) {
-          const float4 nr = *reinterpret_cast<const float4*>(s_nref + c);
-          const float nv[4] = {nr.x, nr.y, nr.z, nr.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float pv = ex2_approx(fmaf(s[c + e], sl, nv[e]));
-            const __nv_bfloat16 ph = __float2bfloat16_rn(pv);
-            l[c + e] += pv;
-            lr[c + e] += __bfloat162float(ph);
-            if (live)
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(p_at + (c + e) * 128 + ((((key >> 3) ^ (c + e)) & 7) << 4)),
-                           "h"(__bfloat16_as_ushort(ph))
-                           : "memory");
-          }
-        }
+        for (int c = 0; c < NH / 2; ++c)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_at[c & 3] + (c >> 2) * 1024), "r"(pk[c]) : "memory");
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
@@ -607,12 +664,10 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
       }
       // ------------------------------------------------------------ output
       float ref = 0.f, sum = 0.f, sum_r = 0.f;  // of row threadIdx.x
-      reduce16<NR>(l, [](float a, float c) { return a + c; });
-      reduce16<NR>(lr, [](float a, float c) { return a + c; });
-      if (live) {
+      reduce16<NH>(l, [](float x, float y) { return x + y; });
+      reduce16<NH>(lr, [](float x, float y) { return x + y; });
 #pragma unroll
-        for (int e = 0; e < NR / 16; ++e) s_red[warp * NR + col0 + e] = l[e];
-      }
+      for (int e = 0; e < OWN; ++e) s_red[warp * NR + my_col + e] = l[e];
       named_bar_sync(1, 128);
       if (threadIdx.x < NR) {
         const int c = threadIdx.x;
@@ -620,12 +675,10 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
         ref = s_nref[c] == kUnset ? 0.f : -s_nref[c];
       }
       named_bar_sync(1, 128);
-      if (live) {
 #pragma unroll
-        for (int e = 0; e < NR / 16; ++e) s_red[warp * NR + col0 + e] = lr[e];
-      }
+      for (int e = 0; e < OWN; ++e) s_red[warp * NR + my_col + e] = lr[e];
       named_bar_sync(1, 128);
-      const bool whole = p.part_o == nullptr || (plan.direct && t0 == 0 && n == tiles_of(nk));
+      const bool whole = plan.direct && t0 == 0 && n == tiles_of(nk);
       const long long slot = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + cut + b;
       const long long orow0 = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r0;
       if (threadIdx.x < NR) {
@@ -643,9 +696,10 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
       if (!wait_all(bar.o_done(), (g - 1) & 1)) return false;  // also orders s_alpha
       tc_fence_after();
       const int d0 = C::UDIM == 128 ? warp * 32 + lane : warp * 16 + lane;  // this lane's dimension of an M unit
-      const bool has_dim = (C::UDIM == 128 || live) && d0 < DV;
+      const bool has_dim = (C::UDIM == 128 || lane < 16) && d0 < DV;
 #pragma unroll 1
       for (int c = 0; c < UM * NR; c += LW) {
+        if (c % NR >= n_rows) continue;
         uint32_t o[LW];
         if constexpr (LW == 16)
           tmem_ld_32x32b_x16(tl + c, o);
@@ -681,17 +735,20 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
 
 // Merges the pieces of each sequence, and the partial results [pre][total] of
 // another set of keys beside them (the prefix), row by row: see
-// seq_combine.cu for the formula.  One warp per row.  Rows of a sequence that
-// was written directly are left alone.
+// seq_combine.cu for the formula.  One warp per row and 128 of its columns;
+// lane i holds the weight of part i, so that the parts' loads do not wait for
+// one another.  Rows of a sequence that was written directly are left alone.
 template <int NR>
 __global__ void __launch_bounds__(128)
     fa_seq_decode_merge_kernel(const __grid_constant__ SeqAttn p, const DecodePlan plan, const float* __restrict__ pre_o,
                                const float* __restrict__ pre_lse, int pre) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long idx = static_cast<long long>(blockIdx.x) * 4 + warp;  // (sequence, head, row)
-  if (idx >= static_cast<long long>(plan.n_seq) * plan.heads * p.rows) return;
-  const int r = static_cast<int>(idx % p.rows);
-  const int group = static_cast<int>(idx / p.rows);
+  const int slices = (p.dv + 127) / 128;
+  const long long idx = static_cast<long long>(blockIdx.x) * 4 + warp;  // (sequence, head, row, slice)
+  if (idx >= static_cast<long long>(plan.n_seq) * plan.heads * p.rows * slices) return;
+  const int slice = static_cast<int>(idx % slices);
+  const int r = static_cast<int>(idx / slices % p.rows);
+  const int group = static_cast<int>(idx / slices / p.rows);
   const int b = group / plan.heads, head = group % plan.heads;
   long long before, total;
   tile_sums(p, plan.n_seq, b, before, total);
@@ -706,35 +763,46 @@ __global__ void __launch_bounds__(128)
   const int grp = head * plan.row_groups + r / NR;
   const long long slot0 = (static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + c0 + b) * NR + r % NR;
   const long long row = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r;
-  auto part = [&](int i) -> long long { return i < pre ? i * p.total + row : slot0 + static_cast<long long>(i - pre) * NR; };
-  auto part_lse = [&](int i) { return i < pre ? pre_lse[part(i)] : p.part_lse[part(i)]; };
   n += pre;
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, part_lse(i));
+  auto part_lse = [&](int i) {
+    return i < pre ? pre_lse[i * p.total + row] : p.part_lse[slot0 + static_cast<long long>(i - pre) * NR];
+  };
+  const float mine = lane < n ? part_lse(lane) : -INFINITY;
+  float m = mine;
+  for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, part_lse(i));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float ref = m == -INFINITY ? 0.f : m;
-  float sum = 0.f;
-  for (int i = lane; i < n; i += 32) sum += expf(part_lse(i) - ref);
+  float sum = lane < n ? expf(mine - ref) : 0.f;
+  for (int i = lane + 32; i < n; i += 32) sum += expf(part_lse(i) - ref);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + row * p.dv;
-  for (int c = 4 * lane; c < p.dv; c += 128) {
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = 0; i < n; ++i) {
-      const float ls = part_lse(i);
-      if (ls == -INFINITY) continue;
-      const float w = expf(ls - ref) * inv;
-      const float4 v = *reinterpret_cast<const float4*>((i < pre ? pre_o : p.part_o) + part(i) * p.dv + c);
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+  const int c = slice * 128 + 4 * lane;
+  const bool on = c < p.dv;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const float ls = i0 == 0 ? mine : (i0 + lane < n ? part_lse(i0 + lane) : -INFINITY);
+    const float w = expf(ls - ref) * inv;
+    const int k = min(32, n - i0);
+#pragma unroll 8
+    for (int i = 0; i < k; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const int part = i0 + i;
+      const float* src = part < pre ? pre_o + (part * p.total + row) * p.dv
+                                    : p.part_o + (slot0 + static_cast<long long>(part - pre) * NR) * p.dv;
+      if (!on || wi == 0.f) continue;  // a part without keys holds zeros or nothing
+      const float4 v = *reinterpret_cast<const float4*>(src + c);
+      acc.x = fmaf(wi, v.x, acc.x);
+      acc.y = fmaf(wi, v.y, acc.y);
+      acc.z = fmaf(wi, v.z, acc.z);
+      acc.w = fmaf(wi, v.w, acc.w);
     }
-    *reinterpret_cast<uint2*>(o + c) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
   }
-  if (lane == 0 && p.lse != nullptr) p.lse[row] = m + logf(sum);
+  if (on)
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * p.dv + c) =
+        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+  if (slice == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = m + logf(sum);
 }
 
 template <int DM, int DX, bool SHARED, int NR>
@@ -794,7 +862,7 @@ cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, cudaStream_
 
 cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
                                     int pre, cudaStream_t s) {
-  const long long warps = static_cast<long long>(w.n_seq) * w.heads * p.rows;
+  const long long warps = static_cast<long long>(w.n_seq) * w.heads * p.rows * ((p.dv + 127) / 128);
   if ((warps + 3) / 4 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
   if (w.nr == 16)

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   const WaitCtl wc{p.status, abort_flag, p.wait_ns};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const int n_items = plan.n_items;
 
   // ring slot of chunk c of V_j's pair: where the pair wraps round the ring
@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   auto role_mma = [&]() {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
+    // The whole warp runs it, converged (see mma_ss_w).
+    {
       constexpr uint32_t idesc_qk = idesc_bf16_f32(BR, BC, 0, 0);
       constexpr uint32_t idesc_pv = idesc_bf16_f32(BR, C::DVP, 0, 1);
       int j0 = 0, nq = 0;
@@ -319,12 +320,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
             if (c * 64 + k4 * 16 >= DQK) break;
-            mma_ss2(tmem + tm_s(t), dq, (c * CHUNK + k4 * 32) >> 4, dk, (k4 * 32) >> 4, idesc_qk, c + k4 > 0);
+            mma_ss_w(tmem + tm_s(t), dq, (c * CHUNK + k4 * 32) >> 4, dk, (k4 * 32) >> 4, idesc_qk, c + k4 > 0);
           }
         }
-        mma_commit(bar.s_full(t));
-        if (it >= w.hi[t ^ 1] || t == 1) mma_commit(bar.k_empty(j % NST));  // the last reader of K_j
-        if (it == w.hi[t] - 1) mma_commit(bar.q_empty(t));                  // the last product that reads Q_t
+        mma_commit_w(bar.s_full(t));
+        if (it >= w.hi[t ^ 1] || t == 1) mma_commit_w(bar.k_empty(j % NST));  // the last reader of K_j
+        if (it == w.hi[t] - 1) mma_commit_w(bar.q_empty(t));                  // the last product that reads Q_t
       };
       auto issue_pv = [&](const Item& w, int t, int it) {  // O_t (+)= P_t V_it
         const int j = j0 + it;
@@ -332,20 +333,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Desc2 dv = desc_sw128(sR + v_slot(j, 0) * CHUNK, lbo, 1024);
 #pragma unroll
         for (int kk = 0; kk < BC / 16; ++kk)
-          mma_ts2(tmem + tm_o(t), tmem + tm_s(t) + kk * 8, dv, (kk * 16 * 128) >> 4, idesc_pv, it > 0 || kk > 0);
-        mma_commit(bar.o_done(t));
-        if (it >= w.hi[t ^ 1] || t == 1) mma_commit(bar.v_empty(j % NST));  // the last reader of V_j
+          mma_ts_w(tmem + tm_o(t), tmem + tm_s(t) + kk * 8, dv, (kk * 16 * 128) >> 4, idesc_pv, it > 0 || kk > 0);
+        mma_commit_w(bar.o_done(t));
+        if (it >= w.hi[t ^ 1] || t == 1) mma_commit_w(bar.v_empty(j % NST));  // the last reader of V_j
       };
       bool ok = true;
       for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x, ++nq) {
         const Item w = decode_item(p, plan, item);
-        ok = mbar_wait2(bar.q_full(0), nq & 1, bar.q_full(1), nq & 1, wc);
+        ok = warp_wait2(bar.q_full(0), nq & 1, bar.q_full(1), nq & 1, wc);
         if (!ok) break;
         tc_fence_after();
         for (int t = 0; t < 2; ++t)
-          if (w.hi[t] == 0) mma_commit(bar.q_empty(t));  // no product of this item reads Q_t
+          if (w.hi[t] == 0) mma_commit_w(bar.q_empty(t));  // no product of this item reads Q_t
         if (w.ntiles > 0) {
-          ok = mbar_wait(bar.k_full(j0 % NST), (j0 / NST) & 1, wc);
+          ok = warp_wait(bar.k_full(j0 % NST), (j0 / NST) & 1, wc);
           if (!ok) break;
           tc_fence_after();
           for (int t = 0; t < 2; ++t)
@@ -358,14 +359,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int t = 0; t < 2; ++t) {
             if (!ok || it >= w.hi[t]) continue;
             const uint32_t pp = (cnt[t] + it) & 1;
-            ok = v_in ? mbar_wait(bar.p_full(t), pp, wc)
-                      : mbar_wait2(bar.v_full(j % NST), (j / NST) & 1, bar.p_full(t), pp, wc);
+            ok = v_in ? warp_wait(bar.p_full(t), pp, wc)
+                      : warp_wait2(bar.v_full(j % NST), (j / NST) & 1, bar.p_full(t), pp, wc);
             if (!ok) break;
             v_in = true;
             tc_fence_after();
             issue_pv(w, t, it);
             if (it + 1 < w.hi[t]) {
-              if (!k_in && !mbar_wait(bar.k_full((j + 1) % NST), ((j + 1) / NST) & 1, wc)) {
+              if (!k_in && !warp_wait(bar.k_full((j + 1) % NST), ((j + 1) / NST) & 1, wc)) {
                 ok = false;
                 break;
               }
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         j0 += w.ntiles;
       }
       // every MMA this thread issued must finish before tensor memory is freed
-      mma_commit(bar.drain());
+      mma_commit_w(bar.drain());
       WaitCtl drain{nullptr, nullptr, wc.limit_ns};
       mbar_wait(bar.drain(), 0, drain);
     }
@@ -395,9 +396,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl = p.scale * 1.4426950408889634f;
     bool ok = true;
     int n = 0;  // key tiles this warpgroup has processed (all items)
-    auto warp_wait = [&](uint32_t bar_addr, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, mbar_wait(bar_addr, parity, wc));
-    };
     for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
       const Item w = decode_item(p, plan, item);
       const Tile x = w.tile[t];
@@ -408,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // error of each tile's largest P, which O's normaliser adds (below)
       float m_ref = -INFINITY, l = 0.f, lc = 0.f;
       for (int it = 0; it < w.hi[t]; ++it, ++n) {
-        if (!warp_wait(bar.s_full(t), n & 1)) {
+        if (!warp_wait(bar.s_full(t), n & 1, wc)) {
           ok = false;
           break;
         }
@@ -466,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // completed: the only one that can be outstanding (S_it was issued
         // after P_{it-1} V_{it-1}, and P_it is not yet published)
         if (it > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          if (!warp_wait(bar.o_done(t), (n - 1) & 1)) {
+          if (!warp_wait(bar.o_done(t), (n - 1) & 1, wc)) {
             tmem_wait_st();
             ok = false;
             break;
@@ -495,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ------------------------------------------------------------ output
-      if (w.hi[t] > 0 && !warp_wait(bar.o_done(t), (n - 1) & 1)) {
+      if (w.hi[t] > 0 && !warp_wait(bar.o_done(t), (n - 1) & 1, wc)) {
         ok = false;
         break;
       }

@@ -23,25 +23,61 @@ __device__ __forceinline__ Desc2 desc_sw128(uint32_t saddr, uint32_t lbo_bytes, 
   const uint64_t d = sdesc_sw128(saddr, lbo_bytes, sbo_bytes);
   return Desc2{static_cast<uint32_t>(d), static_cast<uint32_t>(d >> 32)};
 }
-__device__ __forceinline__ void mma_ss2(uint32_t d_tmem, Desc2 a, uint32_t a_off, Desc2 b, uint32_t b_off,
-                                        uint32_t idesc, uint32_t acc) {
+// tcgen05 instructions for a whole converged warp: every lane runs the code
+// around them, one elected lane (always the same) issues.  Kept converged, the
+// descriptors live in uniform registers; issued from one lane of a diverged
+// warp they are moved there for every instruction.  Measured, cycles a
+// product, back to back: diverged 46 or more at any size (80-120 with the
+// descriptor arithmetic of a real loop); converged 24 at M = 64 N = 16, 32 at
+// M = 64 N = 64, 48 at M = 128 N = 64, 64 at M = N = 128: the operands' bytes
+// over 128 a cycle, or M N 16 / 4096.
+__device__ __forceinline__ void mma_ss_w(uint32_t d_tmem, Desc2 a, uint32_t a_off, Desc2 b, uint32_t b_off,
+                                         uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 da, db;\n"
+      "{\n.reg .pred p, e;\n.reg .b64 da, db;\n"
+      "elect.sync _|e, 0xffffffff;\n"
       "mov.b64 da, {%1, %2};\nmov.b64 db, {%3, %4};\n"
       "setp.ne.b32 p, %6, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n}\n" ::"r"(d_tmem),
       "r"(a.lo + a_off), "r"(a.hi), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts2(uint32_t d_tmem, uint32_t a_tmem, Desc2 b, uint32_t b_off, uint32_t idesc,
-                                        uint32_t acc) {
+__device__ __forceinline__ void mma_ts_w(uint32_t d_tmem, uint32_t a_tmem, Desc2 b, uint32_t b_off, uint32_t idesc,
+                                         uint32_t acc) {
   asm volatile(
-      "{\n.reg .pred p;\n.reg .b64 db;\n"
+      "{\n.reg .pred p, e;\n.reg .b64 db;\n"
+      "elect.sync _|e, 0xffffffff;\n"
       "mov.b64 db, {%2, %3};\n"
       "setp.ne.b32 p, %5, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d_tmem),
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "r"(acc)
       : "memory");
+}
+__device__ __forceinline__ void mma_commit_w(uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar)
+      : "memory");
+}
+// Waits by a whole warp; the answer is the same in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, w));
+}
+__device__ __forceinline__ bool warp_wait2(uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2, const WaitCtl& w) {
+  return __all_sync(0xffffffffu, mbar_wait2(b1, p1, b2, p2, w));
+}
+// Whether a phase has completed, without waiting.
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\n"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, ok != 0);
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
