@@ -325,6 +325,10 @@ def fa_bwd_latent_workspace_bytes(B: int, H: int, Nq: int, Nk: int, dn: int, dr:
     return lib.fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dv)
 
 
+def _at(t):
+    return 0 if t is None else t.data_ptr()
+
+
 def _need(name, t, shape, dtype, device):
     if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {device}, "
@@ -344,16 +348,29 @@ def _first(name, t, dims):
     return code
 
 
-@contextlib.contextmanager
-def _running_on(device, stream):
+class _running_on:
     """The tensors' device made current, and the call's stream on it: the given
-    one, or that device's current stream.  Tensors a call allocates are
-    allocated on that stream (see _alloc_on)."""
-    torch = _torch()
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-    with torch.cuda.device(device), _alloc_on(stream):
-        yield ctypes.c_void_p((torch.cuda.current_stream(device) if stream is None else stream).cuda_stream)
+    one, or that device's current stream; entering gives the stream's handle.
+    Tensors a call allocates are allocated on that stream (see _alloc_on).  When
+    both are current already, entering touches neither (4 us a call)."""
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+        self.device, self.stream, self.stack = device, stream, None
+
+    def __enter__(self):
+        torch = _torch()
+        if self.stream is None and torch.cuda.current_device() == self.device.index:
+            return torch.cuda.current_stream().cuda_stream
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(self.device))
+        self.stack.enter_context(_alloc_on(self.stream))
+        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
 
 
 def _workspace(workspace, need, device):
@@ -398,8 +415,8 @@ def fa_fwd_shared_prefix(q, k_prefix, v_prefix, k, v, lens, scale: float | None 
         elif want_lse:
             lse = torch.empty((B, Hq, Nq), device=dev, dtype=torch.float32)
         ws = _workspace(workspace, lib.fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d), dev)
-        st = lib.fa_fwd_shared_prefix(_ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(k), _ptr(v), _ptr(lens), _ptr(o),
-                                      _ptr(lse), B, Hq, Hkv, Nq, Np, Ns, d, float(scale), code, _ptr(ws),
+        st = lib.fa_fwd_shared_prefix(_at(q), _at(k_prefix), _at(v_prefix), _at(k), _at(v), _at(lens), _at(o),
+                                      _at(lse), B, Hq, Hkv, Nq, Np, Ns, d, float(scale), code, _at(ws),
                                       ws.numel() * ws.element_size(), sp)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_shared_prefix")
@@ -443,8 +460,8 @@ def fa_fwd_latent_absorbed(q, cache, lens, dc: int, scale: float, block_table=No
         elif want_lse:
             lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
         ws = _workspace(workspace, lib.fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc), dev)
-        st = lib.fa_fwd_latent_absorbed(_ptr(q), _ptr(cache), _ptr(block_table), _ptr(lens), _ptr(o), _ptr(lse), B, H,
-                                        Nq, pages, page_size, max_pages, dc, dr, float(scale), code, _ptr(ws),
+        st = lib.fa_fwd_latent_absorbed(_at(q), _at(cache), _at(block_table), _at(lens), _at(o), _at(lse), B, H,
+                                        Nq, pages, page_size, max_pages, dc, dr, float(scale), code, _at(ws),
                                         ws.numel() * ws.element_size(), sp)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_latent_absorbed")
@@ -487,7 +504,7 @@ def fa_fwd_latent(q, k_nope, k_rope, v, scale: float | None = None, causal: bool
             _need("lse", lse, (B, H, Nq), torch.float32, dev)
         elif want_lse:
             lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
-        st = lib.fa_fwd_latent(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), B, H, Nq, Nk, dn, dr,
+        st = lib.fa_fwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), B, H, Nq, Nk, dn, dr,
                                dv, float(scale), int(bool(causal)), code, sp)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_latent")
@@ -513,9 +530,9 @@ def fa_bwd_latent(q, k_nope, k_rope, v, o, lse, do, scale: float | None = None, 
                                     for name, g, t in (("dq", dq, q), ("dk_nope", dk_nope, k_nope),
                                                        ("dk_rope", dk_rope, k_rope), ("dv", dv, v)))
         ws = _workspace(workspace, lib.fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dvw), dev)
-        st = lib.fa_bwd_latent(_ptr(q), _ptr(k_nope), _ptr(k_rope), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), _ptr(dq),
-                               _ptr(dk_nope), _ptr(dk_rope), _ptr(dv), B, H, Nq, Nk, dn, dr, dvw, float(scale),
-                               int(bool(causal)), code, _ptr(ws), ws.numel() * ws.element_size(), sp)
+        st = lib.fa_bwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), _at(do), _at(dq),
+                               _at(dk_nope), _at(dk_rope), _at(dv), B, H, Nq, Nk, dn, dr, dvw, float(scale),
+                               int(bool(causal)), code, _at(ws), ws.numel() * ws.element_size(), sp)
     if st != FA_OK:
         raise FaError(st, "fa_bwd_latent")
     return dq, dk_nope, dk_rope, dv

@@ -34,11 +34,11 @@ __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162flo
 __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-template <typename T>
-__global__ void __launch_bounds__(128) fa_latent_bwd_prep_kernel(const T* __restrict__ o, const T* __restrict__ dO,
-                                                                 const float* __restrict__ lse,
-                                                                 float* __restrict__ lse2, float* __restrict__ dsum,
-                                                                 long long rows, int Nq, int npad, int dv) {
+__global__ void __launch_bounds__(128) fa_latent_bwd_prep_f32_kernel(const float* __restrict__ o,
+                                                                     const float* __restrict__ dO,
+                                                                     const float* __restrict__ lse,
+                                                                     float* __restrict__ lse2, float* __restrict__ dsum,
+                                                                     long long rows, int Nq, int npad, int dv) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long prow = static_cast<long long>(blockIdx.x) * 4 + warp;
   if (prow >= rows) return;
@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(128) fa_latent_bwd_prep_kernel(const T* __rest
   float acc = 0.f, l2 = -INFINITY;
   if (i < Nq) {
     const long long src = (bh * Nq + i) * dv;
-    for (int c = lane; c < dv; c += 32) acc = fmaf(to_f32(o[src + c]), to_f32(dO[src + c]), acc);
+    for (int c = lane; c < dv; c += 32) acc = fmaf(o[src + c], dO[src + c], acc);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
     const float l = lse[bh * Nq + i];
@@ -56,6 +56,53 @@ __global__ void __launch_bounds__(128) fa_latent_bwd_prep_kernel(const T* __rest
   if (lane == 0) {
     lse2[prow] = l2;
     dsum[prow] = i < Nq ? -acc : 0.f;
+  }
+}
+
+// bf16, dv = 128: sixteen lanes a row (16 bytes of O and dO each), two rows a
+// pass, four passes a warp with all their loads in flight; a warp's eight rows
+// lie in one padded head (128 divides npad).
+__global__ void __launch_bounds__(256)
+    fa_latent_bwd_prep_bf16_kernel(const __nv_bfloat16* __restrict__ o, const __nv_bfloat16* __restrict__ dO,
+                                   const float* __restrict__ lse, float* __restrict__ lse2, float* __restrict__ dsum,
+                                   long long rows, int Nq, int npad) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long base = (static_cast<long long>(blockIdx.x) * 8 + warp) * 8;
+  if (base >= rows) return;
+  const long long bh = base / npad;
+  const int i0 = static_cast<int>(base % npad), c = lane & 15, sub = lane >> 4;
+  uint4 ov[4], gv[4];
+  float lv[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int i = i0 + 2 * u + sub;
+    ov[u] = gv[u] = make_uint4(0u, 0u, 0u, 0u);
+    lv[u] = -INFINITY;
+    if (i < Nq) {
+      const long long src = (bh * Nq + i) * 128 + 8 * c;
+      ov[u] = __ldg(reinterpret_cast<const uint4*>(o + src));
+      gv[u] = __ldg(reinterpret_cast<const uint4*>(dO + src));
+      lv[u] = __ldg(lse + bh * Nq + i);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const __nv_bfloat162* op = reinterpret_cast<const __nv_bfloat162*>(&ov[u]);
+    const __nv_bfloat162* gp = reinterpret_cast<const __nv_bfloat162*>(&gv[u]);
+    float acc = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = __bfloat1622float2(op[e]), b = __bfloat1622float2(gp[e]);
+      acc = fmaf(a.x, b.x, acc);
+      acc = fmaf(a.y, b.y, acc);
+    }
+#pragma unroll
+    for (int x = 8; x > 0; x >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, x);
+    if (c == 0) {
+      const long long prow = base + 2 * u + sub;
+      lse2[prow] = lv[u] == -INFINITY ? -INFINITY : -lv[u] * 1.4426950408889634f;  // no key seen: P = 2^(x - inf) = 0
+      dsum[prow] = -acc;
+    }
   }
 }
 
@@ -374,15 +421,13 @@ cudaError_t launch_latent_bwd_prep(const LatentBwd& p, fa_dtype dt, cudaStream_t
   const int npad = (p.Nq + 127) / 128 * 128;
   const long long rows = static_cast<long long>(p.B) * p.H * npad;
   if (rows / 4 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const unsigned blocks = static_cast<unsigned>(rows / 4);
   if (dt == FA_DTYPE_F32)
-    fa_latent_bwd_prep_kernel<float><<<blocks, 128, 0, s>>>(static_cast<const float*>(p.o),
-                                                            static_cast<const float*>(p.dO), p.lse, p.lse2, p.dsum,
-                                                            rows, p.Nq, npad, p.dv);
+    fa_latent_bwd_prep_f32_kernel<<<static_cast<unsigned>(rows / 4), 128, 0, s>>>(
+        static_cast<const float*>(p.o), static_cast<const float*>(p.dO), p.lse, p.lse2, p.dsum, rows, p.Nq, npad, p.dv);
   else
-    fa_latent_bwd_prep_kernel<__nv_bfloat16><<<blocks, 128, 0, s>>>(
+    fa_latent_bwd_prep_bf16_kernel<<<static_cast<unsigned>(rows / 64), 256, 0, s>>>(
         static_cast<const __nv_bfloat16*>(p.o), static_cast<const __nv_bfloat16*>(p.dO), p.lse, p.lse2, p.dsum, rows,
-        p.Nq, npad, p.dv);
+        p.Nq, npad);
   return cudaGetLastError();
 }
 

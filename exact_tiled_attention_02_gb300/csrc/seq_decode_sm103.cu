@@ -313,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
 
   if (warp == 5) {
     // ------------------------------------------------------------------ TMA
-    // The whole warp walks; lane i < boxes issues the loads of box i of a tile
-    // (64 tokens, or fewer where pages are not whole tiles).
+    // The whole warp walks, converged; a tile is one box of 64 tokens, or 2 or 4
+    // where pages are not whole tiles.  Lane i looks box i's page up.
     const int box = plan.box, per = BC / box;
     int g = 0, nq = 0;  // tiles and pieces issued
     int ms = 0, xs = 0;            // next slots of the rings, and the parity their release completes
@@ -323,10 +323,8 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
     pieces([&](int b, int nk, int t0, int n) -> bool {
       const int group = b * plan.heads + head;
       if (nq > 0 && !wait(bar.q_free(), (nq - 1) & 1)) return false;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(bar.q_full(), C::Q_BYTES);
-        for (int c = 0; c < C::QC; ++c) tma_load_3d(sQ + c * NR * 128, &maps.q, bar.q_full(), c * 64, r0, group);
-      }
+      mbar_arrive_expect_tx_w(bar.q_full(), C::Q_BYTES);
+      for (int c = 0; c < C::QC; ++c) tma_load_3d_w(sQ + c * NR * 128, &maps.q, bar.q_full(), c * 64, r0, group);
       ++nq;
       // this lane's box of a tile: token within its page, page (as the table has it)
       auto place = [&](int tile, int& tok, int& page) {
@@ -352,17 +350,23 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
           atomicOr(p.status, kStatusInput);
           page = p.n_pages;  // outside the cache: reads as zeros
         }
+        int box_tok[4], box_page[4];  // the boxes' places, in every lane
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          box_tok[k] = __shfl_sync(0xffffffffu, tok, k);
+          box_page[k] = __shfl_sync(0xffffffffu, page, k);
+        }
         auto load_x = [&]() -> bool {
           if (!wait(bar.x_free(xs), xp)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(bar.x_full(xs), boxes * box * 128 * XC);
-          __syncwarp();
-          if (lane < boxes) {
+          mbar_arrive_expect_tx_w(bar.x_full(xs), boxes * box * 128 * XC);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= boxes) break;
 #pragma unroll
             for (int c = 0; c < XC; ++c)
-              tma_load_3d(sX + xs * C::X_BYTES + c * CB + lane * box * 128, &maps.x, bar.x_full(xs),
-                          (SHARED ? DM : 0) + c * 64, tok, page);
+              tma_load_3d_w(sX + xs * C::X_BYTES + c * CB + i * box * 128, &maps.x, bar.x_full(xs),
+                            (SHARED ? DM : 0) + c * 64, box_tok[i], box_page[i]);
           }
-          __syncwarp();
           if (++xs == NX) {
             xs = 0;
             xp ^= 1;
@@ -372,15 +376,15 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
         if (!SHARED && !load_x()) return false;
         for (int u = 0; u < UM; ++u) {
           if (!wait(bar.m_free(ms), mp)) return false;
-          if (lane == 0) mbar_arrive_expect_tx(bar.m_full(ms), boxes * box * 128 * UC);
-          __syncwarp();
-          if (lane < boxes) {
+          mbar_arrive_expect_tx_w(bar.m_full(ms), boxes * box * 128 * UC);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= boxes) break;
 #pragma unroll
             for (int c = 0; c < UC; ++c)
-              tma_load_3d(sM + ms * C::M_BYTES + c * CB + lane * box * 128, &maps.m, bar.m_full(ms), (u * UC + c) * 64,
-                          tok, page);
+              tma_load_3d_w(sM + ms * C::M_BYTES + c * CB + i * box * 128, &maps.m, bar.m_full(ms), (u * UC + c) * 64,
+                            box_tok[i], box_page[i]);
           }
-          __syncwarp();
           if (++ms == NM) {
             ms = 0;
             mp ^= 1;
