@@ -31,9 +31,10 @@
 // asked for that, others as fp32 partial results that a second kernel merges
 // in a fixed order.
 //
-// 192 threads: warps 0-3 softmax (a 64-row accumulator occupies lanes 0-15 of
-// each warp's quarter of tensor memory: lane l < 16 of warp w holds key 16 w +
-// l), warp 4 MMA issuer and TMEM owner, warp 5 TMA producer.
+// 320 threads: warps 0-7 softmax (a 64-row accumulator occupies lanes 0-15 of
+// each quarter of tensor memory, so key 16 w + l is in lane l < 16 of warps w
+// and w + 4; warps 0-3 take the first half of the columns, 4-7 the second),
+// warp 8 MMA issuer and TMEM owner, warp 9 TMA producer.
 // Shared memory: Q, P, a ring of M units (64 tokens x 128 dimensions; shared
 // form: key and value, otherwise values) and one of X units (shared form: the
 // rotary part; otherwise keys).
@@ -48,7 +49,8 @@ using namespace seq;
 
 constexpr int BC = 64;            // keys per tile
 constexpr int CB = BC * 128;      // bytes of a chunk: 64 tokens x 64 entries
-constexpr int kThreads = 192;
+constexpr int kSoftmax = 256;    // threads of warps 0-7
+constexpr int kThreads = 320;
 constexpr float kUnset = 3e38f;   // negated reference of a row that has seen no key
 constexpr float kRescaleThreshold = 8.0f;
 
@@ -240,18 +242,18 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
     mbar_init(bar.q_free(), 1);
     mbar_init(bar.s_full(0), 1);
     mbar_init(bar.s_full(1), 1);
-    mbar_init(bar.p_full(), 4);
+    mbar_init(bar.p_full(), 8);
     mbar_init(bar.o_done(), 1);
     mbar_init(bar.drain(), 1);
     *abort_flag = 0;
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 4) {
+  if (warp == 8) {
     tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
     tmem_relinquish();
   }
-  if (warp == 5) {
+  if (warp == 9) {
     // where this CTA's range of the tiles, laid end to end, begins
     long long before, total;
     tile_sums(p, plan.n_seq, 0, before, total);
@@ -311,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
     }
   };
 
-  if (warp == 5) {
+  if (warp == 9) {
     // ------------------------------------------------------------------ TMA
     // The whole warp walks, converged; a tile is one box of 64 tokens, or 2 or 4
     // where pages are not whole tiles.  Lane i looks box i's page up.
@@ -405,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
       for (int k = max(0, g + 1 - NX); k < g + 1; ++k) mbar_wait(bar.x_full(k % NX), (k / NX) & 1, drain);
     }
     __syncwarp();
-  } else if (warp == 4) {
+  } else if (warp == 8) {
     // ------------------------------------------------------------------ MMA
     // The whole warp runs it, converged (see mma_ss_w).  Two streams of work:
     // S^T of tile after tile, a ring unit at a time as its loads land, at most
@@ -510,31 +512,31 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
     __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
-    // Tensor memory hands the scores of key 16 w + l to lane l < 16 of warp w;
-    // lane l + 16 takes half of them over (columns NR / 2 ..), so that every
-    // lane has NH columns of one key.
-    constexpr int NH = NR / 2;
-    constexpr int LW = NR < 32 ? 16 : 32;  // columns per tensor-memory access
-    const uint32_t tl = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    const int key = warp * 16 + (lane & 15), col = lane < 16 ? 0 : NH;
+    // Tensor memory hands a key's scores to a lane below 16; lane + 16 takes
+    // half of its warp's columns over, so that every lane has NH = NR / 4
+    // columns of one key.
+    // Once a wait has run out, waits return at once and the loops run on to
+    // their ends (barriers count every warp); nothing is written out then.
+    constexpr int NH = NR / 4;
+    constexpr int LW = NR / 2 < 32 ? NR / 2 : 32;  // columns per tensor-memory access
+    constexpr int OC = UM * NR / 2;                // columns of O that a warp handles
+    const int wg = warp >> 2, quarter = warp & 3;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int key = quarter * 16 + (lane & 15), col = wg * (NR / 2) + (lane < 16 ? 0 : NH);
     const float sl = p.scale * 1.4426950408889634f;
     // P is [row][64 keys], 128-byte rows, 16-byte chunks swizzled by row % 8.
     // Lanes of an even and an odd key pair up: the even one writes both keys'
     // P of an even column, the odd one those of the column after it.
     const int odd = lane & 1;
-    uint32_t p_at[4];
+    constexpr int PA = NH / 2 < 4 ? NH / 2 : 4;
+    uint32_t p_at[PA];
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      p_at[q] = sP + (col + 2 * q + odd) * 128 + (((key >> 3) ^ (2 * q + odd)) << 4) + (key & 6) * 2;
-    const int my_col = col + reduce_col<NH>();  // first column this lane owns after reduce16
-    constexpr int OWN = NH >= 16 ? NH / 16 : 1;
+    for (int q = 0; q < PA; ++q) {
+      const int row = col + 2 * q + odd;
+      p_at[q] = sP + row * 128 + (((key >> 3) ^ (row & 7)) << 4) + (key & 6) * 2;
+    }
+    const int my_col = col + reduce_col<NH>();  // the column this lane owns after reduce16
     int g = 0;
-    bool ok = true;
-    // all four warps give up together: a barrier's count must be met on every path
-    auto wait_all = [&](uint32_t bar_addr, uint32_t parity) -> bool {
-      ok = !bar_any(1, 128, !warp_wait(bar_addr, parity, wc));
-      return ok;
-    };
 
     pieces([&](int b, int nk, int t0, int n) -> bool {
       const int group = b * plan.heads + head;
@@ -542,19 +544,14 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
 #pragma unroll
       for (int c = 0; c < NH; ++c) l[c] = lr[c] = 0.f;
       if (threadIdx.x < NR) s_nref[threadIdx.x] = kUnset;
-      named_bar_sync(1, 128);
+      named_bar_sync(1, kSoftmax);
       for (int i = 0; i < n; ++i, ++g) {
-        if (!wait_all(bar.s_full(g & 1), (g >> 1) & 1)) return false;
+        warp_wait(bar.s_full(g & 1), (g >> 1) & 1, wc);
         tc_fence_after();
         float s[NH];
         {
-          uint32_t r[NR];
-#pragma unroll
-          for (int c = 0; c < NR; c += LW)
-            if constexpr (LW == 16)
-              tmem_ld_32x32b_x16(tl + C::TM_S + NR * (g & 1) + c, r + c);
-            else
-              tmem_ld_32x32b_x32(tl + C::TM_S + NR * (g & 1) + c, r + c);
+          uint32_t r[2 * NH];
+          tmem_ld<2 * NH>(tl + C::TM_S + NR * (g & 1) + wg * (NR / 2), r);
           tmem_wait_ld();
 #pragma unroll
           for (int c = 0; c < NH; ++c) {
@@ -571,9 +568,9 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
         // values past the sequence's end multiply zero probabilities: they must be finite
         const int valid = min(BC, nk - j0);
         if (valid < BC) {
-          if (!SHARED && !wait_all(bar.m_full(g % NM), (g / NM) & 1)) return false;
+          if (!SHARED) warp_wait(bar.m_full(g % NM), (g / NM) & 1, wc);
           const int rows = BC - valid;
-          for (int x = threadIdx.x; x < rows * UM * UC * 8; x += 128) {
+          for (int x = threadIdx.x; x < rows * UM * UC * 8; x += kSoftmax) {
             const int row = valid + x / (UM * UC * 8), y = x % (UM * UC * 8);
             const int u = y / (UC * 8), z = y % (UC * 8);
             st_shared_v4(sM + ((g * UM + u) % NM) * C::M_BYTES + (z >> 3) * CB + row * 128 + (z & 7) * 16, 0u, 0u, 0u, 0u);
@@ -587,17 +584,16 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
           over = fmax3(over, fmaf(s[c], sl, nr.x), fmaf(s[c + 1], sl, nr.y));
           over = fmax3(over, fmaf(s[c + 2], sl, nr.z), fmaf(s[c + 3], sl, nr.w));
         }
-        if (bar_any(1, 128, over > kRescaleThreshold)) {
+        if (bar_any(1, kSoftmax, over > kRescaleThreshold)) {
           // some row's reference rises: column maxima over the 64 keys
           {
             float v[NH];
 #pragma unroll
             for (int c = 0; c < NH; ++c) v[c] = s[c] * sl;
             reduce16<NH>(v, [](float x, float y) { return fmaxf(x, y); });
-#pragma unroll
-            for (int e = 0; e < OWN; ++e) s_red[warp * NR + my_col + e] = v[e];
+            s_red[quarter * NR + my_col] = v[0];
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1, kSoftmax);
           if (threadIdx.x < NR) {
             const int c = threadIdx.x;
             const float mx = fmaxf(fmaxf(s_red[c], s_red[NR + c]), fmaxf(s_red[2 * NR + c], s_red[3 * NR + c]));
@@ -609,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
             }
             s_alpha[c] = alpha;
           }
-          named_bar_sync(1, 128);
+          named_bar_sync(1, kSoftmax);
 #pragma unroll
           for (int c = 0; c < NH; ++c) {
             const float a = s_alpha[col + c];
@@ -617,22 +613,16 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
             lr[c] *= a;
           }
           if (i > 0) {
-            if (!wait_all(bar.o_done(), (g - 1) & 1)) return false;
+            warp_wait(bar.o_done(), (g - 1) & 1, wc);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < UM * NR; c += LW) {
+            for (int c = wg * OC; c < (wg + 1) * OC; c += LW) {
               uint32_t o[LW];
-              if constexpr (LW == 16)
-                tmem_ld_32x32b_x16(tl + c, o);
-              else
-                tmem_ld_32x32b_x32(tl + c, o);
+              tmem_ld<LW>(tl + c, o);
               tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < LW; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * s_alpha[c % NR + e]);
-              if constexpr (LW == 16)
-                tmem_st_32x32b_x16(tl + c, o);
-              else
-                tmem_st_32x32b_x32(tl + c, o);
+              tmem_st<LW>(tl + c, o);
             }
             tmem_wait_st();
           }
@@ -657,58 +647,54 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
           pk[c / 2 + 1] = odd ? __byte_perm(yb, bq, 0x7632) : __byte_perm(bq, yb, 0x5410);
         }
         // P_{g-1} has been read once its P V has completed
-        if (g > 0 && !wait_all(bar.o_done(), (g - 1) & 1)) return false;
+        if (g > 0) warp_wait(bar.o_done(), (g - 1) & 1, wc);
 #pragma unroll
         for (int c = 0; c < NH / 2; ++c)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_at[c & 3] + (c >> 2) * 1024), "r"(pk[c]) : "memory");
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(p_at[c % PA] + (c / PA) * 1024), "r"(pk[c]) : "memory");
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar.p_full());
       }
       // ------------------------------------------------------------ output
-      float ref = 0.f, sum = 0.f, sum_r = 0.f;  // of row threadIdx.x
+      float ref = 0.f, sum = 0.f;  // of row threadIdx.x
       reduce16<NH>(l, [](float x, float y) { return x + y; });
       reduce16<NH>(lr, [](float x, float y) { return x + y; });
-#pragma unroll
-      for (int e = 0; e < OWN; ++e) s_red[warp * NR + my_col + e] = l[e];
-      named_bar_sync(1, 128);
+      s_red[quarter * NR + my_col] = l[0];
+      named_bar_sync(1, kSoftmax);
       if (threadIdx.x < NR) {
         const int c = threadIdx.x;
         sum = (s_red[c] + s_red[NR + c]) + (s_red[2 * NR + c] + s_red[3 * NR + c]);
         ref = s_nref[c] == kUnset ? 0.f : -s_nref[c];
       }
-      named_bar_sync(1, 128);
-#pragma unroll
-      for (int e = 0; e < OWN; ++e) s_red[warp * NR + my_col + e] = lr[e];
-      named_bar_sync(1, 128);
+      named_bar_sync(1, kSoftmax);
+      s_red[quarter * NR + my_col] = lr[0];
+      named_bar_sync(1, kSoftmax);
       const bool whole = plan.direct && t0 == 0 && n == tiles_of(nk);
       const long long slot = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + cut + b;
       const long long orow0 = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r0;
       if (threadIdx.x < NR) {
         const int c = threadIdx.x;
-        sum_r = (s_red[c] + s_red[NR + c]) + (s_red[2 * NR + c] + s_red[3 * NR + c]);
+        const float sum_r = (s_red[c] + s_red[NR + c]) + (s_red[2 * NR + c] + s_red[3 * NR + c]);
         s_alpha[c] = sum_r == 0.f ? 0.f : 1.f / sum_r;
         const float lse = (ref + __log2f(sum)) * 0.69314718055994531f;  // -inf where no key was seen
-        if (c < n_rows) {
+        if (c < n_rows && !*abort_flag) {
           if (!whole)
             p.part_lse[slot * NR + c] = lse;
           else if (p.lse != nullptr)
             p.lse[orow0 + c] = lse;
         }
       }
-      if (!wait_all(bar.o_done(), (g - 1) & 1)) return false;  // also orders s_alpha
+      named_bar_sync(1, kSoftmax);
+      warp_wait(bar.o_done(), (g - 1) & 1, wc);
       tc_fence_after();
-      const int d0 = C::UDIM == 128 ? warp * 32 + lane : warp * 16 + lane;  // this lane's dimension of an M unit
+      const int d0 = C::UDIM == 128 ? quarter * 32 + lane : quarter * 16 + lane;  // this lane's dimension of an M unit
       const bool has_dim = (C::UDIM == 128 || lane < 16) && d0 < DV;
 #pragma unroll 1
-      for (int c = 0; c < UM * NR; c += LW) {
+      for (int c = wg * OC; c < (wg + 1) * OC; c += LW) {
         if (c % NR >= n_rows) continue;
         uint32_t o[LW];
-        if constexpr (LW == 16)
-          tmem_ld_32x32b_x16(tl + c, o);
-        else
-          tmem_ld_32x32b_x32(tl + c, o);
+        tmem_ld<LW>(tl + c, o);
         tmem_wait_ld();
         const int d = (c / NR) * 128 + d0, row = c % NR;
         if (!has_dim || *abort_flag) continue;
@@ -724,14 +710,14 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
         }
       }
       tc_fence_before();
-      named_bar_sync(1, 128);  // the statistics are free for the next piece
+      named_bar_sync(1, kSoftmax);  // the statistics are free for the next piece
       return true;
     });
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }

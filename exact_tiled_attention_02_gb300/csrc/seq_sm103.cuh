@@ -118,6 +118,39 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t* r) 
       : "r"(taddr));
 }
 
+// 32 lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// 8, 16 or 32 columns.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns of one access");
+  if constexpr (N == 8)
+    tmem_ld_32x32b_x8(taddr, r);
+  else if constexpr (N == 16)
+    tmem_ld_32x32b_x16(taddr, r);
+  else
+    tmem_ld_32x32b_x32(taddr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns of one access");
+  if constexpr (N == 8)
+    tmem_st_32x32b_x8(taddr, r);
+  else if constexpr (N == 16)
+    tmem_st_32x32b_x16(taddr, r);
+  else
+    tmem_st_32x32b_x32(taddr, r);
+}
+
 // A bf16 map of up to four dimensions, innermost first (dims[0] contiguous),
 // rows packed; box of 64 columns, 128-byte swizzle, zeros outside.
 inline bool make_map(CUtensorMap* m, const void* base, int rank, const long long* dims, const int* box) {
