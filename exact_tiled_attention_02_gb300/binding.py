@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -313,14 +314,17 @@ def fa_bwd_static_workspace(q, k, v, o, lse, do, dq, dk, dv, scale: float | None
     return dq, dk, dv
 
 
+@functools.lru_cache(maxsize=256)
 def fa_fwd_shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Np: int, Ns: int, d: int) -> int:
     return lib.fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d)
 
 
+@functools.lru_cache(maxsize=256)
 def fa_fwd_latent_absorbed_workspace_bytes(B: int, H: int, Nq: int, page_size: int, max_pages: int, dc: int) -> int:
     return lib.fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc)
 
 
+@functools.lru_cache(maxsize=256)
 def fa_bwd_latent_workspace_bytes(B: int, H: int, Nq: int, Nk: int, dn: int, dr: int, dv: int) -> int:
     return lib.fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dv)
 
@@ -348,6 +352,13 @@ def _first(name, t, dims):
     return code
 
 
+def _raw_stream(index):
+    """The handle of the device's current stream."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 2 us less than building a Stream object
+    return torch.cuda.current_stream(index).cuda_stream if get is None else get(index)
+
+
 class _running_on:
     """The tensors' device made current, and the call's stream on it: the given
     one, or that device's current stream; entering gives the stream's handle.
@@ -362,7 +373,7 @@ class _running_on:
     def __enter__(self):
         torch = _torch()
         if self.stream is None and torch.cuda.current_device() == self.device.index:
-            return torch.cuda.current_stream().cuda_stream
+            return _raw_stream(self.device.index)
         self.stack = contextlib.ExitStack()
         self.stack.enter_context(torch.cuda.device(self.device))
         self.stack.enter_context(_alloc_on(self.stream))
@@ -414,7 +425,7 @@ def fa_fwd_shared_prefix(q, k_prefix, v_prefix, k, v, lens, scale: float | None 
             _need("lse", lse, (B, Hq, Nq), torch.float32, dev)
         elif want_lse:
             lse = torch.empty((B, Hq, Nq), device=dev, dtype=torch.float32)
-        ws = _workspace(workspace, lib.fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d), dev)
+        ws = _workspace(workspace, fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d), dev)
         st = lib.fa_fwd_shared_prefix(_at(q), _at(k_prefix), _at(v_prefix), _at(k), _at(v), _at(lens), _at(o),
                                       _at(lse), B, Hq, Hkv, Nq, Np, Ns, d, float(scale), code, _at(ws),
                                       ws.numel() * ws.element_size(), sp)
@@ -459,7 +470,7 @@ def fa_fwd_latent_absorbed(q, cache, lens, dc: int, scale: float, block_table=No
             _need("lse", lse, (B, H, Nq), torch.float32, dev)
         elif want_lse:
             lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
-        ws = _workspace(workspace, lib.fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc), dev)
+        ws = _workspace(workspace, fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc), dev)
         st = lib.fa_fwd_latent_absorbed(_at(q), _at(cache), _at(block_table), _at(lens), _at(o), _at(lse), B, H,
                                         Nq, pages, page_size, max_pages, dc, dr, float(scale), code, _at(ws),
                                         ws.numel() * ws.element_size(), sp)
@@ -529,7 +540,7 @@ def fa_bwd_latent(q, k_nope, k_rope, v, o, lse, do, scale: float | None = None, 
         dq, dk_nope, dk_rope, dv = (torch.empty_like(t) if g is None else _need(name, g, t.shape, q.dtype, dev)
                                     for name, g, t in (("dq", dq, q), ("dk_nope", dk_nope, k_nope),
                                                        ("dk_rope", dk_rope, k_rope), ("dv", dv, v)))
-        ws = _workspace(workspace, lib.fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dvw), dev)
+        ws = _workspace(workspace, fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dvw), dev)
         st = lib.fa_bwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), _at(do), _at(dq),
                                _at(dk_nope), _at(dk_rope), _at(dv), B, H, Nq, Nk, dn, dr, dvw, float(scale),
                                int(bool(causal)), code, _at(ws), ws.numel() * ws.element_size(), sp)

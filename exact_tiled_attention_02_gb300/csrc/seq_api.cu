@@ -70,10 +70,12 @@ PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, 
   w.bytes = w.off_lse + up256(slots * 4);
   return w;
 }
+// the sequences' 64-key tiles, times the most ranges they are cut into, stay below 2^31
+bool tiles_ok(int n_seq, long long n_keys) { return n_seq * ((n_keys + 63) / 64) * 305 <= 0x7fffffffLL; }
 bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   if (Np < 0 || Ns < 0 || Hkv < 1 || Hq % Hkv != 0) return false;
   return sizes_ok(B, Hq, Nq, d) && sizes_ok(B, Hkv, Ns > 0 ? Ns : 1, d) && sizes_ok(Hkv, Np > 0 ? Np : 1, d) &&
-         static_cast<long long>(B) * Hq * Nq <= 0x7fffffffLL;
+         static_cast<long long>(B) * Hq * Nq <= 0x7fffffffLL / 8 && tiles_ok(B, Ns);
 }
 
 PartLayout absorbed_layout(int B, int H, int Nq, int n_keys, int dc) {
@@ -191,7 +193,7 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
     b.part_lse = reinterpret_cast<float*>(base + w.off_lse);
     cudaError_t e = cudaSuccess;
     if (Np > 0) e = launch_seq_rows(a, s);
-    if (e == cudaSuccess && Ns > 0) e = launch_seq_decode(b, w.plan, s);
+    if (e == cudaSuccess && Ns > 0) e = launch_seq_decode(b, w.plan, Np > 0, s);
     if (e == cudaSuccess) e = launch_seq_decode_merge(b, w.plan, a.part_o, a.part_lse, w.splits, s);
     return of(e);
   }
@@ -210,7 +212,9 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
 }
 
 size_t fa_fwd_latent_absorbed_workspace_bytes(int B, int H, int Nq, int page_size, int max_pages, int dc) {
-  if (!sizes_ok(B, H, Nq, dc) || page_size < 1 || max_pages < 1 || absorbed_keys(page_size, max_pages) < 0) return 0;
+  if (!sizes_ok(B, H, Nq, dc) || page_size < 1 || max_pages < 1 || absorbed_keys(page_size, max_pages) < 0 ||
+      !tiles_ok(B, absorbed_keys(page_size, max_pages)))
+    return 0;
   const size_t f32 = absorbed_layout(B, H, Nq, static_cast<int>(absorbed_keys(page_size, max_pages)), dc).bytes;
   const size_t bf16 = absorbed_layout_bf16(absorbed_plan(B, H, Nq, page_size, true), dc).bytes;
   return f32 > bf16 ? f32 : bf16;
@@ -225,7 +229,8 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
   if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(lse, 4)) return FA_ERR_INVALID;
   if (!sizes_ok(B, H, Nq, dc) || !sizes_ok(B, H, Nq, dr) || dc > 4096 || dr > 4096) return FA_ERR_INVALID;
   if (!sizes_ok(n_pages, page_size, dc + dr) || !sizes_ok(B, max_pages)) return FA_ERR_INVALID;
-  if (static_cast<long long>(B) * H * Nq > 0x7fffffffLL || absorbed_keys(page_size, max_pages) < 0)
+  if (static_cast<long long>(B) * H * Nq > 0x7fffffffLL / 8 || absorbed_keys(page_size, max_pages) < 0 ||
+      !tiles_ok(B, absorbed_keys(page_size, max_pages)))
     return FA_ERR_INVALID;
   if (!block_table && (max_pages != 1 || n_pages < B)) return FA_ERR_INVALID;
   if (!scale_ok(scale) || !dtype_ok(dt)) return FA_ERR_INVALID;
@@ -269,7 +274,7 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
   if (dt == FA_DTYPE_BF16) {
     const DecodePlan plan = absorbed_plan(B, H, Nq, page_size, block_table != nullptr);
     p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + absorbed_layout_bf16(plan, dc).off_lse);
-    cudaError_t e = launch_seq_decode(p, plan, s);
+    cudaError_t e = launch_seq_decode(p, plan, false, s);
     if (e == cudaSuccess) e = launch_seq_decode_merge(p, plan, nullptr, nullptr, 0, s);
     return of(e);
   }

@@ -122,33 +122,27 @@ __device__ __forceinline__ int seq_len(const SeqAttn& p, int b, bool report) {
   if (report && n != nk) atomicOr(p.status, kStatusInput);
   return nk;
 }
-__device__ __forceinline__ int tiles_of(int nk) { return (nk + BC - 1) / BC; }
+__host__ __device__ __forceinline__ int tiles_of(int nk) { return (nk + BC - 1) / BC; }
 
 // Whole warp: the sum over sequences before `b` of their tiles, and over all.
-__device__ __forceinline__ void tile_sums(const SeqAttn& p, int n_seq, int b, long long& before, long long& total) {
+// The launcher keeps totals below 2^31 / cuts (32-bit products below).
+__device__ __forceinline__ void tile_sums(const SeqAttn& p, int n_seq, int b, unsigned& before, unsigned& total) {
   const int lane = threadIdx.x & 31;
-  long long x = 0, y = 0;
+  unsigned x = 0, y = 0;
   for (int i = lane; i < n_seq; i += 32) {
-    const int t = tiles_of(seq_len(p, i, false));
+    const unsigned t = tiles_of(seq_len(p, i, false));
     y += t;
     if (i < b) x += t;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, o);
-    y += __shfl_xor_sync(0xffffffffu, y, o);
-  }
-  before = x;
-  total = y;
+  before = __reduce_add_sync(0xffffffffu, x);
+  total = __reduce_add_sync(0xffffffffu, y);
 }
 // ranges of `total` tiles that `cuts` CTAs take: none of them empty
-__device__ __forceinline__ int range_count(long long total, int cuts) {
-  return total < cuts ? static_cast<int>(total) : cuts;
-}
+__device__ __forceinline__ unsigned range_count(unsigned total, unsigned cuts) { return total < cuts ? total : cuts; }
 // first tile of range c of n
-__device__ __forceinline__ long long range_start(long long total, int c, int n) { return total * c / n; }
+__device__ __forceinline__ unsigned range_start(unsigned total, unsigned c, unsigned n) { return total * c / n; }
 // the range that holds tile x
-__device__ __forceinline__ int owner(long long total, long long x, int n) {
+__device__ __forceinline__ int owner(unsigned total, unsigned x, unsigned n) {
   return static_cast<int>(((x + 1) * n - 1) / total);
 }
 
@@ -206,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
+  pdl_launch();  // the merge waits for this kernel's end before it reads
   if (pad + C::SMEM_USED > static_cast<uint32_t>(C::SMEM_BYTES)) {
     if (threadIdx.x == 0) atomicOr(p.status, kStatusLayout);
     return;
@@ -255,28 +250,29 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
   }
   if (warp == 9) {
     // where this CTA's range of the tiles, laid end to end, begins
-    long long before, total;
+    unsigned before, total;
     tile_sums(p, plan.n_seq, 0, before, total);
-    const int ranges = range_count(total, plan.cuts);
-    const long long t0 = cut < ranges ? range_start(total, cut, ranges) : total;
-    const long long t1 = cut < ranges ? range_start(total, cut + 1, ranges) : total;
-    long long base = 0;
+    const unsigned ranges = range_count(total, plan.cuts);
+    const bool some = cut < static_cast<int>(ranges);
+    const unsigned t0 = some ? range_start(total, cut, ranges) : total;
+    const unsigned t1 = some ? range_start(total, cut + 1, ranges) : total;
+    unsigned base = 0;
     int b0 = 0, first = 0;
     bool found = false;
     for (int i0 = 0; i0 < plan.n_seq && !found; i0 += 32) {
       const int i = i0 + lane;
-      const int t = i < plan.n_seq ? tiles_of(seq_len(p, i, true)) : 0;
-      int inc = t;
+      const unsigned t = i < plan.n_seq ? tiles_of(seq_len(p, i, true)) : 0;
+      unsigned inc = t;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
       }
-      const long long end = base + inc;
+      const unsigned end = base + inc;
       const unsigned hit = __ballot_sync(0xffffffffu, end > t0);
       if (hit) {
         const int l = __ffs(hit) - 1;
-        const long long beg = __shfl_sync(0xffffffffu, end - t, l);
+        const unsigned beg = __shfl_sync(0xffffffffu, end - t, l);
         b0 = i0 + l;
         first = static_cast<int>(t0 - beg);
         found = true;
@@ -721,34 +717,40 @@ __global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
+  pdl_wait();  // the prefix's kernel runs beside this one: the merge waits for both
 }
 
 // Merges the pieces of each sequence, and the partial results [pre][total] of
 // another set of keys beside them (the prefix), row by row: see
-// seq_combine.cu for the formula.  One warp per row and 128 of its columns;
-// lane i holds the weight of part i, so that the parts' loads do not wait for
-// one another.  Rows of a sequence that was written directly are left alone.
-template <int NR>
+// seq_combine.cu for the formula.  One warp per row and W of its 128-column
+// slices (all of them where there are rows enough to fill the GPU); lane i
+// holds the weight of part i, so that the parts' loads do not wait for one
+// another.  Rows of a sequence that was written directly are left alone.
+template <int NR, int W>
 __global__ void __launch_bounds__(128)
     fa_seq_decode_merge_kernel(const __grid_constant__ SeqAttn p, const DecodePlan plan, const float* __restrict__ pre_o,
                                const float* __restrict__ pre_lse, int pre) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slices = (p.dv + 127) / 128;
-  const long long idx = static_cast<long long>(blockIdx.x) * 4 + warp;  // (sequence, head, row, slice)
-  if (idx >= static_cast<long long>(plan.n_seq) * plan.heads * p.rows * slices) return;
-  const int slice = static_cast<int>(idx % slices);
-  const int r = static_cast<int>(idx / slices % p.rows);
-  const int group = static_cast<int>(idx / slices / p.rows);
+  const unsigned slices = (p.dv + 128 * W - 1) / (128 * W);
+  const unsigned idx = blockIdx.x * 4 + warp;  // (sequence, head, row, slices)
+  const unsigned rows = p.rows;
+  const unsigned row_idx = idx / slices, slice = idx - row_idx * slices;
+  const unsigned group = row_idx / rows, r = row_idx - group * rows;
+  if (group >= static_cast<unsigned>(plan.n_seq * plan.heads)) {
+    pdl_wait();
+    return;
+  }
   const int b = group / plan.heads, head = group % plan.heads;
-  long long before, total;
+  unsigned before, total;
   tile_sums(p, plan.n_seq, b, before, total);
   const int nt = tiles_of(seq_len(p, b, true));
   int c0 = 0, n = 0;
   if (nt > 0) {
-    const int ranges = range_count(total, plan.cuts);
+    const unsigned ranges = range_count(total, plan.cuts);
     c0 = owner(total, before, ranges);
     n = owner(total, before + nt - 1, ranges) - c0 + 1;
   }
+  pdl_wait();
   if (plan.direct && n == 1) return;
   const int grp = head * plan.row_groups + r / NR;
   const long long slot0 = (static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + c0 + b) * NR + r % NR;
@@ -768,35 +770,42 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int c = slice * 128 + 4 * lane;
-  const bool on = c < p.dv;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int c = slice * 128 * W + 4 * lane;
+  float4 acc[W];
+#pragma unroll
+  for (int w = 0; w < W; ++w) acc[w] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < n; i0 += 32) {
     const float ls = i0 == 0 ? mine : (i0 + lane < n ? part_lse(i0 + lane) : -INFINITY);
-    const float w = expf(ls - ref) * inv;
+    const float wl = expf(ls - ref) * inv;
     const int k = min(32, n - i0);
 #pragma unroll 8
     for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float wi = __shfl_sync(0xffffffffu, wl, i);
       const int part = i0 + i;
-      const float* src = part < pre ? pre_o + (part * p.total + row) * p.dv
-                                    : p.part_o + (slot0 + static_cast<long long>(part - pre) * NR) * p.dv;
-      if (!on || wi == 0.f) continue;  // a part without keys holds zeros or nothing
-      const float4 v = *reinterpret_cast<const float4*>(src + c);
-      acc.x = fmaf(wi, v.x, acc.x);
-      acc.y = fmaf(wi, v.y, acc.y);
-      acc.z = fmaf(wi, v.z, acc.z);
-      acc.w = fmaf(wi, v.w, acc.w);
+      const float* src = (part < pre ? pre_o + (part * p.total + row) * p.dv
+                                     : p.part_o + (slot0 + static_cast<long long>(part - pre) * NR) * p.dv) + c;
+      if (wi == 0.f) continue;  // a part without keys holds zeros or nothing
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (c + 128 * w >= p.dv) break;
+        const float4 v = *reinterpret_cast<const float4*>(src + 128 * w);
+        acc[w].x = fmaf(wi, v.x, acc[w].x);
+        acc[w].y = fmaf(wi, v.y, acc[w].y);
+        acc[w].z = fmaf(wi, v.z, acc[w].z);
+        acc[w].w = fmaf(wi, v.w, acc[w].w);
+      }
     }
   }
-  if (on)
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * p.dv + c) =
-        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+    if (c + 128 * w < p.dv)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * p.dv + c + 128 * w) =
+          make_uint2(pack_bf16x2(acc[w].x, acc[w].y), pack_bf16x2(acc[w].z, acc[w].w));
   if (slice == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = m + logf(sum);
 }
 
 template <int DM, int DX, bool SHARED, int NR>
-cudaError_t launch_nr(const SeqAttn& p, const DecodePlan& plan, cudaStream_t s) {
+cudaError_t launch_nr(const SeqAttn& p, const DecodePlan& plan, bool beside, cudaStream_t s) {
   using C = Cfg<DM, DX, SHARED, NR>;
   static SmemOnce once;
   cudaError_t e = once(fa_seq_decode_sm103_kernel<DM, DX, SHARED, NR>, C::SMEM_BYTES);
@@ -809,9 +818,23 @@ cudaError_t launch_nr(const SeqAttn& p, const DecodePlan& plan, cudaStream_t s) 
     return cudaErrorInvalidValue;
   m.m = m.x;
   if (!SHARED && !make_map3(&m.m, p.v, DM, page, pages, plan.box)) return cudaErrorInvalidValue;
-  fa_seq_decode_sm103_kernel<DM, DX, SHARED, NR>
-      <<<plan.heads * plan.row_groups * plan.cuts, kThreads, C::SMEM_BYTES, s>>>(m, p, plan);
+  const unsigned grid = static_cast<unsigned>(plan.heads) * plan.row_groups * plan.cuts;
+  if (beside) return launch_after(fa_seq_decode_sm103_kernel<DM, DX, SHARED, NR>, grid, kThreads, C::SMEM_BYTES, s, m, p, plan);
+  fa_seq_decode_sm103_kernel<DM, DX, SHARED, NR><<<grid, kThreads, C::SMEM_BYTES, s>>>(m, p, plan);
   return cudaGetLastError();
+}
+
+template <int NR>
+cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse, int pre,
+                         cudaStream_t s) {
+  // a warp takes a whole row of 512 where the rows alone give every SM 32 warps
+  const long long rows = static_cast<long long>(w.n_seq) * w.heads * p.rows;
+  const bool wide = p.dv > 128 && rows >= 152 * 32;
+  const long long warps = rows * (wide ? (p.dv + 511) / 512 : (p.dv + 127) / 128);
+  if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
+  return wide ? launch_after(fa_seq_decode_merge_kernel<NR, 4>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre)
+              : launch_after(fa_seq_decode_merge_kernel<NR, 1>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
 }
 
 }  // namespace
@@ -833,11 +856,14 @@ size_t decode_slots(const DecodePlan& w) {
   return static_cast<size_t>(w.heads) * w.row_groups * (static_cast<size_t>(w.cuts) + w.n_seq) * w.nr;
 }
 
-cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, cudaStream_t s) {
+cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, bool beside, cudaStream_t s) {
   if (static_cast<long long>(w.heads) * w.row_groups * w.cuts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-#define FA_DECODE(DM, DX, SH)                                                        \
-  (w.nr == 16 ? launch_nr<DM, DX, SH, 16>(p, w, s)                                   \
-              : w.nr == 32 ? launch_nr<DM, DX, SH, 32>(p, w, s) : launch_nr<DM, DX, SH, 64>(p, w, s))
+  // tile counts are summed, and multiplied by the number of cuts, in 32 bits
+  if (static_cast<long long>(w.n_seq) * tiles_of(p.n_keys) * (w.cuts + 1LL) > 0x7fffffffLL)
+    return cudaErrorInvalidConfiguration;
+#define FA_DECODE(DM, DX, SH)                                                          \
+  (w.nr == 16 ? launch_nr<DM, DX, SH, 16>(p, w, beside, s)                             \
+              : w.nr == 32 ? launch_nr<DM, DX, SH, 32>(p, w, beside, s) : launch_nr<DM, DX, SH, 64>(p, w, beside, s))
   if (w.direct) {
     if (p.dv == 512) return FA_DECODE(512, 64, true);
     if (p.dv == 256) return FA_DECODE(256, 64, true);
@@ -852,16 +878,9 @@ cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, cudaStream_
 
 cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
                                     int pre, cudaStream_t s) {
-  const long long warps = static_cast<long long>(w.n_seq) * w.heads * p.rows * ((p.dv + 127) / 128);
-  if ((warps + 3) / 4 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
-  if (w.nr == 16)
-    fa_seq_decode_merge_kernel<16><<<blocks, 128, 0, s>>>(p, w, pre_o, pre_lse, pre);
-  else if (w.nr == 32)
-    fa_seq_decode_merge_kernel<32><<<blocks, 128, 0, s>>>(p, w, pre_o, pre_lse, pre);
-  else
-    fa_seq_decode_merge_kernel<64><<<blocks, 128, 0, s>>>(p, w, pre_o, pre_lse, pre);
-  return cudaGetLastError();
+  if (w.nr == 16) return launch_merge<16>(p, w, pre_o, pre_lse, pre, s);
+  if (w.nr == 32) return launch_merge<32>(p, w, pre_o, pre_lse, pre, s);
+  return launch_merge<64>(p, w, pre_o, pre_lse, pre, s);
 }
 
 }  // namespace fa

@@ -77,7 +77,8 @@ struct DecodePlan {
 };
 DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box);
 size_t decode_slots(const DecodePlan& w);  // rows of part_o
-cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, cudaStream_t s);
+// beside: the kernel before it on the stream is the same call's and independent
+cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, bool beside, cudaStream_t s);
 // o, lse = the pieces merged, with the partial results pre_o [pre][total][dv] of other keys
 cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
                                     int pre, cudaStream_t s);

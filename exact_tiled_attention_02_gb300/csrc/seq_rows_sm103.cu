@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int CK = C::CK, CV = C::CV, CT = C::CT, NCH = C::NCH, NST = C::NST;
   constexpr int CK1 = CK - D2 / 64;  // chunks of the first key part
   extern __shared__ uint8_t smem_raw[];
+  pdl_launch();  // what reads these results waits for this kernel's end
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
   if (pad + C::SMEM_USED > static_cast<uint32_t>(C::SMEM_BYTES)) {

@@ -176,6 +176,32 @@ inline bool make_map3(CUtensorMap* m, const void* base, long long d0, long long 
   return make_map(m, base, 3, dims, box);
 }
 
+// Programmatic dependent launch: the next kernel of a call may be put on the
+// SMs as this one's blocks let go of them.  pdl_launch lets it start;
+// pdl_wait returns once the kernels before this one have completed and their
+// results can be read.  A kernel launched this way waits before it reads what
+// they wrote and, in any case, before it ends, so that its own completion
+// implies theirs.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// A launch that may overlap the kernel before it on the stream (see pdl_wait),
+// which must be one of the same call.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, int smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Raises a kernel's dynamic shared memory limit once per device.
 struct SmemOnce {
   std::atomic<unsigned long long> done{0};
