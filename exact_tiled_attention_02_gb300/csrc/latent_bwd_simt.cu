@@ -14,23 +14,23 @@
 //   dq     one CTA per 64 queries over the key tiles they see;
 //   dkr    sums the rotary parts over the heads, in head order.
 // No atomics: every sum has one fixed order.  A row that sees no key has
-// P = 0 throughout.  Head dimensions stream through shared memory 64 at a
-// time, transposed ([d][64]); a thread holds a 4 x 4 block of S and dP and,
-// of its 4 rows, columns tx + 16 m of the accumulated gradients.
+// P = 0 throughout.  The CTA's own tile stays in shared memory; the other
+// side streams through one 64 x 64 chunk, loaded into registers while the
+// chunk before it is used: q (S), dO (dP), then dO (dV) and q (dK) again for
+// dkdv; k (S), v (dP), k (dQ) for dq.  Thread (ty, tx): rows 4 ty .., columns
+// tx + 16 j of S and dP, columns 4 tx .. of every chunk of a gradient.
+// Bound by the latency of the chunks at small sizes, else by shared memory.
 #include <cmath>
 
 #include "seq_kernels.h"
+#include "seq_simt.cuh"
 #include "sm103.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int T64 = 64;
-constexpr int LD = 68;
-constexpr int kThreads = 256;
+using namespace simt;
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void store(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
@@ -106,156 +106,123 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// rows [r0, r0 + 64) of columns [c0, c0 + 64) of a matrix, transposed:
-// dst[c * LD + row]; zero outside
-template <typename T>
-__device__ __forceinline__ void load_t(float* dst, const T* __restrict__ src, int r0, int n, int stride, int c0, int d) {
-  for (int idx = threadIdx.x; idx < T64 * T64; idx += kThreads) {
-    const int c = idx & 63, row = idx >> 6;
-    dst[c * LD + row] =
-        (r0 + row < n && c0 + c < d) ? to_f32(src[static_cast<long long>(r0 + row) * stride + c0 + c]) : 0.f;
-  }
-}
-// the same of [kn | kr] rows
-template <typename T>
-__device__ __forceinline__ void load_k(float* dst, const T* __restrict__ kn, const T* __restrict__ kr, int r0, int n,
-                                       int dn, int dr, int c0) {
-  for (int idx = threadIdx.x; idx < T64 * T64; idx += kThreads) {
-    const int c = idx & 63, row = idx >> 6, d = c0 + c;
-    float x = 0.f;
-    if (r0 + row < n && d < dn + dr)
-      x = d < dn ? to_f32(kn[static_cast<long long>(r0 + row) * dn + d])
-                 : to_f32(kr[static_cast<long long>(r0 + row) * dr + d - dn]);
-    dst[c * LD + row] = x;
-  }
-}
-
-// acc += A B^T over a chunk: rows 4ty.. of A, 4tx.. of B, both transposed
-__device__ __forceinline__ void block_abt(float (&acc)[4][4], const float* a, const float* b, int ty, int tx) {
-#pragma unroll 4
-  for (int c = 0; c < T64; ++c) {
-    const float4 x = *reinterpret_cast<const float4*>(a + c * LD + 4 * ty);
-    const float4 y = *reinterpret_cast<const float4*>(b + c * LD + 4 * tx);
-    const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(xv[i], yv[j], acc[i][j]);
-  }
-}
-
-// acc[i][m] += sum_r w[4ty + i][r] b[tx + 16 m][r] over the 64 rows of a tile
-__device__ __forceinline__ void accum_wb(float (&acc)[4][4], const float* w, const float* b, int ty, int tx) {
-#pragma unroll 2
-  for (int r4 = 0; r4 < T64; r4 += 4) {
-    float wv[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 t = *reinterpret_cast<const float4*>(w + (4 * ty + i) * LD + r4);
-      wv[i][0] = t.x;
-      wv[i][1] = t.y;
-      wv[i][2] = t.z;
-      wv[i][3] = t.w;
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const float4 t = *reinterpret_cast<const float4*>(b + (tx + 16 * m) * LD + r4);
-      const float bv[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-      for (int rr = 0; rr < 4; ++rr)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i][m] = fmaf(wv[i][rr], bv[rr], acc[i][m]);
-    }
-  }
-}
-
-constexpr int kSmem = 4 * T64 * LD * 4;
-
 // NK, NV: 64-column chunks of dn + dr and of dv
-template <typename T, int NK, int NV>
-__global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const LatentBwd p) {
+template <int NK, int NV>
+constexpr int bwd_smem() {
+  return (NK + NV + 3) * CHUNK * 4;  // own tile, the streamed chunk, P and dS
+}
+
+template <int NK, int NV>
+__global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const LatentBwd p, int vec) {
   extern __shared__ float4 smem4[];
-  float* A = reinterpret_cast<float*>(smem4);
-  float* Bt = A + T64 * LD;
-  float* P = Bt + T64 * LD;   // [key][query]
-  float* dS = P + T64 * LD;
+  float* C = reinterpret_cast<float*>(smem4);  // the streamed chunk
+  float* P = C + CHUNK;                        // [key][query]
+  float* dS = P + CHUNK;
+  float* K = dS + CHUNK;                       // [NK] chunks of the CTA's keys
+  float* V = K + NK * CHUNK;                   // [NV]
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int ktiles = (p.Nk + T64 - 1) / T64;
   const long long bh = blockIdx.x / ktiles;
   const int j0 = (blockIdx.x % ktiles) * T64;
   const int dk = p.dn + p.dr, npad = (p.Nq + 127) / 128 * 128;
-  const T* q = static_cast<const T*>(p.q) + bh * p.Nq * dk;
-  const T* kn = static_cast<const T*>(p.kn) + bh * p.Nk * p.dn;
-  const T* kr = static_cast<const T*>(p.kr) + (bh / p.H) * p.Nk * p.dr;
-  const T* v = static_cast<const T*>(p.v) + bh * p.Nk * p.dv;
-  const T* dO = static_cast<const T*>(p.dO) + bh * p.Nq * p.dv;
+  const float* q = static_cast<const float*>(p.q) + bh * p.Nq * dk;
+  const float* kn = static_cast<const float*>(p.kn) + bh * p.Nk * p.dn;
+  const float* kr = static_cast<const float*>(p.kr) + (bh / p.H) * p.Nk * p.dr;
+  const float* v = static_cast<const float*>(p.v) + bh * p.Nk * p.dv;
+  const float* dO = static_cast<const float*>(p.dO) + bh * p.Nq * p.dv;
   const float* lse2 = p.lse2 + bh * npad;
   const float* dsum = p.dsum + bh * npad;
   const float sl = p.scale * 1.4426950408889634f;
   const int off = p.Nk - p.Nq;
+  const int first = p.causal ? max(0, j0 - off) / T64 : 0;  // the first query tile with a row that sees key j0
+  const int tiles = (p.Nq + T64 - 1) / T64;
+  float4 buf[4];
+  // chunk of the stream: NK of q, NV of dO, NV of dO, NK of q per query tile
+  auto fetch = [&](int tile, int stage) {
+    const bool of_q = stage < NK || stage >= NK + 2 * NV;
+    const int c = stage < NK ? stage : stage < NK + NV ? stage - NK : stage < NK + 2 * NV ? stage - NK - NV : stage - NK - 2 * NV;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = tile * T64 + ty + 16 * i;
+      const float* row = r >= p.Nq ? nullptr : of_q ? q + static_cast<long long>(r) * dk : dO + static_cast<long long>(r) * p.dv;
+      buf[i] = load4(row, c * T64 + 4 * tx, of_q ? dk : p.dv, vec);
+    }
+  };
+  auto next = [&](int tile, int stage) {  // the chunk in C; the one after it is under way
+    __syncthreads();
+    put(C, buf);
+    __syncthreads();
+    if (stage + 1 < 2 * (NK + NV))
+      fetch(tile, stage + 1);
+    else if (tile + 1 < tiles)
+      fetch(tile + 1, 0);
+  };
+  if (first < tiles) fetch(first, 0);
+#pragma unroll
+  for (int c = 0; c < NK + NV; ++c) {
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long r = j0 + ty + 16 * i;
+      const bool in = r < p.Nk;
+      x[i] = c < NK ? load4(in ? kn + r * p.dn : nullptr, p.dn, kr + r * p.dr, p.dr, c * T64 + 4 * tx, vec)
+                    : load4(in ? v + r * p.dv : nullptr, (c - NK) * T64 + 4 * tx, p.dv, vec);
+    }
+    put(K + c * CHUNK, x);
+  }
   float ak[NK][4][4], av[NV][4][4];
 #pragma unroll
-  for (int c = 0; c < NK; ++c)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int m = 0; m < 4; ++m) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) ak[c][i][m] = 0.f;
+      for (int c = 0; c < NK; ++c) ak[c][i][m] = 0.f;
 #pragma unroll
-  for (int c = 0; c < NV; ++c)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int m = 0; m < 4; ++m) av[c][i][m] = 0.f;
-  const int first = p.causal ? max(0, j0 - off) / T64 : 0;  // the first query tile with a row that sees key j0
-  for (int i0 = first * T64; i0 < p.Nq; i0 += T64) {
+      for (int c = 0; c < NV; ++c) av[c][i][m] = 0.f;
+    }
+  for (int t = first; t < tiles; ++t) {
+    const int i0 = t * T64;
     float s[4][4], dp[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = dp[i][j] = 0.f;
+#pragma unroll
     for (int c = 0; c < NK; ++c) {
-      __syncthreads();
-      load_k(A, kn, kr, j0, p.Nk, p.dn, p.dr, c * T64);
-      load_t(Bt, q, i0, p.Nq, dk, c * T64, dk);
-      __syncthreads();
-      block_abt(s, A, Bt, ty, tx);
+      next(t, c);
+      dot<4>(s, K + c * CHUNK, C, 16, ty, tx);
     }
+#pragma unroll
     for (int c = 0; c < NV; ++c) {
-      __syncthreads();
-      load_t(A, v, j0, p.Nk, p.dv, c * T64, p.dv);
-      load_t(Bt, dO, i0, p.Nq, p.dv, c * T64, p.dv);
-      __syncthreads();
-      block_abt(dp, A, Bt, ty, tx);
+      next(t, NK + c);
+      dot<4>(dp, V + c * CHUNK, C, 16, ty, tx);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = j0 + 4 * ty + i;
+    for (int j = 0; j < 4; ++j) {
+      const int row = i0 + tx + 16 * j;
+      const float l2 = row < p.Nq ? lse2[row] : 0.f, dd = row < p.Nq ? dsum[row] : 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int row = i0 + 4 * tx + j;
+      for (int i = 0; i < 4; ++i) {
+        const int key = j0 + 4 * ty + i;
         const bool in = row < p.Nq && key < p.Nk && (!p.causal || key <= row + off);
-        const float pr = in ? exp2f(fmaf(s[i][j], sl, lse2[row])) : 0.f;
-        P[(4 * ty + i) * LD + 4 * tx + j] = pr;
-        dS[(4 * ty + i) * LD + 4 * tx + j] = in ? pr * (dp[i][j] + dsum[row]) : 0.f;
+        const float pr = in ? exp2f(fmaf(s[i][j], sl, l2)) : 0.f;
+        P[(4 * ty + i) * LD + tx + 16 * j] = pr;
+        dS[(4 * ty + i) * LD + tx + 16 * j] = in ? pr * (dp[i][j] + dd) : 0.f;
       }
     }
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      __syncthreads();
-      load_t(Bt, dO, i0, p.Nq, p.dv, c * T64, p.dv);
-      __syncthreads();
-      accum_wb(av[c], P, Bt, ty, tx);
+      next(t, NK + NV + c);
+      accumulate<4>(av[c], P, C, ty, tx);
     }
 #pragma unroll
     for (int c = 0; c < NK; ++c) {
-      __syncthreads();
-      load_t(Bt, q, i0, p.Nq, dk, c * T64, dk);
-      __syncthreads();
-      accum_wb(ak[c], dS, Bt, ty, tx);
+      next(t, NK + 2 * NV + c);
+      accumulate<4>(ak[c], dS, C, ty, tx);
     }
   }
-  T* dkn = static_cast<T*>(p.dkn) + bh * p.Nk * p.dn;
-  T* dv = static_cast<T*>(p.dv_out) + bh * p.Nk * p.dv;
+  float* dkn = static_cast<float*>(p.dkn) + bh * p.Nk * p.dn;
+  float* dv = static_cast<float*>(p.dv_out) + bh * p.Nk * p.dv;
   float* dkr = p.dkr_part + bh * p.Nk * p.dr;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -265,10 +232,10 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const Late
     for (int c = 0; c < NK; ++c)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const int d = c * T64 + tx + 16 * m;
+        const int d = c * T64 + 4 * tx + m;
         const float x = ak[c][i][m] * p.scale;
         if (d < p.dn)
-          store(dkn + key * p.dn + d, x);
+          dkn[key * p.dn + d] = x;
         else if (d < dk)
           dkr[key * p.dr + d - p.dn] = x;
       }
@@ -276,80 +243,113 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const Late
     for (int c = 0; c < NV; ++c)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const int d = c * T64 + tx + 16 * m;
-        if (d < p.dv) store(dv + key * p.dv + d, av[c][i][m]);
+        const int d = c * T64 + 4 * tx + m;
+        if (d < p.dv) dv[key * p.dv + d] = av[c][i][m];
       }
   }
 }
 
-template <typename T, int NK, int NV>
-__global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const LatentBwd p) {
+template <int NK, int NV>
+__global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const LatentBwd p, int vec) {
   extern __shared__ float4 smem4[];
-  float* A = reinterpret_cast<float*>(smem4);
-  float* Bt = A + T64 * LD;
-  float* dS = Bt + T64 * LD;  // [query][key]
+  float* C = reinterpret_cast<float*>(smem4);
+  float* dS = C + CHUNK;      // [query][key]
+  float* Q = dS + CHUNK;      // [NK] chunks of the CTA's queries
+  float* G = Q + NK * CHUNK;  // [NV] of their dO
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
   const int qtiles = (p.Nq + T64 - 1) / T64;
   const long long bh = blockIdx.x / qtiles;
   const int i0 = (blockIdx.x % qtiles) * T64;
   const int dk = p.dn + p.dr, npad = (p.Nq + 127) / 128 * 128;
-  const T* q = static_cast<const T*>(p.q) + bh * p.Nq * dk;
-  const T* kn = static_cast<const T*>(p.kn) + bh * p.Nk * p.dn;
-  const T* kr = static_cast<const T*>(p.kr) + (bh / p.H) * p.Nk * p.dr;
-  const T* v = static_cast<const T*>(p.v) + bh * p.Nk * p.dv;
-  const T* dO = static_cast<const T*>(p.dO) + bh * p.Nq * p.dv;
-  const float* lse2 = p.lse2 + bh * npad;
-  const float* dsum = p.dsum + bh * npad;
+  const float* q = static_cast<const float*>(p.q) + bh * p.Nq * dk;
+  const float* kn = static_cast<const float*>(p.kn) + bh * p.Nk * p.dn;
+  const float* kr = static_cast<const float*>(p.kr) + (bh / p.H) * p.Nk * p.dr;
+  const float* v = static_cast<const float*>(p.v) + bh * p.Nk * p.dv;
+  const float* dO = static_cast<const float*>(p.dO) + bh * p.Nq * p.dv;
   const float sl = p.scale * 1.4426950408889634f;
   const int off = p.Nk - p.Nq;
-  float aq[NK][4][4];
+  const int end = p.causal ? min(p.Nk, min(p.Nq, i0 + T64) + off) : p.Nk;  // keys that some row of the tile sees
+  const int tiles = end > 0 ? (end + T64 - 1) / T64 : 0;
+  float4 buf[4];
+  auto fetch = [&](int tile, int stage) {  // NK chunks of k, NV of v, NK of k per key tile
 #pragma unroll
-  for (int c = 0; c < NK; ++c)
+    for (int i = 0; i < 4; ++i) {
+      const long long r = tile * T64 + ty + 16 * i;
+      const bool in = r < p.Nk;
+      const int c = stage < NK ? stage : stage - NK - NV;
+      buf[i] = stage >= NK && stage < NK + NV
+                   ? load4(in ? v + r * p.dv : nullptr, (stage - NK) * T64 + 4 * tx, p.dv, vec)
+                   : load4(in ? kn + r * p.dn : nullptr, p.dn, kr + r * p.dr, p.dr, c * T64 + 4 * tx, vec);
+    }
+  };
+  auto next = [&](int tile, int stage) {
+    __syncthreads();
+    put(C, buf);
+    __syncthreads();
+    if (stage + 1 < 2 * NK + NV)
+      fetch(tile, stage + 1);
+    else if (tile + 1 < tiles)
+      fetch(tile + 1, 0);
+  };
+  if (tiles > 0) fetch(0, 0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int c = 0; c < NK + NV; ++c) {
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long r = i0 + ty + 16 * i;
+      const bool in = r < p.Nq;
+      x[i] = c < NK ? load4(in ? q + r * dk : nullptr, c * T64 + 4 * tx, dk, vec)
+                    : load4(in ? dO + r * p.dv : nullptr, (c - NK) * T64 + 4 * tx, p.dv, vec);
+    }
+    put(Q + c * CHUNK, x);
+  }
+  float l2[4], dd[4], aq[NK][4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = i0 + 4 * ty + i;  // padded to whole tiles
+    l2[i] = p.lse2[bh * npad + row];
+    dd[i] = p.dsum[bh * npad + row];
+#pragma unroll
+    for (int c = 0; c < NK; ++c)
 #pragma unroll
       for (int m = 0; m < 4; ++m) aq[c][i][m] = 0.f;
-  const int end = p.causal ? min(p.Nk, min(p.Nq, i0 + T64) + off) : p.Nk;  // keys that some row of the tile sees
-  for (int j0 = 0; j0 < end; j0 += T64) {
+  }
+  for (int t = 0; t < tiles; ++t) {
+    const int j0 = t * T64;
     float s[4][4], dp[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = dp[i][j] = 0.f;
+#pragma unroll
     for (int c = 0; c < NK; ++c) {
-      __syncthreads();
-      load_t(A, q, i0, p.Nq, dk, c * T64, dk);
-      load_k(Bt, kn, kr, j0, p.Nk, p.dn, p.dr, c * T64);
-      __syncthreads();
-      block_abt(s, A, Bt, ty, tx);
+      next(t, c);
+      dot<4>(s, Q + c * CHUNK, C, 16, ty, tx);
     }
+#pragma unroll
     for (int c = 0; c < NV; ++c) {
-      __syncthreads();
-      load_t(A, dO, i0, p.Nq, p.dv, c * T64, p.dv);
-      load_t(Bt, v, j0, p.Nk, p.dv, c * T64, p.dv);
-      __syncthreads();
-      block_abt(dp, A, Bt, ty, tx);
+      next(t, NK + c);
+      dot<4>(dp, G + c * CHUNK, C, 16, ty, tx);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = i0 + 4 * ty + i;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = j0 + 4 * tx + j;
+        const int key = j0 + tx + 16 * j;
         const bool in = row < p.Nq && key < p.Nk && (!p.causal || key <= row + off);
-        const float pr = in ? exp2f(fmaf(s[i][j], sl, lse2[row])) : 0.f;
-        dS[(4 * ty + i) * LD + 4 * tx + j] = in ? pr * (dp[i][j] + dsum[row]) : 0.f;
+        const float pr = in ? exp2f(fmaf(s[i][j], sl, l2[i])) : 0.f;
+        dS[(4 * ty + i) * LD + tx + 16 * j] = in ? pr * (dp[i][j] + dd[i]) : 0.f;
       }
     }
 #pragma unroll
     for (int c = 0; c < NK; ++c) {
-      __syncthreads();
-      load_k(Bt, kn, kr, j0, p.Nk, p.dn, p.dr, c * T64);
-      __syncthreads();
-      accum_wb(aq[c], dS, Bt, ty, tx);
+      next(t, NK + NV + c);
+      accumulate<4>(aq[c], dS, C, ty, tx);
     }
   }
-  T* dq = static_cast<T*>(p.dq) + bh * p.Nq * dk;
+  float* dq = static_cast<float*>(p.dq) + bh * p.Nq * dk;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const long long row = i0 + 4 * ty + i;
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const Latent
     for (int c = 0; c < NK; ++c)
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const int d = c * T64 + tx + 16 * m;
-        if (d < dk) store(dq + row * dk + d, aq[c][i][m] * p.scale);
+        const int d = c * T64 + 4 * tx + m;
+        if (d < dk) dq[row * dk + d] = aq[c][i][m] * p.scale;
       }
   }
 }
@@ -375,34 +375,24 @@ __global__ void __launch_bounds__(256) fa_latent_bwd_dkr_kernel(const float* __r
   store(dkr + i, x);
 }
 
-template <typename T, int NK, int NV>
+template <int NK, int NV>
 cudaError_t launch_nkv(const LatentBwd& p, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(fa_latent_bwd_dkdv_kernel<T, NK, NV>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  constexpr int SMEM = bwd_smem<NK, NV>();
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+  cudaError_t e =
+      cudaFuncSetAttribute(fa_latent_bwd_dkdv_kernel<NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(fa_latent_bwd_dq_kernel<T, NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  e = cudaFuncSetAttribute(fa_latent_bwd_dq_kernel<NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   const long long bh = static_cast<long long>(p.B) * p.H;
   const long long kb = bh * ((p.Nk + T64 - 1) / T64), qb = bh * ((p.Nq + T64 - 1) / T64);
   if (kb > 0x7fffffffLL || qb > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  fa_latent_bwd_dkdv_kernel<T, NK, NV><<<static_cast<unsigned>(kb), kThreads, kSmem, s>>>(p);
+  const int vec = p.dn % 4 == 0 && p.dr % 4 == 0 && p.dv % 4 == 0;  // 16-byte rows
+  fa_latent_bwd_dkdv_kernel<NK, NV><<<static_cast<unsigned>(kb), kThreads, SMEM, s>>>(p, vec);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fa_latent_bwd_dq_kernel<T, NK, NV><<<static_cast<unsigned>(qb), kThreads, kSmem, s>>>(p);
+  fa_latent_bwd_dq_kernel<NK, NV><<<static_cast<unsigned>(qb), kThreads, SMEM, s>>>(p, vec);
   return cudaGetLastError();
-}
-
-template <typename T>
-cudaError_t launch_t(const LatentBwd& p, cudaStream_t s) {
-  const int dk = p.dn + p.dr;
-  if (dk > 256 || p.dv > 128) return cudaErrorInvalidValue;
-  if (p.dv <= 64) {
-    if (dk <= 64) return launch_nkv<T, 1, 1>(p, s);
-    if (dk <= 128) return launch_nkv<T, 2, 1>(p, s);
-    return dk <= 192 ? launch_nkv<T, 3, 1>(p, s) : launch_nkv<T, 4, 1>(p, s);
-  }
-  if (dk <= 128) return launch_nkv<T, 2, 2>(p, s);
-  return dk <= 192 ? launch_nkv<T, 3, 2>(p, s) : launch_nkv<T, 4, 2>(p, s);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -431,8 +421,16 @@ cudaError_t launch_latent_bwd_prep(const LatentBwd& p, fa_dtype dt, cudaStream_t
   return cudaGetLastError();
 }
 
-cudaError_t launch_latent_bwd_simt(const LatentBwd& p, fa_dtype dt, cudaStream_t s) {
-  return dt == FA_DTYPE_F32 ? launch_t<float>(p, s) : launch_t<__nv_bfloat16>(p, s);
+cudaError_t launch_latent_bwd_simt(const LatentBwd& p, cudaStream_t s) {
+  const int dk = p.dn + p.dr;
+  if (dk > 256 || p.dv > 128) return cudaErrorInvalidValue;
+  if (p.dv <= 64) {
+    if (dk <= 64) return launch_nkv<1, 1>(p, s);
+    if (dk <= 128) return launch_nkv<2, 1>(p, s);
+    return dk <= 192 ? launch_nkv<3, 1>(p, s) : launch_nkv<4, 1>(p, s);
+  }
+  if (dk <= 128) return launch_nkv<2, 2>(p, s);
+  return dk <= 192 ? launch_nkv<3, 2>(p, s) : launch_nkv<4, 2>(p, s);
 }
 
 cudaError_t launch_latent_bwd_dkr(const LatentBwd& p, fa_dtype dt, cudaStream_t s) {

@@ -51,8 +51,8 @@ struct SeqAttn {
   unsigned long long wait_ns;
 };
 
-// fp32 on CUDA cores (seq_fwd_simt.cu).
-cudaError_t launch_seq_simt(const SeqAttn& p, fa_dtype dt, cudaStream_t s);
+// float32 on CUDA cores (seq_fwd_simt.cu).
+cudaError_t launch_seq_simt(const SeqAttn& p, cudaStream_t s);
 // Splits of the keys that give the launch enough blocks.
 int seq_simt_splits(long long groups, int rows, int max_keys);
 
@@ -83,9 +83,9 @@ cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, bool beside
 cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
                                     int pre, cudaStream_t s);
 
-// o, lse = the merged partial results [splits][total] (seq_combine.cu).
+// float32 o, lse = the merged partial results [splits][total] (seq_combine.cu).
 cudaError_t launch_seq_combine(const float* part_o, const float* part_lse, int splits, long long total, int dv,
-                               void* o, float* lse, fa_dtype dt, cudaStream_t s);
+                               float* o, float* lse, cudaStream_t s);
 
 // Expanded latent attention's backward.
 struct LatentBwd {
@@ -115,7 +115,7 @@ size_t latent_bwd_workspace_layout(int B, int H, int Nq, int Nk, int dr, size_t*
 cudaError_t launch_latent_bwd_prep(const LatentBwd& p, fa_dtype dt, cudaStream_t s);
 // bf16 on the tensor cores (latent_bwd_sm103.cu)
 cudaError_t launch_latent_bwd_sm103(const LatentBwd& p, cudaStream_t s);
-cudaError_t launch_latent_bwd_simt(const LatentBwd& p, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_latent_bwd_simt(const LatentBwd& p, cudaStream_t s);  // float32
 // dkr = the sum over heads of dkr_part
 cudaError_t launch_latent_bwd_dkr(const LatentBwd& p, fa_dtype dt, cudaStream_t s);
 
