@@ -9,15 +9,15 @@
 //   dk_j = scale sum_i dS_ij q_i,  dkn_j = dk_j[:dn],  dkr_j = sum_heads dk_j[dn:].
 //
 //   prep   -lse_i log2 e and -D_i of every row (padded to 128 rows a head);
-//   dkdv   one CTA per 64 keys of a head over the 64-row query tiles that see
+//   dkdv   one CTA per 64 (or 32) keys of a head over the 64-row query tiles that see
 //          them; the rotary part of dk goes to an fp32 array per head;
-//   dq     one CTA per 64 queries over the key tiles they see;
+//   dq     one CTA per 64 (or 32) queries over the key tiles they see;
 //   dkr    sums the rotary parts over the heads, in head order.
 // No atomics: every sum has one fixed order.  A row that sees no key has
 // P = 0 throughout.  The CTA's own tile stays in shared memory; the other
-// side streams through one 64 x 64 chunk, loaded into registers while the
-// chunk before it is used: q (S), dO (dP), then dO (dV) and q (dK) again for
-// dkdv; k (S), v (dP), k (dQ) for dq.  Thread (ty, tx): rows 4 ty .., columns
+// side streams through a ring of 64 x 64 chunks, copied asynchronously two
+// ahead: q (S), dO (dP), then dO (dV) and q (dK) again for dkdv; k (S), v (dP),
+// k (dQ) for dq.  Thread (ty, tx): rows 4 ty .. (of 64; 2 ty .. of 32), columns
 // tx + 16 j of S and dP, columns 4 tx .. of every chunk of a gradient.
 // Bound by the latency of the chunks at small sizes, else by shared memory.
 #include <cmath>
@@ -106,24 +106,53 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// NK, NV: 64-column chunks of dn + dr and of dv
-template <int NK, int NV>
+constexpr int DEPTH = 3;  // chunks of the ring
+
+// NK, NV: 64-column chunks of dn + dr and of dv; 16 R rows a CTA
+template <int NK, int NV, int R>
 constexpr int bwd_smem() {
-  return (NK + NV + 3) * CHUNK * 4;  // own tile, the streamed chunk, P and dS
+  return (DEPTH * CHUNK + (NK + NV + 2) * 16 * R * LD) * 4;  // the ring, the CTA's own rows, P and dS
 }
 
-template <int NK, int NV>
+// The ring: chunk after chunk of a stream, copied DEPTH - 1 ahead of its use.
+// F: f(n, dst) copies this thread's share of the n-th chunk to dst.
+template <typename F>
+struct Ring {
+  float* base;
+  int total, asked, slot, f_slot;
+  F f;
+  __device__ Ring(float* b, int n, F fn) : base(b), total(n), asked(0), slot(0), f_slot(0), f(fn) {}
+  __device__ void ask() {
+    if (asked < total) f(asked, base + f_slot * CHUNK);
+    ++asked;
+    copies_commit();  // a group a call, empty or not, so that the wait below counts chunks
+    f_slot = f_slot + 1 == DEPTH ? 0 : f_slot + 1;
+  }
+  // the next chunk, complete, and what threads wrote to shared memory before;
+  // asks for a later one into the slot that every thread has left
+  __device__ const float* next() {
+    copies_wait<DEPTH - 2>();
+    __syncthreads();
+    const float* chunk = base + slot * CHUNK;
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
+    ask();
+    return chunk;
+  }
+};
+
+template <int NK, int NV, int R>
 __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const LatentBwd p, int vec) {
+  constexpr int BR = 16 * R, OWN = BR * LD;
   extern __shared__ float4 smem4[];
-  float* C = reinterpret_cast<float*>(smem4);  // the streamed chunk
-  float* P = C + CHUNK;                        // [key][query]
-  float* dS = P + CHUNK;
-  float* K = dS + CHUNK;                       // [NK] chunks of the CTA's keys
-  float* V = K + NK * CHUNK;                   // [NV]
+  float* base = reinterpret_cast<float*>(smem4);
+  float* P = base + DEPTH * CHUNK;  // [key][query]
+  float* dS = P + OWN;
+  float* K = dS + OWN;              // [NK] chunks of the CTA's keys
+  float* V = K + NK * OWN;          // [NV]
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int ktiles = (p.Nk + T64 - 1) / T64;
+  const int ktiles = (p.Nk + BR - 1) / BR;
   const long long bh = blockIdx.x / ktiles;
-  const int j0 = (blockIdx.x % ktiles) * T64;
+  const int j0 = (blockIdx.x % ktiles) * BR;
   const int dk = p.dn + p.dr, npad = (p.Nq + 127) / 128 * 128;
   const float* q = static_cast<const float*>(p.q) + bh * p.Nq * dk;
   const float* kn = static_cast<const float*>(p.kn) + bh * p.Nk * p.dn;
@@ -136,43 +165,41 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const Late
   const int off = p.Nk - p.Nq;
   const int first = p.causal ? max(0, j0 - off) / T64 : 0;  // the first query tile with a row that sees key j0
   const int tiles = (p.Nq + T64 - 1) / T64;
-  float4 buf[4];
-  // chunk of the stream: NK of q, NV of dO, NV of dO, NK of q per query tile
-  auto fetch = [&](int tile, int stage) {
+  constexpr int PER = 2 * (NK + NV);  // chunks a query tile: NK of q, NV of dO, NV of dO, NK of q
+  auto fetch = [&](int n, float* dst) {
+    const int tile = first + n / PER, stage = n % PER;
     const bool of_q = stage < NK || stage >= NK + 2 * NV;
     const int c = stage < NK ? stage : stage < NK + NV ? stage - NK : stage < NK + 2 * NV ? stage - NK - NV : stage - NK - 2 * NV;
+    dst += ty * LD + 4 * tx;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = tile * T64 + ty + 16 * i;
-      const float* row = r >= p.Nq ? nullptr : of_q ? q + static_cast<long long>(r) * dk : dO + static_cast<long long>(r) * p.dv;
-      buf[i] = load4(row, c * T64 + 4 * tx, of_q ? dk : p.dv, vec);
+    for (int i = 0; i < 4; ++i, dst += 16 * LD) {
+      const long long r = tile * T64 + ty + 16 * i;
+      const bool on = r < p.Nq;
+      if (of_q)
+        copy_row4(dst, q + (on ? r * dk : 0), on, c * T64 + 4 * tx, dk, vec);
+      else
+        copy_row4(dst, dO + (on ? r * p.dv : 0), on, c * T64 + 4 * tx, p.dv, vec);
     }
   };
-  auto next = [&](int tile, int stage) {  // the chunk in C; the one after it is under way
-    __syncthreads();
-    put(C, buf);
-    __syncthreads();
-    if (stage + 1 < 2 * (NK + NV))
-      fetch(tile, stage + 1);
-    else if (tile + 1 < tiles)
-      fetch(tile + 1, 0);
-  };
-  if (first < tiles) fetch(first, 0);
 #pragma unroll
-  for (int c = 0; c < NK + NV; ++c) {
-    float4 x[4];
+  for (int i = 0; i < R; ++i) {
+    const int row = ty + 16 * i;
+    const long long r = j0 + row;
+    const bool on = r < p.Nk;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long r = j0 + ty + 16 * i;
-      const bool in = r < p.Nk;
-      x[i] = c < NK ? load4(in ? kn + r * p.dn : nullptr, p.dn, kr + r * p.dr, p.dr, c * T64 + 4 * tx, vec)
-                    : load4(in ? v + r * p.dv : nullptr, (c - NK) * T64 + 4 * tx, p.dv, vec);
-    }
-    put(K + c * CHUNK, x);
+    for (int c = 0; c < NK; ++c)
+      copy_row4(K + c * OWN + row * LD + 4 * tx, kn + (on ? r * p.dn : 0), p.dn, kr + (on ? r * p.dr : 0), p.dr, on,
+                c * T64 + 4 * tx, vec);
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+      copy_row4(V + c * OWN + row * LD + 4 * tx, v + (on ? r * p.dv : 0), on, c * T64 + 4 * tx, p.dv, vec);
   }
-  float ak[NK][4][4], av[NV][4][4];
+  Ring ring(base, max(0, tiles - first) * PER, fetch);  // (the own rows travel in the first chunk's group)
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int c = 0; c < DEPTH - 1; ++c) ring.ask();
+  float ak[NK][R][4], av[NV][R][4];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
 #pragma unroll
@@ -182,51 +209,40 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const Late
     }
   for (int t = first; t < tiles; ++t) {
     const int i0 = t * T64;
-    float s[4][4], dp[4][4];
+    float s[R][4], dp[R][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = dp[i][j] = 0.f;
 #pragma unroll
-    for (int c = 0; c < NK; ++c) {
-      next(t, c);
-      dot<4>(s, K + c * CHUNK, C, 16, ty, tx);
-    }
+    for (int c = 0; c < NK; ++c) dot<R>(s, K + c * OWN, ring.next(), 16, ty, tx);
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      next(t, NK + c);
-      dot<4>(dp, V + c * CHUNK, C, 16, ty, tx);
-    }
+    for (int c = 0; c < NV; ++c) dot<R>(dp, V + c * OWN, ring.next(), 16, ty, tx);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = i0 + tx + 16 * j;
       const float l2 = row < p.Nq ? lse2[row] : 0.f, dd = row < p.Nq ? dsum[row] : 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int key = j0 + 4 * ty + i;
+      for (int i = 0; i < R; ++i) {
+        const int key = j0 + R * ty + i;
         const bool in = row < p.Nq && key < p.Nk && (!p.causal || key <= row + off);
         const float pr = in ? exp2f(fmaf(s[i][j], sl, l2)) : 0.f;
-        P[(4 * ty + i) * LD + tx + 16 * j] = pr;
-        dS[(4 * ty + i) * LD + tx + 16 * j] = in ? pr * (dp[i][j] + dd) : 0.f;
+        P[(R * ty + i) * LD + tx + 16 * j] = pr;
+        dS[(R * ty + i) * LD + tx + 16 * j] = in ? pr * (dp[i][j] + dd) : 0.f;
       }
     }
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      next(t, NK + NV + c);
-      accumulate<4>(av[c], P, C, ty, tx);
-    }
+    for (int c = 0; c < NV; ++c) accumulate<R>(av[c], P, ring.next(), ty, tx);
 #pragma unroll
-    for (int c = 0; c < NK; ++c) {
-      next(t, NK + 2 * NV + c);
-      accumulate<4>(ak[c], dS, C, ty, tx);
-    }
+    for (int c = 0; c < NK; ++c) accumulate<R>(ak[c], dS, ring.next(), ty, tx);
   }
+  copies_wait<0>();
   float* dkn = static_cast<float*>(p.dkn) + bh * p.Nk * p.dn;
   float* dv = static_cast<float*>(p.dv_out) + bh * p.Nk * p.dv;
   float* dkr = p.dkr_part + bh * p.Nk * p.dr;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long key = j0 + 4 * ty + i;
+  for (int i = 0; i < R; ++i) {
+    const long long key = j0 + R * ty + i;
     if (key >= p.Nk) continue;
 #pragma unroll
     for (int c = 0; c < NK; ++c)
@@ -249,17 +265,18 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const Late
   }
 }
 
-template <int NK, int NV>
+template <int NK, int NV, int R>
 __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const LatentBwd p, int vec) {
+  constexpr int BR = 16 * R, OWN = BR * LD;
   extern __shared__ float4 smem4[];
-  float* C = reinterpret_cast<float*>(smem4);
-  float* dS = C + CHUNK;      // [query][key]
-  float* Q = dS + CHUNK;      // [NK] chunks of the CTA's queries
-  float* G = Q + NK * CHUNK;  // [NV] of their dO
+  float* base = reinterpret_cast<float*>(smem4);
+  float* dS = base + DEPTH * CHUNK;  // [query][key]
+  float* Q = dS + OWN;               // [NK] chunks of the CTA's queries
+  float* G = Q + NK * OWN;           // [NV] of their dO
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-  const int qtiles = (p.Nq + T64 - 1) / T64;
+  const int qtiles = (p.Nq + BR - 1) / BR;
   const long long bh = blockIdx.x / qtiles;
-  const int i0 = (blockIdx.x % qtiles) * T64;
+  const int i0 = (blockIdx.x % qtiles) * BR;
   const int dk = p.dn + p.dr, npad = (p.Nq + 127) / 128 * 128;
   const float* q = static_cast<const float*>(p.q) + bh * p.Nq * dk;
   const float* kn = static_cast<const float*>(p.kn) + bh * p.Nk * p.dn;
@@ -268,46 +285,43 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const Latent
   const float* dO = static_cast<const float*>(p.dO) + bh * p.Nq * p.dv;
   const float sl = p.scale * 1.4426950408889634f;
   const int off = p.Nk - p.Nq;
-  const int end = p.causal ? min(p.Nk, min(p.Nq, i0 + T64) + off) : p.Nk;  // keys that some row of the tile sees
+  const int end = p.causal ? min(p.Nk, min(p.Nq, i0 + BR) + off) : p.Nk;  // keys that some row of the tile sees
   const int tiles = end > 0 ? (end + T64 - 1) / T64 : 0;
-  float4 buf[4];
-  auto fetch = [&](int tile, int stage) {  // NK chunks of k, NV of v, NK of k per key tile
+  constexpr int PER = 2 * NK + NV;  // chunks a key tile: NK of k, NV of v, NK of k
+  auto fetch = [&](int n, float* dst) {
+    const int tile = n / PER, stage = n % PER;
+    const bool of_v = stage >= NK && stage < NK + NV;
+    const int c = stage < NK ? stage : of_v ? stage - NK : stage - NK - NV;
+    dst += ty * LD + 4 * tx;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i, dst += 16 * LD) {
       const long long r = tile * T64 + ty + 16 * i;
-      const bool in = r < p.Nk;
-      const int c = stage < NK ? stage : stage - NK - NV;
-      buf[i] = stage >= NK && stage < NK + NV
-                   ? load4(in ? v + r * p.dv : nullptr, (stage - NK) * T64 + 4 * tx, p.dv, vec)
-                   : load4(in ? kn + r * p.dn : nullptr, p.dn, kr + r * p.dr, p.dr, c * T64 + 4 * tx, vec);
+      const bool on = r < p.Nk;
+      if (of_v)
+        copy_row4(dst, v + (on ? r * p.dv : 0), on, c * T64 + 4 * tx, p.dv, vec);
+      else
+        copy_row4(dst, kn + (on ? r * p.dn : 0), p.dn, kr + (on ? r * p.dr : 0), p.dr, on, c * T64 + 4 * tx, vec);
     }
   };
-  auto next = [&](int tile, int stage) {
-    __syncthreads();
-    put(C, buf);
-    __syncthreads();
-    if (stage + 1 < 2 * NK + NV)
-      fetch(tile, stage + 1);
-    else if (tile + 1 < tiles)
-      fetch(tile + 1, 0);
-  };
-  if (tiles > 0) fetch(0, 0);
 #pragma unroll
-  for (int c = 0; c < NK + NV; ++c) {
-    float4 x[4];
+  for (int i = 0; i < R; ++i) {
+    const int row = ty + 16 * i;
+    const long long r = i0 + row;
+    const bool on = r < p.Nq;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long r = i0 + ty + 16 * i;
-      const bool in = r < p.Nq;
-      x[i] = c < NK ? load4(in ? q + r * dk : nullptr, c * T64 + 4 * tx, dk, vec)
-                    : load4(in ? dO + r * p.dv : nullptr, (c - NK) * T64 + 4 * tx, p.dv, vec);
-    }
-    put(Q + c * CHUNK, x);
+    for (int c = 0; c < NK; ++c)
+      copy_row4(Q + c * OWN + row * LD + 4 * tx, q + (on ? r * dk : 0), on, c * T64 + 4 * tx, dk, vec);
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+      copy_row4(G + c * OWN + row * LD + 4 * tx, dO + (on ? r * p.dv : 0), on, c * T64 + 4 * tx, p.dv, vec);
   }
-  float l2[4], dd[4], aq[NK][4][4];
+  Ring ring(base, tiles * PER, fetch);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = i0 + 4 * ty + i;  // padded to whole tiles
+  for (int c = 0; c < DEPTH - 1; ++c) ring.ask();
+  float l2[R], dd[R], aq[NK][R][4];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int row = i0 + R * ty + i;  // padded to whole tiles
     l2[i] = p.lse2[bh * npad + row];
     dd[i] = p.dsum[bh * npad + row];
 #pragma unroll
@@ -317,42 +331,34 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const Latent
   }
   for (int t = 0; t < tiles; ++t) {
     const int j0 = t * T64;
-    float s[4][4], dp[4][4];
+    float s[R][4], dp[R][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = dp[i][j] = 0.f;
 #pragma unroll
-    for (int c = 0; c < NK; ++c) {
-      next(t, c);
-      dot<4>(s, Q + c * CHUNK, C, 16, ty, tx);
-    }
+    for (int c = 0; c < NK; ++c) dot<R>(s, Q + c * OWN, ring.next(), 16, ty, tx);
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      next(t, NK + c);
-      dot<4>(dp, G + c * CHUNK, C, 16, ty, tx);
-    }
+    for (int c = 0; c < NV; ++c) dot<R>(dp, G + c * OWN, ring.next(), 16, ty, tx);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = i0 + 4 * ty + i;
+    for (int i = 0; i < R; ++i) {
+      const int row = i0 + R * ty + i;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int key = j0 + tx + 16 * j;
         const bool in = row < p.Nq && key < p.Nk && (!p.causal || key <= row + off);
         const float pr = in ? exp2f(fmaf(s[i][j], sl, l2[i])) : 0.f;
-        dS[(4 * ty + i) * LD + tx + 16 * j] = in ? pr * (dp[i][j] + dd[i]) : 0.f;
+        dS[(R * ty + i) * LD + tx + 16 * j] = in ? pr * (dp[i][j] + dd[i]) : 0.f;
       }
     }
 #pragma unroll
-    for (int c = 0; c < NK; ++c) {
-      next(t, NK + NV + c);
-      accumulate<4>(aq[c], dS, C, ty, tx);
-    }
+    for (int c = 0; c < NK; ++c) accumulate<R>(aq[c], dS, ring.next(), ty, tx);
   }
+  copies_wait<0>();
   float* dq = static_cast<float*>(p.dq) + bh * p.Nq * dk;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const long long row = i0 + 4 * ty + i;
+  for (int i = 0; i < R; ++i) {
+    const long long row = i0 + R * ty + i;
     if (row >= p.Nq) continue;
 #pragma unroll
     for (int c = 0; c < NK; ++c)
@@ -375,24 +381,31 @@ __global__ void __launch_bounds__(256) fa_latent_bwd_dkr_kernel(const float* __r
   store(dkr + i, x);
 }
 
-template <int NK, int NV>
-cudaError_t launch_nkv(const LatentBwd& p, cudaStream_t s) {
-  constexpr int SMEM = bwd_smem<NK, NV>();
+template <int NK, int NV, int R>
+cudaError_t launch_r(const LatentBwd& p, cudaStream_t s) {
+  constexpr int SMEM = bwd_smem<NK, NV, R>();
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
   cudaError_t e =
-      cudaFuncSetAttribute(fa_latent_bwd_dkdv_kernel<NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+      cudaFuncSetAttribute(fa_latent_bwd_dkdv_kernel<NK, NV, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(fa_latent_bwd_dq_kernel<NK, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  e = cudaFuncSetAttribute(fa_latent_bwd_dq_kernel<NK, NV, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
   const long long bh = static_cast<long long>(p.B) * p.H;
-  const long long kb = bh * ((p.Nk + T64 - 1) / T64), qb = bh * ((p.Nq + T64 - 1) / T64);
+  const long long kb = bh * ((p.Nk + 16 * R - 1) / (16 * R)), qb = bh * ((p.Nq + 16 * R - 1) / (16 * R));
   if (kb > 0x7fffffffLL || qb > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const int vec = p.dn % 4 == 0 && p.dr % 4 == 0 && p.dv % 4 == 0;  // 16-byte rows
-  fa_latent_bwd_dkdv_kernel<NK, NV><<<static_cast<unsigned>(kb), kThreads, SMEM, s>>>(p, vec);
+  fa_latent_bwd_dkdv_kernel<NK, NV, R><<<static_cast<unsigned>(kb), kThreads, SMEM, s>>>(p, vec);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fa_latent_bwd_dq_kernel<NK, NV><<<static_cast<unsigned>(qb), kThreads, SMEM, s>>>(p, vec);
+  fa_latent_bwd_dq_kernel<NK, NV, R><<<static_cast<unsigned>(qb), kThreads, SMEM, s>>>(p, vec);
   return cudaGetLastError();
+}
+// 64 rows a CTA where that fills the SMs, else 32 (which take less time each)
+template <int NK, int NV>
+cudaError_t launch_nkv(const LatentBwd& p, cudaStream_t s) {
+  const long long n = p.Nk < p.Nq ? p.Nk : p.Nq;
+  return static_cast<long long>(p.B) * p.H * ((n + 63) / 64) >= 152 ? launch_r<NK, NV, 4>(p, s)
+                                                                    : launch_r<NK, NV, 2>(p, s);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

@@ -9,8 +9,8 @@
 //
 // One CTA of 256 threads per TR query rows (64, 32 or 16, by the group's row
 // count) and split of the keys; tiles of 64 keys.  The queries stay in shared
-// memory; keys and values stream through one 64 x 64 chunk, each chunk loaded
-// into registers while the one before it is used.  Thread (ty, tx): rows
+// memory; keys and values stream through a ring of 64 x 64 chunks, copied
+// asynchronously up to three chunks ahead.  Thread (ty, tx): rows
 // TR/16 ty .., keys tx + 16 j of S, columns 4 tx .. of every chunk of O.
 // Calls with few rows are bound by the latency of their chunks, one after the
 // other (the keys are split until every CTA has about one tile); many rows by
@@ -27,6 +27,7 @@ namespace {
 using namespace simt;
 
 constexpr int BK = T64;  // keys per tile
+constexpr int DEPTH = 4;  // chunks of the ring
 
 __device__ __forceinline__ float half_warp_max(float x) {
 #pragma unroll
@@ -48,9 +49,9 @@ template <int TR, int NCV>
 __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn p, int vec) {
   constexpr int RPT = TR / 16;
   extern __shared__ float4 smem4[];
-  float* Ks = reinterpret_cast<float*>(smem4);  // one chunk of keys or values
-  float* Ps = Ks + CHUNK;                       // [TR][LD]
-  float* Qs = Ps + TR * LD;                     // [chunks of dk][TR][LD]
+  float* ring = reinterpret_cast<float*>(smem4);  // [DEPTH] chunks of keys or values
+  float* Ps = ring + DEPTH * CHUNK;               // [TR][LD]
+  float* Qs = Ps + TR * LD;                       // [chunks of dk][TR][LD]
   const int row_tiles = (p.rows + TR - 1) / TR;
   const int g = blockIdx.x / row_tiles;
   const int r0 = (blockIdx.x % row_tiles) * TR;
@@ -96,31 +97,54 @@ __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn
       }
     }
   };
-  float4 buf[4];
-  auto fetch = [&](int stage) {  // stage < nck: a chunk of keys, else of values
+  // chunk `stage` of the tile that krow describes (keys first, then values) to ring slot `slot`
+  auto fetch = [&](int stage, int slot) {
+    float* dst = ring + slot * CHUNK + ty * LD + 4 * tx;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (stage < nck) {
-        const float* a = krow[i] >= 0 ? k1 + krow[i] * p.d1 : nullptr;
-        buf[i] = load4(a, p.d1, k2 + krow2[i] * p.d2, p.d2, stage * T64 + 4 * tx, vec);
-      } else {
-        buf[i] = load4(krow[i] >= 0 ? v + krow[i] * p.v_stride : nullptr, (stage - nck) * T64 + 4 * tx, p.dv, vec);
-      }
+    for (int i = 0; i < 4; ++i, dst += 16 * LD) {
+      const bool on = krow[i] >= 0;
+      if (stage < nck)
+        copy_row4(dst, k1 + (on ? krow[i] * p.d1 : 0), p.d1, k2 + (on ? krow2[i] * p.d2 : 0), p.d2, on,
+                  stage * T64 + 4 * tx, vec);
+      else
+        copy_row4(dst, v + (on ? krow[i] * p.v_stride : 0), on, (stage - nck) * T64 + 4 * tx, p.dv, vec);
     }
   };
-  if (t0 < t1) {
-    place(t0);
-    fetch(0);
-  }
-  for (int c = 0; c < nck; ++c) {
-    float4 x[RPT];
+  // the stream: nck + ncv chunks a tile; (f_tile, f_stage) is the next one to ask for, into slot f_slot
+  int f_tile = t0, f_stage = 0, f_slot = 0, slot = 0;
+  auto ask = [&]() {
+    if (f_tile < t1) {
+      if (f_stage == 0) place(f_tile);
+      fetch(f_stage, f_slot);
+      if (++f_stage == nck + ncv) {
+        f_stage = 0;
+        ++f_tile;
+      }
+    }
+    copies_commit();  // a group a call, empty or not, so that the wait below counts chunks
+    f_slot = f_slot + 1 == DEPTH ? 0 : f_slot + 1;
+  };
+  // the next chunk of the stream, complete; asks for the one DEPTH - 1 later,
+  // whose slot every thread has left
+  auto next = [&]() -> const float* {
+    copies_wait<DEPTH - 2>();
+    __syncthreads();
+    const float* chunk = ring + slot * CHUNK;
+    slot = slot + 1 == DEPTH ? 0 : slot + 1;
+    ask();
+    return chunk;
+  };
+  for (int c = 0; c < nck; ++c)
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       const int r = r0 + ty + 16 * i;
-      x[i] = load4(r < p.rows ? q + out_row(p, g, r) * dk : nullptr, c * T64 + 4 * tx, dk, vec);
+      const bool on = r < p.rows;
+      copy_row4(Qs + (c * TR + ty + 16 * i) * LD + 4 * tx, q + (on ? out_row(p, g, r) * dk : 0), on, c * T64 + 4 * tx,
+                dk, vec);
     }
-    put(Qs + c * TR * LD, x);
-  }
+  // (the queries travel in the first chunk's group)
+#pragma unroll
+  for (int c = 0; c < DEPTH - 1; ++c) ask();
   int limit[RPT];  // keys that the thread's rows see
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
@@ -145,13 +169,8 @@ __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn
     for (int i = 0; i < RPT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-    for (int c = 0; c < nck; ++c) {
-      __syncthreads();  // the previous chunk is no longer read
-      put(Ks, buf);
-      __syncthreads();
-      fetch(c + 1);  // values follow the last chunk of keys
-      dot<RPT>(s, Qs + c * TR * LD, Ks, (min(T64, dk - c * T64) + 3) >> 2, ty, tx);
-    }
+    for (int c = 0; c < nck; ++c)
+      dot<RPT>(s, Qs + c * TR * LD, next(), (min(T64, dk - c * T64) + 3) >> 2, ty, tx);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       float tmax = -INFINITY;
@@ -178,20 +197,10 @@ __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn
         for (int e = 0; e < 4; ++e) acc[c][i][e] *= alpha;
     }
 #pragma unroll
-    for (int c = 0; c < NCV; ++c) {
-      if (c >= ncv) break;
-      __syncthreads();
-      put(Ks, buf);
-      __syncthreads();
-      if (c + 1 < ncv) {
-        fetch(nck + c + 1);
-      } else if (kt + 1 < t1) {
-        place(kt + 1);
-        fetch(0);
-      }
-      accumulate<RPT>(acc[c], Ps, Ks, ty, tx);
-    }
+    for (int c = 0; c < NCV; ++c)
+      if (c < ncv) accumulate<RPT>(acc[c], Ps, next(), ty, tx);  // next() also makes P visible
   }
+  copies_wait<0>();
 
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn
 template <int TR, int NCV>
 cudaError_t launch_one(const SeqAttn& p, cudaStream_t s) {
   const int nck = (p.d1 + p.d2 + T64 - 1) / T64;
-  const int smem = (CHUNK + TR * LD * (1 + nck)) * 4;
+  const int smem = (DEPTH * CHUNK + TR * LD * (1 + nck)) * 4;
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
   const cudaError_t e =
       cudaFuncSetAttribute(fa_seq_fwd_simt_kernel<TR, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -243,12 +252,19 @@ cudaError_t launch_tr(const SeqAttn& p, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-int rows_per_cta(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+// Rows of a CTA: 64 unless that leaves SMs idle (a CTA with fewer rows takes
+// less time, though more for each row: 2300, 1300 and 1200 cycles a chunk for
+// 64, 32 and 16 rows).
+int rows_per_cta(long long groups, int rows, int splits, int dk) {
+  for (int tr = dk > 512 ? 32 : 64; tr > 16; tr /= 2)  // (64 wider rows would not fit shared memory)
+    if (rows > tr / 2 && groups * ((rows + tr - 1) / tr) * splits >= 152) return tr;
+  return 16;
+}
 
 }  // namespace
 
 int seq_simt_splits(long long groups, int rows, int max_keys) {
-  const int tr = rows_per_cta(rows);
+  const int tr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   const long long blocks = groups * ((rows + tr - 1) / tr);
   const int tiles = (max_keys + BK - 1) / BK;
   long long n = (4 * 152 + blocks - 1) / blocks;
@@ -257,8 +273,10 @@ int seq_simt_splits(long long groups, int rows, int max_keys) {
   return n < 1 ? 1 : static_cast<int>(n);
 }
 
-cudaError_t launch_seq_simt(const SeqAttn& p, cudaStream_t s) {
-  switch (rows_per_cta(p.rows)) {
+cudaError_t launch_seq_simt(const SeqAttn& args, cudaStream_t s) {
+  SeqAttn p = args;
+  if (p.k2 == nullptr) p.k2 = p.k1;  // never read: copies of nothing still name an address
+  switch (rows_per_cta(p.groups, p.rows, p.splits, p.d1 + p.d2)) {
     case 16: return launch_tr<16>(p, s);
     case 32: return launch_tr<32>(p, s);
     default: return launch_tr<64>(p, s);

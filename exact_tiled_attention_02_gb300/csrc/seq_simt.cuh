@@ -1,48 +1,67 @@
 // seq_simt.cuh -- tiles of the fp32 CUDA-core kernels of the language-model
-// operators: 64 x 64 chunks, row-major in shared memory, filled from registers
-// that were loaded while the previous chunk was being used.
+// operators: 64 x 64 chunks, row-major in shared memory, copied there
+// asynchronously several chunks ahead of their use.
 #pragma once
 
+#include <cstdint>
 #include <cuda_runtime.h>
 
 namespace fa {
 namespace simt {
 
-constexpr int T64 = 64;       // rows of a tile, and columns of a chunk
+constexpr int T64 = 64;       // rows of a streamed tile, and columns of a chunk
 constexpr int LD = 68;        // row stride of a chunk in floats: rows 16-byte aligned, 8 rows apart in 32 banks
 constexpr int kThreads = 256;
 constexpr int CHUNK = T64 * LD;
 
-// Entries d .. d + 3 of a row, zeros at and past n.
-__device__ __forceinline__ float4 load4(const float* row, int d, int n, bool vec) {
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (row == nullptr || d >= n) return v;
-  if (vec) return *reinterpret_cast<const float4*>(row + d);
-  v.x = row[d];
-  if (d + 1 < n) v.y = row[d + 1];
-  if (d + 2 < n) v.z = row[d + 2];
-  if (d + 3 < n) v.w = row[d + 3];
-  return v;
+// Asynchronous copy of 16 or 4 bytes to shared memory; zeros where !on (then
+// src is any valid address).
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(on ? 16 : 0)
+               : "memory");
 }
-// The same of a row in two parts, n1 and n2 entries; no row (zeros) where r1 is null.
-__device__ __forceinline__ float4 load4(const float* r1, int n1, const float* r2, int n2, int d, bool vec) {
-  if (r1 == nullptr) return make_float4(0.f, 0.f, 0.f, 0.f);
-  if (vec || d + 4 <= n1 || d >= n1) return d < n1 ? load4(r1, d, n1, vec) : load4(r2, d - n1, n2, vec);
-  float x[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int c = d + e;
-    x[e] = c < n1 ? r1[c] : c - n1 < n2 ? r2[c - n1] : 0.f;
-  }
-  return make_float4(x[0], x[1], x[2], x[3]);
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool on) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(on ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of this thread's committed groups are still on their way.
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Thread tid's share of a chunk: rows tid / 16 + 16 i, columns 4 (tid % 16) ..
-template <int N>
-__device__ __forceinline__ void put(float* chunk, const float4 (&v)[N]) {
-  const int row = threadIdx.x >> 4, c = (threadIdx.x & 15) * 4;
+// Entries d .. d + 3 of a row of n to dst, zeros past n and where there is no
+// row (on false; row is then any valid address).  vec: rows are 16-byte
+// aligned and n a multiple of 4.
+__device__ __forceinline__ void copy_row4(float* dst, const float* row, bool on, int d, int n, bool vec) {
+  if (vec) {
+    copy16(dst, on && d < n ? row + d : row, on && d < n);
+  } else {
 #pragma unroll
-  for (int i = 0; i < N; ++i) *reinterpret_cast<float4*>(chunk + (row + 16 * i) * LD + c) = v[i];
+    for (int e = 0; e < 4; ++e) copy4(dst + e, on && d + e < n ? row + d + e : row, on && d + e < n);
+  }
+}
+// The same of a row in two parts, n1 and n2 entries.
+__device__ __forceinline__ void copy_row4(float* dst, const float* r1, int n1, const float* r2, int n2, bool on, int d,
+                                          bool vec) {
+  if (vec) {
+    if (d < n1)
+      copy_row4(dst, r1, on, d, n1, true);
+    else
+      copy_row4(dst, r2, on, d - n1, n2, true);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int c = d + e;
+      const bool in = on && c < n1 + n2;
+      copy4(dst + e, !in ? r1 : c < n1 ? r1 + c : r2 + c - n1, in);
+    }
+  }
 }
 
 // acc[i][j] += row R ty + i of A . row tx + 16 j of B, over the first n4 groups of four columns
