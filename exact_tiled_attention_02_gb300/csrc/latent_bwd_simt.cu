@@ -9,22 +9,21 @@
 //   dk_j = scale sum_i dS_ij q_i,  dkn_j = dk_j[:dn],  dkr_j = sum_heads dk_j[dn:].
 //
 //   prep   -lse_i log2 e and -D_i of every row (padded to 128 rows a head);
-//   dkdv   one CTA per 64 (or 32) keys of a head over the 64-row query tiles that see
+//   dkdv   one CTA per 64 (32, 16) keys of a head over the 64-row query tiles that see
 //          them; the rotary part of dk goes to an fp32 array per head;
-//   dq     one CTA per 64 (or 32) queries over the key tiles they see;
+//   dq     one CTA per 64 (32, 16) queries over the key tiles they see;
 //   dkr    sums the rotary parts over the heads, in head order.
 // No atomics: every sum has one fixed order.  A row that sees no key has
 // P = 0 throughout.  The CTA's own tile stays in shared memory; the other
 // side streams through a ring of 64 x 64 chunks, copied asynchronously two
 // ahead: q (S), dO (dP), then dO (dV) and q (dK) again for dkdv; k (S), v (dP),
-// k (dQ) for dq.  Thread (ty, tx): rows 4 ty .. (of 64; 2 ty .. of 32), columns
-// tx + 16 j of S and dP, columns 4 tx .. of every chunk of a gradient.
+// k (dQ) for dq.  Products go in 4 x 4 blocks a thread (seq_simt.cuh).
 // Bound by the latency of the chunks at small sizes, else by shared memory.
 #include <cmath>
 
 #include "seq_kernels.h"
 #include "seq_simt.cuh"
-#include "sm103.cuh"
+#include "seq_sm103.cuh"
 
 namespace fa {
 namespace {
@@ -108,10 +107,10 @@ __global__ void __launch_bounds__(256)
 
 constexpr int DEPTH = 3;  // chunks of the ring
 
-// NK, NV: 64-column chunks of dn + dr and of dv; 16 R rows a CTA
-template <int NK, int NV, int R>
+// NK, NV: 64-column chunks of dn + dr and of dv; BR rows a CTA
+template <int NK, int NV, int BR>
 constexpr int bwd_smem() {
-  return (DEPTH * CHUNK + (NK + NV + 2) * 16 * R * LD) * 4;  // the ring, the CTA's own rows, P and dS
+  return (DEPTH * CHUNK + CHUNK + (NK + NV + 2) * BR * LD) * 4;  // ring, partial sums, own rows, P and dS
 }
 
 // The ring: chunk after chunk of a stream, copied DEPTH - 1 ahead of its use.
@@ -140,12 +139,14 @@ struct Ring {
   }
 };
 
-template <int NK, int NV, int R>
+template <int NK, int NV, int BR>
 __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const LatentBwd p, int vec) {
-  constexpr int BR = 16 * R, OWN = BR * LD;
+  constexpr int R = BR / 16, OWN = BR * LD;
+  const Block<BR> blk;
   extern __shared__ float4 smem4[];
   float* base = reinterpret_cast<float*>(smem4);
-  float* P = base + DEPTH * CHUNK;  // [key][query]
+  float* red = base + DEPTH * CHUNK;  // the groups' partial sums
+  float* P = red + CHUNK;           // [key][query]
   float* dS = P + OWN;
   float* K = dS + OWN;              // [NK] chunks of the CTA's keys
   float* V = K + NK * OWN;          // [NV]
@@ -197,9 +198,9 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const Late
   Ring ring(base, max(0, tiles - first) * PER, fetch);  // (the own rows travel in the first chunk's group)
 #pragma unroll
   for (int c = 0; c < DEPTH - 1; ++c) ring.ask();
-  float ak[NK][R][4], av[NV][R][4];
+  float ak[NK][4][4], av[NV][4][4];
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
 #pragma unroll
@@ -209,40 +210,61 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const Late
     }
   for (int t = first; t < tiles; ++t) {
     const int i0 = t * T64;
-    float s[R][4], dp[R][4];
+    float s[4][4], dp[4][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = dp[i][j] = 0.f;
 #pragma unroll
-    for (int c = 0; c < NK; ++c) dot<R>(s, K + c * OWN, ring.next(), 16, ty, tx);
+    for (int c = 0; c < NK; ++c) blk.dot(s, K + c * OWN, ring.next(), 16);
 #pragma unroll
-    for (int c = 0; c < NV; ++c) dot<R>(dp, V + c * OWN, ring.next(), 16, ty, tx);
+    for (int c = 0; c < NV; ++c) blk.dot(dp, V + c * OWN, ring.next(), 16);
+    // the groups' sums, S then dP through the same array; thread: keys R ty .., queries tx + 16 j
+    float pr[R][4];
+    blk.put_dot(red, s);
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = i0 + tx + 16 * j;
-      const float l2 = row < p.Nq ? lse2[row] : 0.f, dd = row < p.Nq ? dsum[row] : 0.f;
+      const float l2 = row < p.Nq ? lse2[row] : 0.f;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const int key = j0 + R * ty + i;
         const bool in = row < p.Nq && key < p.Nk && (!p.causal || key <= row + off);
-        const float pr = in ? exp2f(fmaf(s[i][j], sl, l2)) : 0.f;
-        P[(R * ty + i) * LD + tx + 16 * j] = pr;
-        dS[(R * ty + i) * LD + tx + 16 * j] = in ? pr * (dp[i][j] + dd) : 0.f;
+        pr[i][j] = in ? exp2f(fmaf(Block<BR>::get(red, R * ty + i, tx + 16 * j), sl, l2)) : 0.f;
+        P[(R * ty + i) * LD + tx + 16 * j] = pr[i][j];
+      }
+    }
+    __syncthreads();
+    blk.put_dot(red, dp);
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = i0 + tx + 16 * j;
+      const float dd = row < p.Nq ? dsum[row] : 0.f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float g = Block<BR>::get(red, R * ty + i, tx + 16 * j);
+        dS[(R * ty + i) * LD + tx + 16 * j] = pr[i][j] == 0.f ? 0.f : pr[i][j] * (g + dd);
       }
     }
 #pragma unroll
-    for (int c = 0; c < NV; ++c) accumulate<R>(av[c], P, ring.next(), ty, tx);
+    for (int c = 0; c < NV; ++c) blk.accumulate(av[c], P, ring.next());
 #pragma unroll
-    for (int c = 0; c < NK; ++c) accumulate<R>(ak[c], dS, ring.next(), ty, tx);
+    for (int c = 0; c < NK; ++c) blk.accumulate(ak[c], dS, ring.next());
   }
   copies_wait<0>();
+#pragma unroll
+  for (int c = 0; c < NK; ++c) blk.add_up(red, ak[c]);
+#pragma unroll
+  for (int c = 0; c < NV; ++c) blk.add_up(red, av[c]);
+  if (blk.grp != 0) return;
   float* dkn = static_cast<float*>(p.dkn) + bh * p.Nk * p.dn;
   float* dv = static_cast<float*>(p.dv_out) + bh * p.Nk * p.dv;
   float* dkr = p.dkr_part + bh * p.Nk * p.dr;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const long long key = j0 + R * ty + i;
+  for (int i = 0; i < 4; ++i) {
+    const long long key = j0 + 4 * blk.ty + i;
     if (key >= p.Nk) continue;
 #pragma unroll
     for (int c = 0; c < NK; ++c)
@@ -265,12 +287,14 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const Late
   }
 }
 
-template <int NK, int NV, int R>
+template <int NK, int NV, int BR>
 __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const LatentBwd p, int vec) {
-  constexpr int BR = 16 * R, OWN = BR * LD;
+  constexpr int R = BR / 16, OWN = BR * LD;
+  const Block<BR> blk;
   extern __shared__ float4 smem4[];
   float* base = reinterpret_cast<float*>(smem4);
-  float* dS = base + DEPTH * CHUNK;  // [query][key]
+  float* red = base + DEPTH * CHUNK;  // the groups' partial sums
+  float* dS = red + CHUNK;           // [query][key]
   float* Q = dS + OWN;               // [NK] chunks of the CTA's queries
   float* G = Q + NK * OWN;           // [NV] of their dO
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
@@ -318,28 +342,33 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const Latent
   Ring ring(base, tiles * PER, fetch);
 #pragma unroll
   for (int c = 0; c < DEPTH - 1; ++c) ring.ask();
-  float l2[R], dd[R], aq[NK][R][4];
+  float l2[R], dd[R], aq[NK][4][4];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int row = i0 + R * ty + i;  // padded to whole tiles
     l2[i] = p.lse2[bh * npad + row];
     dd[i] = p.dsum[bh * npad + row];
+  }
 #pragma unroll
-    for (int c = 0; c < NK; ++c)
+  for (int c = 0; c < NK; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int m = 0; m < 4; ++m) aq[c][i][m] = 0.f;
-  }
   for (int t = 0; t < tiles; ++t) {
     const int j0 = t * T64;
-    float s[R][4], dp[R][4];
+    float s[4][4], dp[4][4];
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = dp[i][j] = 0.f;
 #pragma unroll
-    for (int c = 0; c < NK; ++c) dot<R>(s, Q + c * OWN, ring.next(), 16, ty, tx);
+    for (int c = 0; c < NK; ++c) blk.dot(s, Q + c * OWN, ring.next(), 16);
 #pragma unroll
-    for (int c = 0; c < NV; ++c) dot<R>(dp, G + c * OWN, ring.next(), 16, ty, tx);
+    for (int c = 0; c < NV; ++c) blk.dot(dp, G + c * OWN, ring.next(), 16);
+    float pr[R][4];  // thread: queries R ty .., keys tx + 16 j
+    blk.put_dot(red, s);
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int row = i0 + R * ty + i;
@@ -347,18 +376,30 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const Latent
       for (int j = 0; j < 4; ++j) {
         const int key = j0 + tx + 16 * j;
         const bool in = row < p.Nq && key < p.Nk && (!p.causal || key <= row + off);
-        const float pr = in ? exp2f(fmaf(s[i][j], sl, l2[i])) : 0.f;
-        dS[(R * ty + i) * LD + tx + 16 * j] = in ? pr * (dp[i][j] + dd[i]) : 0.f;
+        pr[i][j] = in ? exp2f(fmaf(Block<BR>::get(red, R * ty + i, tx + 16 * j), sl, l2[i])) : 0.f;
       }
     }
+    __syncthreads();
+    blk.put_dot(red, dp);
+    __syncthreads();
 #pragma unroll
-    for (int c = 0; c < NK; ++c) accumulate<R>(aq[c], dS, ring.next(), ty, tx);
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float g = Block<BR>::get(red, R * ty + i, tx + 16 * j);
+        dS[(R * ty + i) * LD + tx + 16 * j] = pr[i][j] == 0.f ? 0.f : pr[i][j] * (g + dd[i]);
+      }
+#pragma unroll
+    for (int c = 0; c < NK; ++c) blk.accumulate(aq[c], dS, ring.next());
   }
   copies_wait<0>();
+#pragma unroll
+  for (int c = 0; c < NK; ++c) blk.add_up(red, aq[c]);
+  if (blk.grp != 0) return;
   float* dq = static_cast<float*>(p.dq) + bh * p.Nq * dk;
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const long long row = i0 + R * ty + i;
+  for (int i = 0; i < 4; ++i) {
+    const long long row = i0 + 4 * blk.ty + i;
     if (row >= p.Nq) continue;
 #pragma unroll
     for (int c = 0; c < NK; ++c)
@@ -381,31 +422,31 @@ __global__ void __launch_bounds__(256) fa_latent_bwd_dkr_kernel(const float* __r
   store(dkr + i, x);
 }
 
-template <int NK, int NV, int R>
-cudaError_t launch_r(const LatentBwd& p, cudaStream_t s) {
-  constexpr int SMEM = bwd_smem<NK, NV, R>();
+template <int NK, int NV, int BR>
+cudaError_t launch_rows(const LatentBwd& p, cudaStream_t s) {
+  constexpr int SMEM = bwd_smem<NK, NV, BR>();
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
-  cudaError_t e =
-      cudaFuncSetAttribute(fa_latent_bwd_dkdv_kernel<NK, NV, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  static seq::SmemOnce once_kv, once_q;
+  cudaError_t e = once_kv(fa_latent_bwd_dkdv_kernel<NK, NV, BR>, SMEM);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(fa_latent_bwd_dq_kernel<NK, NV, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  e = once_q(fa_latent_bwd_dq_kernel<NK, NV, BR>, SMEM);
   if (e != cudaSuccess) return e;
   const long long bh = static_cast<long long>(p.B) * p.H;
-  const long long kb = bh * ((p.Nk + 16 * R - 1) / (16 * R)), qb = bh * ((p.Nq + 16 * R - 1) / (16 * R));
+  const long long kb = bh * ((p.Nk + BR - 1) / BR), qb = bh * ((p.Nq + BR - 1) / BR);
   if (kb > 0x7fffffffLL || qb > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const int vec = p.dn % 4 == 0 && p.dr % 4 == 0 && p.dv % 4 == 0;  // 16-byte rows
-  fa_latent_bwd_dkdv_kernel<NK, NV, R><<<static_cast<unsigned>(kb), kThreads, SMEM, s>>>(p, vec);
+  fa_latent_bwd_dkdv_kernel<NK, NV, BR><<<static_cast<unsigned>(kb), kThreads, SMEM, s>>>(p, vec);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fa_latent_bwd_dq_kernel<NK, NV, R><<<static_cast<unsigned>(qb), kThreads, SMEM, s>>>(p, vec);
+  fa_latent_bwd_dq_kernel<NK, NV, BR><<<static_cast<unsigned>(qb), kThreads, SMEM, s>>>(p, vec);
   return cudaGetLastError();
 }
-// 64 rows a CTA where that fills the SMs, else 32 (which take less time each)
+// 64 rows a CTA where that fills the SMs, else 32 or 16 (which take less time each)
 template <int NK, int NV>
 cudaError_t launch_nkv(const LatentBwd& p, cudaStream_t s) {
-  const long long n = p.Nk < p.Nq ? p.Nk : p.Nq;
-  return static_cast<long long>(p.B) * p.H * ((n + 63) / 64) >= 152 ? launch_r<NK, NV, 4>(p, s)
-                                                                    : launch_r<NK, NV, 2>(p, s);
+  const long long n = p.Nk < p.Nq ? p.Nk : p.Nq, bh = static_cast<long long>(p.B) * p.H;
+  if (bh * ((n + 63) / 64) >= 152) return launch_rows<NK, NV, 64>(p, s);
+  return bh * ((n + 31) / 32) >= 152 ? launch_rows<NK, NV, 32>(p, s) : launch_rows<NK, NV, 16>(p, s);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

@@ -204,8 +204,8 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
   a.part0 = 0;
   b.splits = w.splits_b;
   b.part0 = w.splits_a;
-  cudaError_t e = launch_seq_simt(a, s);
-  if (e == cudaSuccess) e = launch_seq_simt(b, s);
+  cudaError_t e = launch_seq_simt(a, false, s);
+  if (e == cudaSuccess) e = launch_seq_simt(b, true, s);
   if (e == cudaSuccess)
     e = launch_seq_combine(a.part_o, a.part_lse, w.splits_a + w.splits_b, p.total, d, static_cast<float*>(o), lse, s);
   return of(e);
@@ -282,7 +282,7 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
   p.splits = w.splits_a;
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.off_lse);
   if (w.splits_a == 1) p.part_o = p.part_lse = nullptr;
-  const cudaError_t e = launch_seq_simt(p, s);
+  const cudaError_t e = launch_seq_simt(p, false, s);
   if (e != cudaSuccess || w.splits_a == 1) return of(e);
   return of(launch_seq_combine(p.part_o, p.part_lse, w.splits_a, p.total, dc, static_cast<float*>(o), lse, s));
 }
@@ -323,7 +323,7 @@ fa_status fa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, c
   p.wait_ns = device_wait_ns();
   if (device_status_ptr(&p.status) != cudaSuccess) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return of(dt == FA_DTYPE_BF16 ? launch_seq_rows(p, s) : launch_seq_simt(p, s));
+  return of(dt == FA_DTYPE_BF16 ? launch_seq_rows(p, s) : launch_seq_simt(p, false, s));
 }
 
 size_t fa_bwd_latent_workspace_bytes(int B, int H, int Nq, int Nk, int dn, int dr, int dv) {

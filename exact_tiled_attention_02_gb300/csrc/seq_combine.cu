@@ -12,7 +12,7 @@
 // so that the parts' loads do not wait for one another.
 #include <cmath>
 
-#include "seq_kernels.h"
+#include "seq_sm103.cuh"
 
 namespace fa {
 namespace {
@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   const long long idx = static_cast<long long>(blockIdx.x) * kWarps + warp;
   const long long row = idx / slices;
   const int slice = static_cast<int>(idx % slices);
+  seq::pdl_wait();
   if (row >= total) return;
   const float mine = lane < splits ? part_lse[lane * total + row] : -INFINITY;
   float m = mine;
@@ -61,9 +62,8 @@ cudaError_t launch_seq_combine(const float* part_o, const float* part_lse, int s
                                float* o, float* lse, cudaStream_t s) {
   const long long blocks = (total * ((dv + 31) / 32) + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  fa_seq_combine_kernel<<<static_cast<unsigned>(blocks), kWarps * 32, 0, s>>>(part_o, part_lse, splits, total, dv, o,
-                                                                              lse);
-  return cudaGetLastError();
+  return seq::launch_after(fa_seq_combine_kernel, static_cast<unsigned>(blocks), kWarps * 32, 0, s, part_o, part_lse,
+                           splits, total, dv, o, lse);
 }
 
 }  // namespace fa

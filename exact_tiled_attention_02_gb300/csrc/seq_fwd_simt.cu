@@ -10,16 +10,16 @@
 // One CTA of 256 threads per TR query rows (64, 32 or 16, by the group's row
 // count) and split of the keys; tiles of 64 keys.  The queries stay in shared
 // memory; keys and values stream through a ring of 64 x 64 chunks, copied
-// asynchronously up to three chunks ahead.  Thread (ty, tx): rows
-// TR/16 ty .., keys tx + 16 j of S, columns 4 tx .. of every chunk of O.
-// Calls with few rows are bound by the latency of their chunks, one after the
-// other (the keys are split until every CTA has about one tile); many rows by
-// shared memory (8 reads of 16 bytes for 64 multiply-adds).
+// asynchronously up to three chunks ahead.  Products go in 4 x 4 blocks a
+// thread (seq_simt.cuh); the scores pass through shared memory, where the
+// softmax takes them a half-warp a row.
+// Calls with few rows are bound by the latency of one tile's chunks (the keys
+// are split until every CTA has about one tile), many rows by the multiply-adds.
 #include <cmath>
 
 #include "seq_kernels.h"
 #include "seq_simt.cuh"
-#include "sm103.cuh"
+#include "seq_sm103.cuh"
 
 namespace fa {
 namespace {
@@ -45,18 +45,25 @@ __device__ __forceinline__ long long out_row(const SeqAttn& p, int g, int r) {
 }
 
 // NCV: 64-column chunks of O a thread holds (dv <= 64 NCV)
-template <int TR, int NCV>
-__global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn p, int vec) {
-  constexpr int RPT = TR / 16;
+// VEC: every row and part begins on a 16-byte boundary
+template <int TR, int NCV, bool VEC>
+__global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const __grid_constant__ SeqAttn p) {
+  constexpr bool vec = VEC;
+  constexpr int RPT = TR / 16;  // rows of the softmax a half-warp
+  constexpr int G = Block<TR>::G;
   extern __shared__ float4 smem4[];
+  seq::pdl_launch();  // the merge waits for this kernel's end before it reads
   float* ring = reinterpret_cast<float*>(smem4);  // [DEPTH] chunks of keys or values
   float* Ps = ring + DEPTH * CHUNK;               // [TR][LD]
-  float* Qs = Ps + TR * LD;                       // [chunks of dk][TR][LD]
+  float* red = Ps + TR * LD;                      // [G][TR][LD] scores, partial sums
+  float* row_alpha = red + G * TR * LD;           // [TR] factor of a row's O, then 1 / its sum
+  float* Qs = row_alpha + TR;                     // [chunks of dk][TR][LD]
   const int row_tiles = (p.rows + TR - 1) / TR;
   const int g = blockIdx.x / row_tiles;
   const int r0 = (blockIdx.x % row_tiles) * TR;
   const int split = blockIdx.y;
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const Block<TR> blk;
   const int dk = p.d1 + p.d2, nck = (dk + T64 - 1) / T64, ncv = (p.dv + T64 - 1) / T64;
   const float* q = static_cast<const float*>(p.q);
   const float* k1 = static_cast<const float*>(p.k1);
@@ -77,37 +84,39 @@ __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn
   const int t0 = static_cast<int>(static_cast<long long>(tiles) * split / p.splits);
   const int t1 = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / p.splits);
 
-  // this thread's four rows of a tile of keys: where they are (-1: no such key, reads as zero)
-  long long krow[4], krow2[4];
+  // this thread's four rows of a tile of keys (null: no such key, reads as zero)
+  const float *kp[4], *k2p[4], *vp[4];
   auto place = [&](int tile) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = tile * BK + ty + 16 * i;
-      krow[i] = krow2[i] = -1;
-      if (j < nk) {
-        krow[i] = static_cast<long long>(g) * p.n_keys + j;
-        krow2[i] = static_cast<long long>(g / p.k2_div) * p.n_keys + j;
-        if (p.page_size > 0) {
-          const int at = j / p.page_size;
-          const int page = p.table != nullptr ? p.table[static_cast<long long>(g) * p.max_pages + at] : g;
-          const bool bad = page < 0 || page >= p.n_pages;
-          if (bad) atomicOr(p.status, sm103::kStatusInput);
-          krow[i] = bad ? -1 : static_cast<long long>(page) * p.page_size + (j - at * p.page_size);
+      kp[i] = nullptr;
+      if (j >= nk) continue;
+      long long row = static_cast<long long>(g) * p.n_keys + j;
+      k2p[i] = k2 + (static_cast<long long>(g / p.k2_div) * p.n_keys + j) * p.d2;
+      if (p.page_size > 0) {
+        const int at = j / p.page_size;
+        const int page = p.table != nullptr ? p.table[static_cast<long long>(g) * p.max_pages + at] : g;
+        if (page < 0 || page >= p.n_pages) {
+          atomicOr(p.status, sm103::kStatusInput);
+          continue;
         }
+        row = static_cast<long long>(page) * p.page_size + (j - at * p.page_size);
       }
+      kp[i] = k1 + row * p.d1;
+      vp[i] = v + row * p.v_stride;
     }
   };
-  // chunk `stage` of the tile that krow describes (keys first, then values) to ring slot `slot`
+  // chunk `stage` of the tile that was placed (keys first, then values) to ring slot `slot`
   auto fetch = [&](int stage, int slot) {
     float* dst = ring + slot * CHUNK + ty * LD + 4 * tx;
 #pragma unroll
     for (int i = 0; i < 4; ++i, dst += 16 * LD) {
-      const bool on = krow[i] >= 0;
+      const bool on = kp[i] != nullptr;
       if (stage < nck)
-        copy_row4(dst, k1 + (on ? krow[i] * p.d1 : 0), p.d1, k2 + (on ? krow2[i] * p.d2 : 0), p.d2, on,
-                  stage * T64 + 4 * tx, vec);
+        copy_row4(dst, on ? kp[i] : k1, p.d1, on ? k2p[i] : k2, p.d2, on, stage * T64 + 4 * tx, vec);
       else
-        copy_row4(dst, v + (on ? krow[i] * p.v_stride : 0), on, (stage - nck) * T64 + 4 * tx, p.dv, vec);
+        copy_row4(dst, on ? vp[i] : v, on, (stage - nck) * T64 + 4 * tx, p.dv, vec);
     }
   };
   // the stream: nck + ncv chunks a tile; (f_tile, f_stage) is the next one to ask for, into slot f_slot
@@ -134,16 +143,17 @@ __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn
     ask();
     return chunk;
   };
-  for (int c = 0; c < nck; ++c)
-#pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      const int r = r0 + ty + 16 * i;
-      const bool on = r < p.rows;
-      copy_row4(Qs + (c * TR + ty + 16 * i) * LD + 4 * tx, q + (on ? out_row(p, g, r) * dk : 0), on, c * T64 + 4 * tx,
-                dk, vec);
-    }
+#pragma unroll 1
+  for (int i = 0; i < RPT; ++i) {
+    const int r = r0 + ty + 16 * i;
+    const bool on = r < p.rows;
+    const float* row = q + (on ? out_row(p, g, r) * dk : 0);
+#pragma unroll 1
+    for (int c = 0; c < nck; ++c)
+      copy_row4(Qs + (c * TR + ty + 16 * i) * LD + 4 * tx, row, on, c * T64 + 4 * tx, dk, vec);
+  }
   // (the queries travel in the first chunk's group)
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < DEPTH - 1; ++c) ask();
   int limit[RPT];  // keys that the thread's rows see
 #pragma unroll
@@ -151,112 +161,150 @@ __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const SeqAttn
     const int r = r0 + RPT * ty + i;
     limit[i] = r < p.rows ? (p.causal ? nk - (p.n_new - 1 - r % p.n_new) : nk) : 0;
   }
-  float m[RPT], l[RPT], acc[NCV][RPT][4];
+  float m[RPT], l[RPT], acc[NCV][4][4];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
+  }
 #pragma unroll
-    for (int c = 0; c < NCV; ++c)
+  for (int c = 0; c < NCV; ++c)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[c][i][e] = 0.f;
-  }
 
+#pragma unroll 1
   for (int kt = t0; kt < t1; ++kt) {
     const int k0 = kt * BK;
-    float s[RPT][4];
+    float s[4][4];
 #pragma unroll
-    for (int i = 0; i < RPT; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-    for (int c = 0; c < nck; ++c)
-      dot<RPT>(s, Qs + c * TR * LD, next(), (min(T64, dk - c * T64) + 3) >> 2, ty, tx);
+#pragma unroll 1
+    for (int c = 0; c < nck + ncv; ++c) {
+      const float* chunk = next();  // (also makes P and the rows' factors visible)
+      if (c < nck) blk.dot(s, Qs + c * TR * LD, chunk, (min(T64, dk - c * T64) + 3) >> 2);
+      if (c == nck) {
 #pragma unroll
-    for (int i = 0; i < RPT; ++i) {
-      float tmax = -INFINITY;
+        for (int i = 0; i < 4; ++i) {
+          const float a = row_alpha[4 * blk.ty + i];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = k0 + tx + 16 * j < limit[i] ? s[i][j] * p.scale : -INFINITY;
-        tmax = fmaxf(tmax, s[i][j]);
+          for (int e = 0; e < NCV; ++e)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[e][i][x] *= a;
+        }
       }
-      const float m_new = fmaxf(m[i], half_warp_max(tmax));
-      const float ref = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = expf(m[i] - ref);  // 0 while the row has seen no key
-      float rs = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float pv = expf(s[i][j] - ref);
-        rs += pv;
-        Ps[(RPT * ty + i) * LD + tx + 16 * j] = pv;
+      for (int e = 0; e < NCV; ++e)
+        if (c == nck + e) blk.accumulate(acc[e], Ps, chunk);
+      if (c != nck - 1) continue;
+      blk.put_dot(red, s);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const int r = RPT * ty + i;
+        float tmax = -INFINITY, x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float sc = Block<TR>::get(red, r, tx + 16 * j);
+          x[j] = k0 + tx + 16 * j < limit[i] ? sc * p.scale : -INFINITY;
+          tmax = fmaxf(tmax, x[j]);
+        }
+        const float m_new = fmaxf(m[i], half_warp_max(tmax));
+        const float ref = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = expf(m[i] - ref);  // 0 while the row has seen no key
+        float rs = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float pv = expf(x[j] - ref);
+          rs += pv;
+          Ps[r * LD + tx + 16 * j] = pv;
+        }
+        l[i] = l[i] * alpha + half_warp_sum(rs);
+        m[i] = m_new;
+        if (tx == 0) row_alpha[r] = alpha;
       }
-      l[i] = l[i] * alpha + half_warp_sum(rs);
-      m[i] = m_new;
+    }
+  }
+  copies_wait<0>();
+#pragma unroll
+  for (int c = 0; c < NCV; ++c)
+    if (c < ncv) blk.add_up(red, acc[c]);
+  __syncthreads();  // row_alpha is no longer read
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = RPT * ty + i;
+    if (tx == 0) {
+      row_alpha[r] = l[i] == 0.f ? 0.f : 1.f / l[i];  // no key: 0
+      if (r0 + r < p.rows) {
+        const long long row = out_row(p, g, r0 + r);
+        const float lse = m[i] + logf(l[i]);  // no key: -inf
+        if (p.part_o != nullptr)
+          p.part_lse[(p.part0 + split) * p.total + row] = lse;
+        else if (p.lse != nullptr)
+          p.lse[row] = lse;
+      }
+    }
+  }
+  __syncthreads();
+  if (blk.grp == 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * blk.ty + i;
+      if (r0 + r >= p.rows) continue;
+      const long long row = out_row(p, g, r0 + r);
+      const float inv = row_alpha[r];
+      float* dst = p.part_o != nullptr ? p.part_o + ((p.part0 + split) * p.total + row) * p.dv
+                                       : static_cast<float*>(p.o) + row * p.dv;
 #pragma unroll
       for (int c = 0; c < NCV; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[c][i][e] *= alpha;
-    }
-#pragma unroll
-    for (int c = 0; c < NCV; ++c)
-      if (c < ncv) accumulate<RPT>(acc[c], Ps, next(), ty, tx);  // next() also makes P visible
-  }
-  copies_wait<0>();
-
-#pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    const int r = r0 + RPT * ty + i;
-    if (r >= p.rows) continue;
-    const long long row = out_row(p, g, r);
-    const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];  // no key: 0
-    const float lse = m[i] + logf(l[i]);               // no key: -inf
-    const long long prow = (p.part0 + split) * p.total + row;
-    float* dst = p.part_o != nullptr ? p.part_o + prow * p.dv : static_cast<float*>(p.o) + row * p.dv;
-#pragma unroll
-    for (int c = 0; c < NCV; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = c * T64 + 4 * tx + e;
-        if (d < p.dv) dst[d] = acc[c][i][e] * inv;
-      }
-    if (tx == 0) {
-      if (p.part_o != nullptr)
-        p.part_lse[prow] = lse;
-      else if (p.lse != nullptr)
-        p.lse[row] = lse;
+        for (int e = 0; e < 4; ++e) {
+          const int d = c * T64 + 4 * tx + e;
+          if (d < p.dv) dst[d] = acc[c][i][e] * inv;
+        }
     }
   }
+  seq::pdl_wait();  // a kernel of the same call may run beside this one: the merge waits for both
 }
 
-template <int TR, int NCV>
-cudaError_t launch_one(const SeqAttn& p, cudaStream_t s) {
+template <int TR, int NCV, bool VEC>
+cudaError_t launch_vec(const SeqAttn& p, bool beside, cudaStream_t s) {
   const int nck = (p.d1 + p.d2 + T64 - 1) / T64;
-  const int smem = (DEPTH * CHUNK + TR * LD * (1 + nck)) * 4;
+  const int smem = (DEPTH * CHUNK + TR * LD * (1 + nck) + 64 * LD + TR) * 4;
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(fa_seq_fwd_simt_kernel<TR, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static seq::SmemOnce once;
+  const cudaError_t e = once(fa_seq_fwd_simt_kernel<TR, NCV, VEC>, 227 * 1024);
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.groups) * ((p.rows + TR - 1) / TR);
   if (blocks > 0x7fffffffLL || p.splits > 65535) return cudaErrorInvalidConfiguration;
-  // 16-byte loads where every row and part begins on a 16-byte boundary
-  const int vec = p.d1 % 4 == 0 && p.d2 % 4 == 0 && p.dv % 4 == 0 && p.v_stride % 4 == 0;
-  fa_seq_fwd_simt_kernel<TR, NCV><<<dim3(static_cast<unsigned>(blocks), p.splits), kThreads, smem, s>>>(p, vec);
+  const dim3 grid(static_cast<unsigned>(blocks), p.splits);
+  if (beside) return seq::launch_after(fa_seq_fwd_simt_kernel<TR, NCV, VEC>, grid, kThreads, smem, s, p);
+  fa_seq_fwd_simt_kernel<TR, NCV, VEC><<<grid, kThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
+template <int TR, int NCV>
+cudaError_t launch_one(const SeqAttn& p, bool beside, cudaStream_t s) {
+  const bool vec = p.d1 % 4 == 0 && p.d2 % 4 == 0 && p.dv % 4 == 0 && p.v_stride % 4 == 0;
+  return vec ? launch_vec<TR, NCV, true>(p, beside, s) : launch_vec<TR, NCV, false>(p, beside, s);
+}
+
 template <int TR>
-cudaError_t launch_tr(const SeqAttn& p, cudaStream_t s) {
-  if (p.dv <= 64) return launch_one<TR, 1>(p, s);
-  if (p.dv <= 128) return launch_one<TR, 2>(p, s);
-  if (p.dv <= 256) return launch_one<TR, 4>(p, s);
-  if (p.dv <= 512) return launch_one<TR, 8>(p, s);
+cudaError_t launch_tr(const SeqAttn& p, bool beside, cudaStream_t s) {
+  if (p.dv <= 64) return launch_one<TR, 1>(p, beside, s);
+  if (p.dv <= 128) return launch_one<TR, 2>(p, beside, s);
+  if (p.dv <= 256) return launch_one<TR, 4>(p, beside, s);
+  if (p.dv <= 512) return launch_one<TR, 8>(p, beside, s);
   return cudaErrorInvalidValue;
 }
 
-// Rows of a CTA: 64 unless that leaves SMs idle (a CTA with fewer rows takes
-// less time, though more for each row: 2300, 1300 and 1200 cycles a chunk for
-// 64, 32 and 16 rows).
+// Rows of a CTA: 64 unless that leaves SMs idle (a chunk costs a CTA with 32
+// or 16 rows less, though more for each row).
 int rows_per_cta(long long groups, int rows, int splits, int dk) {
-  for (int tr = dk > 512 ? 32 : 64; tr > 16; tr /= 2)  // (64 wider rows would not fit shared memory)
+  for (int tr = dk > 448 ? 32 : 64; tr > 16; tr /= 2)  // (64 wider rows would not fit shared memory)
     if (rows > tr / 2 && groups * ((rows + tr - 1) / tr) * splits >= 152) return tr;
   return 16;
 }
@@ -273,13 +321,13 @@ int seq_simt_splits(long long groups, int rows, int max_keys) {
   return n < 1 ? 1 : static_cast<int>(n);
 }
 
-cudaError_t launch_seq_simt(const SeqAttn& args, cudaStream_t s) {
+cudaError_t launch_seq_simt(const SeqAttn& args, bool beside, cudaStream_t s) {
   SeqAttn p = args;
   if (p.k2 == nullptr) p.k2 = p.k1;  // never read: copies of nothing still name an address
   switch (rows_per_cta(p.groups, p.rows, p.splits, p.d1 + p.d2)) {
-    case 16: return launch_tr<16>(p, s);
-    case 32: return launch_tr<32>(p, s);
-    default: return launch_tr<64>(p, s);
+    case 16: return launch_tr<16>(p, beside, s);
+    case 32: return launch_tr<32>(p, beside, s);
+    default: return launch_tr<64>(p, beside, s);
   }
 }
 

@@ -51,8 +51,9 @@ struct SeqAttn {
   unsigned long long wait_ns;
 };
 
-// float32 on CUDA cores (seq_fwd_simt.cu).
-cudaError_t launch_seq_simt(const SeqAttn& p, cudaStream_t s);
+// float32 on CUDA cores (seq_fwd_simt.cu).  beside: the kernel before it on the
+// stream is the same call's and independent.
+cudaError_t launch_seq_simt(const SeqAttn& p, bool beside, cudaStream_t s);
 // Splits of the keys that give the launch enough blocks.
 int seq_simt_splits(long long groups, int rows, int max_keys);
 
@@ -77,7 +78,7 @@ struct DecodePlan {
 };
 DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box);
 size_t decode_slots(const DecodePlan& w);  // rows of part_o
-// beside: the kernel before it on the stream is the same call's and independent
+// beside: as launch_seq_simt
 cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, bool beside, cudaStream_t s);
 // o, lse = the pieces merged, with the partial results pre_o [pre][total][dv] of other keys
 cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
