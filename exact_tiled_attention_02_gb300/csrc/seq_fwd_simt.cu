@@ -50,13 +50,12 @@ template <int TR, int NCV, bool VEC>
 __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const __grid_constant__ SeqAttn p) {
   constexpr bool vec = VEC;
   constexpr int RPT = TR / 16;  // rows of the softmax a half-warp
-  constexpr int G = Block<TR>::G;
   extern __shared__ float4 smem4[];
   seq::pdl_launch();  // the merge waits for this kernel's end before it reads
   float* ring = reinterpret_cast<float*>(smem4);  // [DEPTH] chunks of keys or values
-  float* Ps = ring + DEPTH * CHUNK;               // [TR][LD]
-  float* red = Ps + TR * LD;                      // [G][TR][LD] scores, partial sums
-  float* row_alpha = red + G * TR * LD;           // [TR] factor of a row's O, then 1 / its sum
+  float* red = ring + DEPTH * CHUNK;              // [G][TR][LD] the groups' scores, or sums
+  float* Ps = red;                                // [TR][LD] P: an entry replaces group 0's score of the same thread
+  float* row_alpha = red + T64 * LD;           // [TR] factor of a row's O, then 1 / its sum
   float* Qs = row_alpha + TR;                     // [chunks of dk][TR][LD]
   const int row_tiles = (p.rows + TR - 1) / TR;
   const int g = blockIdx.x / row_tiles;
@@ -273,7 +272,7 @@ __global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const __grid_
 template <int TR, int NCV, bool VEC>
 cudaError_t launch_vec(const SeqAttn& p, bool beside, cudaStream_t s) {
   const int nck = (p.d1 + p.d2 + T64 - 1) / T64;
-  const int smem = (DEPTH * CHUNK + TR * LD * (1 + nck) + 64 * LD + TR) * 4;
+  const int smem = (DEPTH * CHUNK + TR * LD * nck + 64 * LD + TR) * 4;
   if (smem > 227 * 1024) return cudaErrorInvalidValue;
   static seq::SmemOnce once;
   const cudaError_t e = once(fa_seq_fwd_simt_kernel<TR, NCV, VEC>, 227 * 1024);
@@ -304,7 +303,7 @@ cudaError_t launch_tr(const SeqAttn& p, bool beside, cudaStream_t s) {
 // Rows of a CTA: 64 unless that leaves SMs idle (a chunk costs a CTA with 32
 // or 16 rows less, though more for each row).
 int rows_per_cta(long long groups, int rows, int splits, int dk) {
-  for (int tr = dk > 448 ? 32 : 64; tr > 16; tr /= 2)  // (64 wider rows would not fit shared memory)
+  for (int tr = dk > 512 ? 32 : 64; tr > 16; tr /= 2)  // (64 wider rows would not fit shared memory)
     if (rows > tr / 2 && groups * ((rows + tr - 1) / tr) * splits >= 152) return tr;
   return 16;
 }
@@ -315,7 +314,7 @@ int seq_simt_splits(long long groups, int rows, int max_keys) {
   const int tr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   const long long blocks = groups * ((rows + tr - 1) / tr);
   const int tiles = (max_keys + BK - 1) / BK;
-  long long n = (4 * 152 + blocks - 1) / blocks;
+  long long n = 2 * 152 / blocks;  // two CTAs an SM: a second round costs more than a second tile
   if (n > tiles) n = tiles;
   if (n > 64) n = 64;
   return n < 1 ? 1 : static_cast<int>(n);
