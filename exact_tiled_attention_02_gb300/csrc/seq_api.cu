@@ -53,16 +53,51 @@ PartLayout prefix_layout(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) 
 }
 // bf16: the prefix's splits [splits][rows], then the pieces of the sequences
 struct PrefixLayout {
-  int splits;
+  int splits, ctas;  // of the prefix's part
   DecodePlan plan;
   size_t off_pre_lse, off_o, off_lse, bytes;
 };
+// The prefix's part is bound by the tensor cores, the sequences' own part by
+// memory, and a CTA of the first takes a whole SM: so they run side by side on
+// SMs of their own (n and 152 - n) where that is faster than one after the
+// other, by measured rates: the first as seq_rows_time, the second 5 us and 90
+// GB/s an SM up to 6.2 TB/s of keys and values (taking every sequence as three
+// quarters of its room), the merge 4 us and 5 TB/s of partial results.
+// (128 x 32 heads x 4 tokens, 32768 + 2048 keys, d = 128: 332 us one after the
+// other; the sum of both alone is 318 + 16.)
 PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   PrefixLayout w{};
-  const int G = Hq / Hkv;
+  const int G = Hq / Hkv, R = B * G * Nq, block = G * Nq, kSms = 152;
   const size_t rows = static_cast<size_t>(B) * Hq * Nq;
-  w.splits = Np > 0 ? seq_rows_splits(Hkv, B * G * Nq, G * Nq, Np) : 0;
-  w.plan = decode_plan(B, Hkv, G * Nq, false, 64);
+  const double own = 0.75 * 4.0 * B * Hkv * d * Ns;  // bytes of the sequences' keys and values
+  auto own_time = [&](int sms) {
+    const double rate = 0.09e6 * sms < 6.2e6 ? 0.09e6 * sms : 6.2e6;
+    return own > 0 ? 5.0 + own / rate : 0.0;
+  };
+  int own_sms = kSms;
+  if (Np > 0) {
+    const int items = seq_rows_items(Hkv, R, block), tiles = (Np + 127) / 128;
+    double best = 1e30;
+    for (int n = kSms; n >= 8; n -= 8) {
+      if (n < kSms && Ns == 0) break;
+      for (int k = 1; k <= 4; ++k) {  // rounds of items to aim at
+        int s = static_cast<int>(static_cast<long long>(k) * n / items);
+        if (s < 1) s = 1;
+        if (s > tiles) s = tiles;
+        if (s > 64) s = 64;
+        const double r = seq_rows_time(Hkv, R, block, Np, d, n, s);
+        const double merge = 4.0 + static_cast<double>(s) * rows * d * 8.0 / 5e6;
+        const double t = merge + (n == kSms ? r + own_time(kSms) : r > own_time(kSms - n) ? r : own_time(kSms - n));
+        if (t < best) {
+          best = t;
+          w.splits = s;
+          w.ctas = n;
+        }
+      }
+    }
+    if (w.ctas < kSms) own_sms = kSms - w.ctas;
+  }
+  w.plan = decode_plan(B, Hkv, block, false, 64, own_sms);
   const size_t slots = Ns > 0 ? decode_slots(w.plan) : 0;
   w.off_pre_lse = up256(w.splits * rows * d * 4);
   w.off_o = w.off_pre_lse + up256(w.splits * rows * 4);
@@ -88,7 +123,7 @@ PartLayout absorbed_layout_bf16(const DecodePlan& plan, int dc) {
 }
 DecodePlan absorbed_plan(int B, int H, int Nq, int page_size, bool table) {
   const int box = !table || page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
-  return decode_plan(B, 1, H * Nq, true, box);
+  return decode_plan(B, 1, H * Nq, true, box, 152);
 }
 // tokens a sequence can hold, or -1
 long long absorbed_keys(int page_size, int max_pages) {
@@ -189,6 +224,7 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
     a.part_o = reinterpret_cast<float*>(base);
     a.part_lse = reinterpret_cast<float*>(base + w.off_pre_lse);
     a.splits = w.splits;
+    a.ctas = w.ctas;
     b.part_o = reinterpret_cast<float*>(base + w.off_o);
     b.part_lse = reinterpret_cast<float*>(base + w.off_lse);
     cudaError_t e = cudaSuccess;

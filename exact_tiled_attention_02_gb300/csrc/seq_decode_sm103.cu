@@ -839,13 +839,13 @@ cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre
 
 }  // namespace
 
-DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box) {
+DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box, int sms) {
   DecodePlan w{};
   w.n_seq = n_seq;
   w.heads = heads;
   w.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   w.row_groups = (rows + w.nr - 1) / w.nr;
-  const int ctas = shared || w.nr == 64 ? 152 : 304;  // one CTA an SM, or two
+  const int ctas = shared || w.nr == 64 ? sms : 2 * sms;  // one CTA an SM, or two
   const long long groups = static_cast<long long>(heads) * w.row_groups;
   w.cuts = groups < ctas ? static_cast<int>(ctas / groups) : 1;
   w.direct = shared;

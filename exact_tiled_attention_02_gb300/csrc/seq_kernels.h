@@ -47,6 +47,7 @@ struct SeqAttn {
   float* part_lse;
   int part0;
   long long total;  // rows of o
+  int ctas;         // rows kernel: at most so many CTAs (0: one an SM)
   unsigned int* status;
   unsigned long long wait_ns;
 };
@@ -61,7 +62,10 @@ int seq_simt_splits(long long groups, int rows, int max_keys);
 // pages; the expanded latent shape to o and lse, or d = 64, 96, 128 to partial
 // results.
 cudaError_t launch_seq_rows(const SeqAttn& p, cudaStream_t s);
-int seq_rows_splits(int groups, int rows, int row_block, int n_keys);
+// The work items of a partial-result call before its keys are split, and the
+// time (us) it takes on n CTAs.
+int seq_rows_items(int groups, int rows, int row_block);
+double seq_rows_time(int groups, int rows, int row_block, int n_keys, int d, int n, int splits);
 
 // bf16 on the tensor cores, few rows a group over (paged) caches
 // (seq_decode_sm103.cu).  Groups are (sequence, head) pairs, lens per
@@ -76,7 +80,7 @@ struct DecodePlan {
   int direct;      // keys and values shared (the latent form): whole sequences go straight to o and lse
   int box;         // tokens of one load: 64, or 32 or 16 where pages are not whole tiles
 };
-DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box);
+DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box, int sms);
 size_t decode_slots(const DecodePlan& w);  // rows of part_o
 // beside: as launch_seq_simt
 cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, bool beside, cudaStream_t s);

@@ -612,9 +612,10 @@ cudaError_t launch_rows(const SeqAttn& p, cudaStream_t s) {
     return cudaErrorInvalidValue;
   m.k2 = m.k;
   if (D2 > 0 && !make_map3(&m.k2, p.k2, D2, keys, p.groups / p.k2_div, BC)) return cudaErrorInvalidValue;
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int grid = w.n_items < sms ? w.n_items : sms;
+  int ctas = sm_count();
+  if (ctas <= 0) return cudaErrorInvalidDevice;
+  if (p.ctas > 0 && p.ctas < ctas) ctas = p.ctas;
+  const int grid = w.n_items < ctas ? w.n_items : ctas;
   fa_seq_rows_sm103_kernel<DQK, DV, D2, PART><<<grid, kThreads, C::SMEM_BYTES, s>>>(m, p, w);
   return cudaGetLastError();
 }
@@ -630,24 +631,17 @@ cudaError_t launch_seq_rows(const SeqAttn& p, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-int seq_rows_splits(int groups, int rows, int row_block, int n_keys) {
-  const int tiles = (n_keys + BC - 1) / BC;
+// How long the prefix's part takes (us) on n CTAs, its keys in `splits`
+// ranges.  Measured at d = 128: 7.5 us to launch, load and write out, 1.45 us
+// a 128-key tile of two query tiles; 1.5 us a further item.
+double seq_rows_time(int groups, int rows, int row_block, int n_keys, int d, int n, int splits) {
   const RowsPlan w = rows_plan(rows, row_block, false);
-  const long long items = static_cast<long long>(w.pairs) * groups;
-  // the share of the SMs' time that whole rounds of items fill, against the
-  // partial results that more splits write and merge (a hundredth each)
-  int best = 1;
-  double top = -1.0;
-  for (int n = 1; n <= tiles && n <= 152; ++n) {
-    const long long all = items * n, rounds = (all + 151) / 152;
-    const double per = static_cast<double>((tiles + n - 1) / n) * n / tiles;  // the longest split over the mean
-    const double score = static_cast<double>(all) / (152.0 * rounds) / per - 0.01 * static_cast<double>(rows) / 1024 * n;
-    if (score > top) {
-      top = score;
-      best = n;
-    }
-  }
-  return best;
+  const long long items = static_cast<long long>(w.pairs) * groups * splits;
+  const int tiles = (n_keys + BC - 1) / BC;
+  const double rounds = static_cast<double>((items + n - 1) / n);
+  const double tile = 0.35 + 0.0086 * d;
+  return 7.5 + rounds * ((tiles + splits - 1) / splits * tile) + (rounds - 1.0) * 1.5;
 }
+int seq_rows_items(int groups, int rows, int row_block) { return rows_plan(rows, row_block, false).pairs * groups; }
 
 }  // namespace fa
