@@ -88,6 +88,7 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -334,10 +335,10 @@ def _at(t):
 
 
 def _need(name, t, shape, dtype, device):
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {device}, "
-                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
-    return t
+    if t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return t
+    raise ValueError(f"{name} must be a contiguous {dtype} {tuple(shape)} tensor on {device}, "
+                     f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _first(name, t, dims):
@@ -352,45 +353,33 @@ def _first(name, t, dims):
     return code
 
 
-def _raw_stream(index):
-    """The handle of the device's current stream."""
+def _current_stream(device, stream):
+    """The handle of the stream a call runs on where nothing has to be made
+    current for it: no stream given, the tensors on the current device."""
     torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # 2 us less than building a Stream object
-    return torch.cuda.current_stream(index).cuda_stream if get is None else get(index)
+    if stream is not None or torch._C._cuda_getDevice() != device.index:
+        return None
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-class _running_on:
-    """The tensors' device made current, and the call's stream on it: the given
-    one, or that device's current stream; entering gives the stream's handle.
-    Tensors a call allocates are allocated on that stream (see _alloc_on).  When
-    both are current already, entering touches neither (4 us a call)."""
-
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-        self.device, self.stream, self.stack = device, stream, None
-
-    def __enter__(self):
-        torch = _torch()
-        if self.stream is None and torch.cuda.current_device() == self.device.index:
-            return _raw_stream(self.device.index)
-        self.stack = contextlib.ExitStack()
-        self.stack.enter_context(torch.cuda.device(self.device))
-        self.stack.enter_context(_alloc_on(self.stream))
-        return (torch.cuda.current_stream() if self.stream is None else self.stream).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.stack is not None:
-            self.stack.close()
+@contextlib.contextmanager
+def _made_current(device, stream):
+    """The tensors' device, and the stream if one is given, made current: the
+    call's work and the tensors it allocates go there (see _alloc_on)."""
+    torch = _torch()
+    if stream is not None and stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
+    with torch.cuda.device(device), _alloc_on(stream):
+        yield
 
 
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, like):
     torch = _torch()
     if workspace is None:
-        return torch.empty(need, device=device, dtype=torch.uint8)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace
+        return like.new_empty(need, dtype=torch.uint8), need
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def fa_fwd_shared_prefix(q, k_prefix, v_prefix, k, v, lens, scale: float | None = None, o=None, lse=None,
@@ -408,27 +397,30 @@ def fa_fwd_shared_prefix(q, k_prefix, v_prefix, k, v, lens, scale: float | None 
     """
     torch = _torch()
     code = _first("q", q, 4)
-    B, Hq, Nq, d = q.shape
+    dev = q.device
+    sp = _current_stream(dev, stream)
+    if sp is None:
+        with _made_current(dev, stream):
+            return fa_fwd_shared_prefix(q, k_prefix, v_prefix, k, v, lens, scale, o, lse, want_lse, workspace)
     if k_prefix.dim() != 3 or k.dim() != 4:
         raise ValueError("k_prefix must be [Hkv, Np, d] and k [B, Hkv, Ns, d]")
-    Hkv, Np, Ns = k_prefix.shape[0], k_prefix.shape[1], k.shape[2]
-    dev = q.device
-    for name, t, shape in (("k_prefix", k_prefix, (Hkv, Np, d)), ("v_prefix", v_prefix, (Hkv, Np, d)),
-                           ("k", k, (B, Hkv, Ns, d)), ("v", v, (B, Hkv, Ns, d))):
-        _need(name, t, shape, q.dtype, dev)
+    B, Hq, Nq, d = q.shape
+    Hkv, Np, _ = k_prefix.shape
+    Ns, t = k.shape[2], q.dtype
+    _need("k_prefix", k_prefix, (Hkv, Np, d), t, dev)
+    _need("v_prefix", v_prefix, (Hkv, Np, d), t, dev)
+    _need("k", k, (B, Hkv, Ns, d), t, dev)
+    _need("v", v, (B, Hkv, Ns, d), t, dev)
     _need("lens", lens, (B,), torch.int32, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    with _running_on(dev, stream) as sp:
-        o = torch.empty_like(q) if o is None else _need("o", o, q.shape, q.dtype, dev)
-        if lse is not None:
-            _need("lse", lse, (B, Hq, Nq), torch.float32, dev)
-        elif want_lse:
-            lse = torch.empty((B, Hq, Nq), device=dev, dtype=torch.float32)
-        ws = _workspace(workspace, fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d), dev)
-        st = lib.fa_fwd_shared_prefix(_at(q), _at(k_prefix), _at(v_prefix), _at(k), _at(v), _at(lens), _at(o),
-                                      _at(lse), B, Hq, Hkv, Nq, Np, Ns, d, float(scale), code, _at(ws),
-                                      ws.numel() * ws.element_size(), sp)
+    o = torch.empty_like(q) if o is None else _need("o", o, (B, Hq, Nq, d), t, dev)
+    if lse is not None:
+        _need("lse", lse, (B, Hq, Nq), torch.float32, dev)
+    elif want_lse:
+        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+    ws, ws_bytes = _workspace(workspace, fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d), q)
+    st = lib.fa_fwd_shared_prefix(_at(q), _at(k_prefix), _at(v_prefix), _at(k), _at(v), _at(lens), _at(o), _at(lse), B,
+                                  Hq, Hkv, Nq, Np, Ns, d, 1.0 / math.sqrt(d) if scale is None else scale, code,
+                                  _at(ws), ws_bytes, sp)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_shared_prefix")
     return o, lse
@@ -449,12 +441,15 @@ def fa_fwd_latent_absorbed(q, cache, lens, dc: int, scale: float, block_table=No
     """
     torch = _torch()
     code = _first("q", q, 4)
+    dev = q.device
+    sp = _current_stream(dev, stream)
+    if sp is None:
+        with _made_current(dev, stream):
+            return fa_fwd_latent_absorbed(q, cache, lens, dc, scale, block_table, o, lse, want_lse, workspace)
     B, H, Nq, dk = q.shape
-    dr = dk - dc
     if cache.dim() != 3 or not 0 < dc < dk:
         raise ValueError("cache must be [pages, page_size, dc + dr], with 0 < dc < dc + dr")
-    pages, page_size = cache.shape[:2]
-    dev = q.device
+    pages, page_size, _ = cache.shape
     _need("cache", cache, (pages, page_size, dk), q.dtype, dev)
     _need("lens", lens, (B,), torch.int32, dev)
     max_pages = 1
@@ -463,17 +458,14 @@ def fa_fwd_latent_absorbed(q, cache, lens, dc: int, scale: float, block_table=No
             raise ValueError("block_table must be [B, max_pages]")
         max_pages = block_table.shape[1]
         _need("block_table", block_table, (B, max_pages), torch.int32, dev)
-    with _running_on(dev, stream) as sp:
-        o = torch.empty((B, H, Nq, dc), device=dev, dtype=q.dtype) if o is None else \
-            _need("o", o, (B, H, Nq, dc), q.dtype, dev)
-        if lse is not None:
-            _need("lse", lse, (B, H, Nq), torch.float32, dev)
-        elif want_lse:
-            lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
-        ws = _workspace(workspace, fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc), dev)
-        st = lib.fa_fwd_latent_absorbed(_at(q), _at(cache), _at(block_table), _at(lens), _at(o), _at(lse), B, H,
-                                        Nq, pages, page_size, max_pages, dc, dr, float(scale), code, _at(ws),
-                                        ws.numel() * ws.element_size(), sp)
+    o = q.new_empty((B, H, Nq, dc)) if o is None else _need("o", o, (B, H, Nq, dc), q.dtype, dev)
+    if lse is not None:
+        _need("lse", lse, (B, H, Nq), torch.float32, dev)
+    elif want_lse:
+        lse = q.new_empty((B, H, Nq), dtype=torch.float32)
+    ws, ws_bytes = _workspace(workspace, fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc), q)
+    st = lib.fa_fwd_latent_absorbed(_at(q), _at(cache), _at(block_table), _at(lens), _at(o), _at(lse), B, H, Nq, pages,
+                                    page_size, max_pages, dc, dk - dc, scale, code, _at(ws), ws_bytes, sp)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_latent_absorbed")
     return o, lse
@@ -506,17 +498,17 @@ def fa_fwd_latent(q, k_nope, k_rope, v, scale: float | None = None, causal: bool
     torch = _torch()
     code, (B, H, Nq, Nk, dn, dr, dv) = _check_latent(q, k_nope, k_rope, v)
     dev = q.device
-    if scale is None:
-        scale = 1.0 / math.sqrt(dn + dr)
-    with _running_on(dev, stream) as sp:
-        o = torch.empty((B, H, Nq, dv), device=dev, dtype=q.dtype) if o is None else \
-            _need("o", o, (B, H, Nq, dv), q.dtype, dev)
-        if lse is not None:
-            _need("lse", lse, (B, H, Nq), torch.float32, dev)
-        elif want_lse:
-            lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
-        st = lib.fa_fwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), B, H, Nq, Nk, dn, dr,
-                               dv, float(scale), int(bool(causal)), code, sp)
+    sp = _current_stream(dev, stream)
+    if sp is None:
+        with _made_current(dev, stream):
+            return fa_fwd_latent(q, k_nope, k_rope, v, scale, causal, o, lse, want_lse)
+    o = q.new_empty((B, H, Nq, dv)) if o is None else _need("o", o, (B, H, Nq, dv), q.dtype, dev)
+    if lse is not None:
+        _need("lse", lse, (B, H, Nq), torch.float32, dev)
+    elif want_lse:
+        lse = q.new_empty((B, H, Nq), dtype=torch.float32)
+    st = lib.fa_fwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), B, H, Nq, Nk, dn, dr, dv,
+                           1.0 / math.sqrt(dn + dr) if scale is None else scale, bool(causal), code, sp)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_latent")
     return o, lse
@@ -531,19 +523,21 @@ def fa_bwd_latent(q, k_nope, k_rope, v, o, lse, do, scale: float | None = None, 
     torch = _torch()
     code, (B, H, Nq, Nk, dn, dr, dvw) = _check_latent(q, k_nope, k_rope, v)
     dev = q.device
+    sp = _current_stream(dev, stream)
+    if sp is None:
+        with _made_current(dev, stream):
+            return fa_bwd_latent(q, k_nope, k_rope, v, o, lse, do, scale, causal, dq, dk_nope, dk_rope, dv, workspace)
     _need("o", o, (B, H, Nq, dvw), q.dtype, dev)
     _need("do", do, (B, H, Nq, dvw), q.dtype, dev)
     _need("lse", lse, (B, H, Nq), torch.float32, dev)
-    if scale is None:
-        scale = 1.0 / math.sqrt(dn + dr)
-    with _running_on(dev, stream) as sp:
-        dq, dk_nope, dk_rope, dv = (torch.empty_like(t) if g is None else _need(name, g, t.shape, q.dtype, dev)
-                                    for name, g, t in (("dq", dq, q), ("dk_nope", dk_nope, k_nope),
-                                                       ("dk_rope", dk_rope, k_rope), ("dv", dv, v)))
-        ws = _workspace(workspace, fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dvw), dev)
-        st = lib.fa_bwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), _at(do), _at(dq),
-                               _at(dk_nope), _at(dk_rope), _at(dv), B, H, Nq, Nk, dn, dr, dvw, float(scale),
-                               int(bool(causal)), code, _at(ws), ws.numel() * ws.element_size(), sp)
+    dq, dk_nope, dk_rope, dv = (torch.empty_like(t) if g is None else _need(name, g, t.shape, q.dtype, dev)
+                                for name, g, t in (("dq", dq, q), ("dk_nope", dk_nope, k_nope),
+                                                   ("dk_rope", dk_rope, k_rope), ("dv", dv, v)))
+    ws, ws_bytes = _workspace(workspace, fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dvw), q)
+    st = lib.fa_bwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), _at(do), _at(dq), _at(dk_nope),
+                           _at(dk_rope), _at(dv), B, H, Nq, Nk, dn, dr, dvw,
+                           1.0 / math.sqrt(dn + dr) if scale is None else scale, bool(causal), code, _at(ws), ws_bytes,
+                           sp)
     if st != FA_OK:
         raise FaError(st, "fa_bwd_latent")
     return dq, dk_nope, dk_rope, dv

@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(256)
                                    long long rows, int Nq, int npad) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long base = (static_cast<long long>(blockIdx.x) * 8 + warp) * 8;
+  seq::pdl_launch();
   if (base >= rows) return;
   const long long bh = base / npad;
   const int i0 = static_cast<int>(base % npad), c = lane & 15, sub = lane >> 4;
@@ -415,6 +416,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) fa_latent_bwd_dkr_kernel(const float* __restrict__ part, T* __restrict__ dkr,
                                                                 int H, long long per_head, long long total) {
   const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  seq::pdl_wait();
   if (i >= total) return;
   const float* src = part + (i / per_head) * H * per_head + i % per_head;
   float x = 0.f;
@@ -492,12 +494,10 @@ cudaError_t launch_latent_bwd_dkr(const LatentBwd& p, fa_dtype dt, cudaStream_t 
   const long long blocks = (total + 255) / 256;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   if (dt == FA_DTYPE_F32)
-    fa_latent_bwd_dkr_kernel<float><<<static_cast<unsigned>(blocks), 256, 0, s>>>(
-        p.dkr_part, static_cast<float*>(p.dkr), p.H, per_head, total);
-  else
-    fa_latent_bwd_dkr_kernel<__nv_bfloat16><<<static_cast<unsigned>(blocks), 256, 0, s>>>(
-        p.dkr_part, static_cast<__nv_bfloat16*>(p.dkr), p.H, per_head, total);
-  return cudaGetLastError();
+    return seq::launch_after(fa_latent_bwd_dkr_kernel<float>, static_cast<unsigned>(blocks), 256, 0, s, p.dkr_part,
+                             static_cast<float*>(p.dkr), p.H, per_head, total);
+  return seq::launch_after(fa_latent_bwd_dkr_kernel<__nv_bfloat16>, static_cast<unsigned>(blocks), 256, 0, s,
+                           p.dkr_part, static_cast<__nv_bfloat16*>(p.dkr), p.H, per_head, total);
 }
 
 }  // namespace fa

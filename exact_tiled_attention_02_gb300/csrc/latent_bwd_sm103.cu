@@ -138,6 +138,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  // The keys form waits for the row terms and only then lets the queries form
+  // start, which fills its last round and, as the last of the two to end,
+  // waits for it (they share no output).
+  if (KEYS) {
+    pdl_wait();
+    pdl_launch();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -392,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if (!KEYS) pdl_wait();
 }
 
 template <bool KEYS>
@@ -401,8 +409,7 @@ cudaError_t launch_form(const LatentBwd& p, const BwdMapsL& m, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(p.B) * p.H * (((KEYS ? p.Nk : p.Nq) + BR - 1) / BR);
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  fa_latent_bwd_sm103_kernel<KEYS><<<static_cast<unsigned>(blocks), kThreads, SMEM_BYTES, s>>>(m, p);
-  return cudaGetLastError();
+  return launch_after(fa_latent_bwd_sm103_kernel<KEYS>, static_cast<unsigned>(blocks), kThreads, SMEM_BYTES, s, m, p);
 }
 
 }  // namespace
