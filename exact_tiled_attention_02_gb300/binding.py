@@ -373,13 +373,30 @@ def _made_current(device, stream):
         yield
 
 
-def _workspace(workspace, need, like):
-    torch = _torch()
-    if workspace is None:
-        return like.new_empty(need, dtype=torch.uint8), need
-    if workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
-    return workspace, workspace.numel() * workspace.element_size()
+class _Workspace:
+    """A call's workspace: the tensor given, or a block of torch's caching
+    allocator on the call's stream, handed back on leaving (calls queued later
+    on that stream may reuse it in order).  Taken without a tensor around it: a
+    tensor costs 6 us more beside a kernel launch."""
+
+    __slots__ = ("at", "bytes", "block")
+
+    def __init__(self, workspace, need, device, stream_ptr):
+        self.block = None
+        if workspace is None:
+            self.block = self.at = _torch()._C._cuda_cudaCachingAllocator_raw_alloc(need, stream_ptr)
+            self.bytes = need
+        else:
+            if workspace.device != device or not workspace.is_contiguous():
+                raise ValueError(f"workspace must be a contiguous tensor on {device}")
+            self.at, self.bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        if self.block:
+            _torch()._C._cuda_cudaCachingAllocator_raw_delete(self.block)
 
 
 def fa_fwd_shared_prefix(q, k_prefix, v_prefix, k, v, lens, scale: float | None = None, o=None, lse=None,
@@ -417,10 +434,10 @@ def fa_fwd_shared_prefix(q, k_prefix, v_prefix, k, v, lens, scale: float | None 
         _need("lse", lse, (B, Hq, Nq), torch.float32, dev)
     elif want_lse:
         lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
-    ws, ws_bytes = _workspace(workspace, fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d), q)
-    st = lib.fa_fwd_shared_prefix(_at(q), _at(k_prefix), _at(v_prefix), _at(k), _at(v), _at(lens), _at(o), _at(lse), B,
-                                  Hq, Hkv, Nq, Np, Ns, d, 1.0 / math.sqrt(d) if scale is None else scale, code,
-                                  _at(ws), ws_bytes, sp)
+    with _Workspace(workspace, fa_fwd_shared_prefix_workspace_bytes(B, Hq, Hkv, Nq, Np, Ns, d), dev, sp) as ws:
+        st = lib.fa_fwd_shared_prefix(_at(q), _at(k_prefix), _at(v_prefix), _at(k), _at(v), _at(lens), _at(o), _at(lse),
+                                      B, Hq, Hkv, Nq, Np, Ns, d, 1.0 / math.sqrt(d) if scale is None else scale, code,
+                                      ws.at, ws.bytes, sp)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_shared_prefix")
     return o, lse
@@ -463,9 +480,10 @@ def fa_fwd_latent_absorbed(q, cache, lens, dc: int, scale: float, block_table=No
         _need("lse", lse, (B, H, Nq), torch.float32, dev)
     elif want_lse:
         lse = q.new_empty((B, H, Nq), dtype=torch.float32)
-    ws, ws_bytes = _workspace(workspace, fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc), q)
-    st = lib.fa_fwd_latent_absorbed(_at(q), _at(cache), _at(block_table), _at(lens), _at(o), _at(lse), B, H, Nq, pages,
-                                    page_size, max_pages, dc, dk - dc, scale, code, _at(ws), ws_bytes, sp)
+    need = fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc)
+    with _Workspace(workspace, need, dev, sp) as ws:
+        st = lib.fa_fwd_latent_absorbed(_at(q), _at(cache), _at(block_table), _at(lens), _at(o), _at(lse), B, H, Nq,
+                                        pages, page_size, max_pages, dc, dk - dc, scale, code, ws.at, ws.bytes, sp)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_latent_absorbed")
     return o, lse
@@ -533,11 +551,11 @@ def fa_bwd_latent(q, k_nope, k_rope, v, o, lse, do, scale: float | None = None, 
     dq, dk_nope, dk_rope, dv = (torch.empty_like(t) if g is None else _need(name, g, t.shape, q.dtype, dev)
                                 for name, g, t in (("dq", dq, q), ("dk_nope", dk_nope, k_nope),
                                                    ("dk_rope", dk_rope, k_rope), ("dv", dv, v)))
-    ws, ws_bytes = _workspace(workspace, fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dvw), q)
-    st = lib.fa_bwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), _at(do), _at(dq), _at(dk_nope),
-                           _at(dk_rope), _at(dv), B, H, Nq, Nk, dn, dr, dvw,
-                           1.0 / math.sqrt(dn + dr) if scale is None else scale, bool(causal), code, _at(ws), ws_bytes,
-                           sp)
+    with _Workspace(workspace, fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dvw), dev, sp) as ws:
+        st = lib.fa_bwd_latent(_at(q), _at(k_nope), _at(k_rope), _at(v), _at(o), _at(lse), _at(do), _at(dq),
+                               _at(dk_nope), _at(dk_rope), _at(dv), B, H, Nq, Nk, dn, dr, dvw,
+                               1.0 / math.sqrt(dn + dr) if scale is None else scale, bool(causal), code, ws.at,
+                               ws.bytes, sp)
     if st != FA_OK:
         raise FaError(st, "fa_bwd_latent")
     return dq, dk_nope, dk_rope, dv

@@ -230,7 +230,7 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
     cudaError_t e = cudaSuccess;
     if (Np > 0) e = launch_seq_rows(a, s);
     if (e == cudaSuccess && Ns > 0) e = launch_seq_decode(b, w.plan, Np > 0, s);
-    if (e == cudaSuccess) e = launch_seq_decode_merge(b, w.plan, a.part_o, a.part_lse, w.splits, s);
+    if (e == cudaSuccess) e = launch_seq_decode_merge(b, w.plan, a.part_o, a.part_lse, w.splits, Np > 0 || Ns > 0, s);
     return of(e);
   }
   const PartLayout w = prefix_layout(B, Hq, Hkv, Nq, Np, Ns, d);
@@ -311,7 +311,7 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
     const DecodePlan plan = absorbed_plan(B, H, Nq, page_size, block_table != nullptr);
     p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + absorbed_layout_bf16(plan, dc).off_lse);
     cudaError_t e = launch_seq_decode(p, plan, false, s);
-    if (e == cudaSuccess) e = launch_seq_decode_merge(p, plan, nullptr, nullptr, 0, s);
+    if (e == cudaSuccess) e = launch_seq_decode_merge(p, plan, nullptr, nullptr, 0, true, s);
     return of(e);
   }
   const PartLayout w = absorbed_layout(B, H, Nq, n_keys, dc);

@@ -826,13 +826,18 @@ cudaError_t launch_nr(const SeqAttn& p, const DecodePlan& plan, bool beside, cud
 
 template <int NR>
 cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse, int pre,
-                         cudaStream_t s) {
+                         bool after, cudaStream_t s) {
   // a warp takes a whole row of 512 where the rows alone give every SM 32 warps
   const long long rows = static_cast<long long>(w.n_seq) * w.heads * p.rows;
   const bool wide = p.dv > 128 && rows >= 152 * 32;
   const long long warps = rows * (wide ? (p.dv + 511) / 512 : (p.dv + 127) / 128);
   if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
+  if (!after) {  // no kernel of this call before it: the lengths may only now be complete
+    fa_seq_decode_merge_kernel<NR, 1><<<static_cast<unsigned>((rows * ((p.dv + 127) / 128) + 3) / 4), 128, 0, s>>>(
+        p, w, pre_o, pre_lse, pre);
+    return cudaGetLastError();
+  }
   return wide ? launch_after(fa_seq_decode_merge_kernel<NR, 4>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre)
               : launch_after(fa_seq_decode_merge_kernel<NR, 1>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
 }
@@ -877,10 +882,10 @@ cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, bool beside
 }
 
 cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
-                                    int pre, cudaStream_t s) {
-  if (w.nr == 16) return launch_merge<16>(p, w, pre_o, pre_lse, pre, s);
-  if (w.nr == 32) return launch_merge<32>(p, w, pre_o, pre_lse, pre, s);
-  return launch_merge<64>(p, w, pre_o, pre_lse, pre, s);
+                                    int pre, bool after, cudaStream_t s) {
+  if (w.nr == 16) return launch_merge<16>(p, w, pre_o, pre_lse, pre, after, s);
+  if (w.nr == 32) return launch_merge<32>(p, w, pre_o, pre_lse, pre, after, s);
+  return launch_merge<64>(p, w, pre_o, pre_lse, pre, after, s);
 }
 
 }  // namespace fa

@@ -84,9 +84,11 @@ DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box, int
 size_t decode_slots(const DecodePlan& w);  // rows of part_o
 // beside: as launch_seq_simt
 cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, bool beside, cudaStream_t s);
-// o, lse = the pieces merged, with the partial results pre_o [pre][total][dv] of other keys
+// o, lse = the pieces merged, with the partial results pre_o [pre][total][dv]
+// of other keys.  after: the kernels before it on the stream, back to one that
+// was launched normally, are the same call's.
 cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
-                                    int pre, cudaStream_t s);
+                                    int pre, bool after, cudaStream_t s);
 
 // float32 o, lse = the merged partial results [splits][total] (seq_combine.cu).
 cudaError_t launch_seq_combine(const float* part_o, const float* part_lse, int splits, long long total, int dv,
