@@ -47,7 +47,7 @@ __device__ __forceinline__ long long out_row(const SeqAttn& p, int g, int r) {
 // NCV: 64-column chunks of O a thread holds (dv <= 64 NCV)
 // VEC: every row and part begins on a 16-byte boundary
 template <int TR, int NCV, bool VEC>
-__global__ void __launch_bounds__(kThreads) fa_seq_fwd_simt_kernel(const __grid_constant__ SeqAttn p) {
+__global__ void __launch_bounds__(kThreads, NCV <= 2 ? 2 : 1) fa_seq_fwd_simt_kernel(const __grid_constant__ SeqAttn p) {
   constexpr bool vec = VEC;
   constexpr int RPT = TR / 16;  // rows of the softmax a half-warp
   extern __shared__ float4 smem4[];
