@@ -509,13 +509,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      const bool mine = row < x.rows && !*abort_flag;
-      const long long orow = (w.g / p.group_div) * p.q_s1 + (w.g % p.group_div) * p.q_s2 +
-                             (x.block0 + (plan.per_block > 1 ? 0 : row / plan.block_rows)) * p.q_s3 +
-                             (plan.per_block > 1 ? x.r_off + row : row % plan.block_rows);
-      const long long prow = (p.part0 + w.split) * p.total + orow;
+      const bool out = __all_sync(0xffffffffu, *abort_flag == 0);
+      const bool mine = out && row < x.rows;
+      const long long group_row = (w.g / p.group_div) * p.q_s1 + (w.g % p.group_div) * p.q_s2;
+      auto out_row = [&](int i) -> long long {  // of row i of the tile
+        return plan.per_block > 1 ? group_row + x.block0 * p.q_s3 + x.r_off + i
+                                  : group_row + (x.block0 + i / plan.block_rows) * p.q_s3 + i % plan.block_rows;
+      };
+      const long long orow = out_row(row), prow = (p.part0 + w.split) * p.total + orow;
       const float norm = l + lc;
       const float inv_l = l == 0.f ? 0.f : 1.f / norm;
+      // the rows that this lane stores for its group of four (store_rows64)
+      uint8_t* dst[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = (row & ~3) + i;
+        const long long at = PART ? (p.part0 + w.split) * p.total + out_row(rr) : out_row(rr);
+        dst[i] = !out || rr >= x.rows ? nullptr
+                                      : (PART ? reinterpret_cast<uint8_t*>(p.part_o) : static_cast<uint8_t*>(p.o)) +
+                                            at * DV * (PART ? 4 : 2);
+      }
 #pragma unroll 1
       for (int c = 0; c < DV / 32; ++c) {
         uint32_t o[32];
@@ -523,30 +536,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(tO + c * 32, o);
           tmem_wait_ld();
         }
-        if (!mine) continue;
+        float v[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float v = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv_l;  // no key seen: O (never written) is 0
-          o[e] = __float_as_uint(v);
-        }
-        if constexpr (PART) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * DV + c * 32);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                 __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-        } else {
-          uint8_t* dst = static_cast<uint8_t*>(p.o) + (orow * DV + c * 32) * 2;
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint4 v;
-            v.x = pack_bf16x2(__uint_as_float(o[q4 * 8 + 0]), __uint_as_float(o[q4 * 8 + 1]));
-            v.y = pack_bf16x2(__uint_as_float(o[q4 * 8 + 2]), __uint_as_float(o[q4 * 8 + 3]));
-            v.z = pack_bf16x2(__uint_as_float(o[q4 * 8 + 4]), __uint_as_float(o[q4 * 8 + 5]));
-            v.w = pack_bf16x2(__uint_as_float(o[q4 * 8 + 6]), __uint_as_float(o[q4 * 8 + 7]));
-            st_global_v4(dst + q4 * 16, v);
-          }
-        }
+        for (int e = 0; e < 32; ++e) v[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv_l;  // no key seen: 0
+        auto at = [&](int i) -> void* {
+          uint8_t* q = dst[i & 3];
+          return q == nullptr ? nullptr : q + c * 32 * (PART ? 4 : 2);
+        };
+        if constexpr (PART)
+          store_rows_f32(v, at);
+        else
+          store_rows_bf16(v, at);
       }
       if (mine) {
         const float mref = (m_ref == -INFINITY) ? 0.f : m_ref;
