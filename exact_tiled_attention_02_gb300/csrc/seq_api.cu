@@ -47,8 +47,10 @@ PartLayout part_layout(int sa, int sb, long long rows, int dv) {
 
 PartLayout prefix_layout(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   const int G = Hq / Hkv;
-  const int sp = seq_simt_splits(Hkv, B * G * Nq, Np);
-  const int ss = seq_simt_splits(static_cast<long long>(B) * Hkv, G * Nq, Ns);
+  // The prefix's kernel and the sequences' run side by side, a CTA an SM each
+  // (7 x 8 heads x 3 tokens, 2999 + 333 keys, d = 80: 37.6 us; two each, 46.6).
+  const int sp = seq_simt_splits(Hkv, B * G * Nq, Np, Ns > 0 ? 1 : 2);
+  const int ss = seq_simt_splits(static_cast<long long>(B) * Hkv, G * Nq, Ns, Np > 0 ? 1 : 2);
   return part_layout(sp, ss, static_cast<long long>(B) * Hq * Nq, d);
 }
 // bf16: the prefix's splits [splits][rows], then the pieces of the sequences
@@ -60,18 +62,21 @@ struct PrefixLayout {
 // The prefix's part is bound by the tensor cores, the sequences' own part by
 // memory, and a CTA of the first takes a whole SM: so they run side by side on
 // SMs of their own (n and 152 - n) where that is faster than one after the
-// other, by measured rates: the first as seq_rows_time, the second 5 us and 90
-// GB/s an SM up to 6.2 TB/s of keys and values (taking every sequence as three
-// quarters of its room), the merge 4 us and 5 TB/s of partial results.
-// (128 x 32 heads x 4 tokens, 32768 + 2048 keys, d = 128: 332 us one after the
-// other; the sum of both alone is 318 + 16.)
+// other, by measured rates: the first as seq_rows_time, the second 5 us and a
+// time an SM for a 64-key tile by its row columns (16, 32, 64), up to 6.2 TB/s
+// of keys and values (taking every sequence as three quarters of its room), the
+// merge 4 us and 5 TB/s of partial results.  (128 x 32 heads x 4 tokens, 32768 +
+// 2048 keys, d = 128: 332 us one after the other; the sum of both alone is
+// 318 + 16.)
 PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   PrefixLayout w{};
   const int G = Hq / Hkv, R = B * G * Nq, block = G * Nq, kSms = 152;
   const size_t rows = static_cast<size_t>(B) * Hq * Nq;
   const double own = 0.75 * 4.0 * B * Hkv * d * Ns;  // bytes of the sequences' keys and values
+  const int nr = decode_plan(B, Hkv, block, false, 64, kSms).nr;
+  const double sm_rate = 256.0 * d / (nr == 16 ? 0.36 : nr == 32 ? 0.42 : 0.69);  // bytes a us
   auto own_time = [&](int sms) {
-    const double rate = 0.09e6 * sms < 6.2e6 ? 0.09e6 * sms : 6.2e6;
+    const double rate = sm_rate * sms < 6.2e6 ? sm_rate * sms : 6.2e6;
     return own > 0 ? 5.0 + own / rate : 0.0;
   };
   int own_sms = kSms;
@@ -114,7 +119,8 @@ bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
 }
 
 PartLayout absorbed_layout(int B, int H, int Nq, int n_keys, int dc) {
-  const int sp = seq_simt_splits(B, H * Nq, n_keys);
+  // (5 x 12 heads, up to 2047 tokens of 192 + 40: 25.3 us; one CTA an SM, 31.0)
+  const int sp = seq_simt_splits(B, H * Nq, n_keys, 2);
   return part_layout(sp, 0, static_cast<long long>(B) * H * Nq, dc);
 }
 // bf16: the pieces of sequences that several CTAs share

@@ -65,7 +65,7 @@ struct Cfg {
   static constexpr int Q_BYTES = QC * NR * 128;
   static constexpr int P_BYTES = NR * 128;
   static constexpr int M_BYTES = UC * CB, X_BYTES = XC * CB;
-  static constexpr int CTAS = SHARED || NR == 64 ? 1 : 2;  // a SM
+  static constexpr int CTAS = SHARED ? 1 : 2;                  // a SM
   static constexpr int BUDGET = CTAS == 1 ? 227 * 1024 : 113 * 1024;
   static constexpr int BARS = DM == 512 && NR == 64 ? 27 : 40;
   static constexpr int MISC = 3 * NR * 4 + 4 * NR * 4 + 8 * BARS + 24;  // stats, warp scratch, barriers, start
@@ -192,7 +192,7 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool x) {
 }
 
 template <int DM, int DX, bool SHARED, int NR>
-__global__ void __launch_bounds__(kThreads, SHARED || NR == 64 ? 1 : 2)
+__global__ void __launch_bounds__(kThreads, Cfg<DM, DX, SHARED, NR>::CTAS)
     fa_seq_decode_sm103_kernel(const __grid_constant__ DecodeMaps maps, const __grid_constant__ SeqAttn p,
                                const DecodePlan plan) {
   using C = Cfg<DM, DX, SHARED, NR>;
@@ -827,7 +827,9 @@ cudaError_t launch_nr(const SeqAttn& p, const DecodePlan& plan, bool beside, cud
 template <int NR>
 cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse, int pre,
                          bool after, cudaStream_t s) {
-  // a warp takes a whole row of 512 where the rows alone give every SM 32 warps
+  // A warp takes a whole row of 512 where the rows alone give every SM 32 warps
+  // (the whole call at 16384 rows: 105 us, 117 with a warp a slice; at 1024
+  // rows 71 and 68; at 16 rows 18.9 and 15.4).
   const long long rows = static_cast<long long>(w.n_seq) * w.heads * p.rows;
   const bool wide = p.dv > 128 && rows >= 152 * 32;
   const long long warps = rows * (wide ? (p.dv + 511) / 512 : (p.dv + 127) / 128);
@@ -848,9 +850,13 @@ DecodePlan decode_plan(int n_seq, int heads, int rows, bool shared, int box, int
   DecodePlan w{};
   w.n_seq = n_seq;
   w.heads = heads;
+  // The narrowest product that holds the rows (64 sequences of 4000 to 8000
+  // tokens of 512 + 64, 16 heads: 84, 86, 92 us with 16, 32, 64 columns; 32
+  // heads: 125, 92, 97; separate keys and values, 128 x 8 heads of 2048, d =
+  // 128: 16 rows 150, 169, 290; 32 rows 244, 181, 306).
   w.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   w.row_groups = (rows + w.nr - 1) / w.nr;
-  const int ctas = shared || w.nr == 64 ? sms : 2 * sms;  // one CTA an SM, or two
+  const int ctas = shared ? sms : 2 * sms;  // one CTA an SM, or two
   const long long groups = static_cast<long long>(heads) * w.row_groups;
   w.cuts = groups < ctas ? static_cast<int>(ctas / groups) : 1;
   w.direct = shared;

@@ -7,10 +7,10 @@
 // one pass over the keys with the row's running maximum and sum (all fp32,
 // accurate expf / logf).  A row that sees no key gives O = 0, lse = -inf.
 //
-// One CTA of 256 threads per TR query rows (64, 32 or 16, by the group's row
-// count) and split of the keys; tiles of 64 keys.  The queries stay in shared
-// memory; keys and values stream through a ring of 64 x 64 chunks, copied
-// asynchronously up to three chunks ahead.  Products go in 4 x 4 blocks a
+// One CTA of 256 threads per TR query rows (32 or 16, by the launch's size) and
+// split of the keys; tiles of 64 keys.  The queries stay in shared memory; keys
+// and values stream through a ring of 64 x 64 chunks, copied asynchronously up
+// to three chunks ahead.  Products go in 4 x 4 blocks a
 // thread (seq_simt.cuh); the scores pass through shared memory, where the
 // softmax takes them a half-warp a row.
 // Calls with few rows are bound by the latency of one tile's chunks (the keys
@@ -300,21 +300,23 @@ cudaError_t launch_tr(const SeqAttn& p, bool beside, cudaStream_t s) {
   return cudaErrorInvalidValue;
 }
 
-// Rows of a CTA: 64 unless that leaves SMs idle (a chunk costs a CTA with 32
-// or 16 rows less, though more for each row).
-int rows_per_cta(long long groups, int rows, int splits, int dk) {
-  for (int tr = dk > 512 ? 32 : 64; tr > 16; tr /= 2)  // (64 wider rows would not fit shared memory)
-    if (rows > tr / 2 && groups * ((rows + tr - 1) / tr) * splits >= 152) return tr;
-  return 16;
+// Rows of a CTA: 32, or 16 where that leaves SMs idle (a chunk costs such a CTA
+// less, though more for each row).  Causal, 68 + 40 wide, 6 heads: 333 tokens
+// 33 us with 32 rows, 27 with 16; 1500 tokens 168 and 181.  (64 rows: 48 and
+// 169; 16 heads of 2500 tokens, 96 + 64 wide: 804 us with 32 rows, 875 with 64.)
+int rows_per_cta(long long groups, int rows, int splits) {
+  return rows > 16 && groups * ((rows + 31) / 32) * splits >= 152 ? 32 : 16;
 }
 
 }  // namespace
 
-int seq_simt_splits(long long groups, int rows, int max_keys) {
-  const int tr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+// Splits of the keys: one round of CTAs, `ctas` an SM (a second round costs more
+// than a second tile), or a tile a split.
+int seq_simt_splits(long long groups, int rows, int max_keys, int ctas) {
+  const int tr = rows <= 16 ? 16 : 32;
   const long long blocks = groups * ((rows + tr - 1) / tr);
   const int tiles = (max_keys + BK - 1) / BK;
-  long long n = 2 * 152 / blocks;  // two CTAs an SM: a second round costs more than a second tile
+  long long n = ctas * 152LL / blocks;
   if (n > tiles) n = tiles;
   if (n > 64) n = 64;
   return n < 1 ? 1 : static_cast<int>(n);
@@ -323,11 +325,7 @@ int seq_simt_splits(long long groups, int rows, int max_keys) {
 cudaError_t launch_seq_simt(const SeqAttn& args, bool beside, cudaStream_t s) {
   SeqAttn p = args;
   if (p.k2 == nullptr) p.k2 = p.k1;  // never read: copies of nothing still name an address
-  switch (rows_per_cta(p.groups, p.rows, p.splits, p.d1 + p.d2)) {
-    case 16: return launch_tr<16>(p, beside, s);
-    case 32: return launch_tr<32>(p, beside, s);
-    default: return launch_tr<64>(p, beside, s);
-  }
+  return rows_per_cta(p.groups, p.rows, p.splits) == 32 ? launch_tr<32>(p, beside, s) : launch_tr<16>(p, beside, s);
 }
 
 }  // namespace fa

@@ -55,8 +55,8 @@ struct SeqAttn {
 // float32 on CUDA cores (seq_fwd_simt.cu).  beside: the kernel before it on the
 // stream is the same call's and independent.
 cudaError_t launch_seq_simt(const SeqAttn& p, bool beside, cudaStream_t s);
-// Splits of the keys that give the launch enough blocks.
-int seq_simt_splits(long long groups, int rows, int max_keys);
+// Splits of the keys that give the launch `ctas` blocks an SM.
+int seq_simt_splits(long long groups, int rows, int max_keys, int ctas);
 
 // bf16 on the tensor cores, many rows a group (seq_rows_sm103.cu): no lens, no
 // pages; the expanded latent shape to o and lse, or d = 64, 96, 128 to partial

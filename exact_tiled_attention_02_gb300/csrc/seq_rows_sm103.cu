@@ -598,7 +598,7 @@ cudaError_t launch_rows(const SeqAttn& p, cudaStream_t s) {
   cudaError_t e = once(fa_seq_rows_sm103_kernel<DQK, DV, D2, PART>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   RowsPlan w = rows_plan(p.rows, p.row_block, p.causal != 0);
-  w.heavy_first = p.causal && p.splits == 1;
+  w.heavy_first = p.causal;
   const long long items = static_cast<long long>(w.pairs) * p.groups * p.splits;
   if (items > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
   w.n_items = static_cast<int>(items);
