@@ -207,8 +207,15 @@ fa_status fa_bwd_static_workspace(const void* q, const void* k, const void* v, c
  *     index outside the cache as a page of zeros; each is reported by
  *     fa_last_device_status() as FA_ERR_INVALID.  Nothing out of range is read.
  *   - Entries of K, V and the cache at positions a sequence's length does not
- *     cover may hold anything (NaN included); those within it must be finite.
- *   - Outputs must not overlap inputs, nor the workspace anything.
+ *     cover may hold anything (NaN included).  Everything else must be finite,
+ *     the padding of the expanded form included: a masked probability is 0,
+ *     and 0 times an infinity or a NaN is not.
+ *   - Outputs must not overlap inputs, nor the workspace anything.  A workspace
+ *     serves one call at a time: calls (and replays of graphs) that share one
+ *     must run in order.
+ *   - Sizes: every tensor below 2^40 elements; shared prefix and absorbed also
+ *     B H Nq < 2^28 rows and B times a sequence's room (Ns, or max_pages *
+ *     page_size) below 4.5e8 tokens; past these FA_ERR_INVALID.
  *   - The order of every sum is fixed by the shapes, the lengths and the
  *     number of SMs: results repeat bit for bit.
  */
@@ -279,8 +286,9 @@ size_t fa_fwd_latent_absorbed_workspace_bytes(int B, int H, int Nq, int page_siz
  *   causal       1: query row i sees keys j <= i + Nk - Nq (rows are the last
  *                Nq of Nk tokens; with Nq > Nk the first Nq - Nk rows see
  *                none); 0: every key.
- * A batch of unequal lengths is padded on the right: with causal = 1 no real
- * token sees the padding behind it.
+ * A batch of unequal lengths is padded on the right, with finite values: with
+ * causal = 1 no real token sees the padding behind it, and rows whose dO is 0
+ * add nothing to the gradients.
  * bf16 with dn = 128, dr = 64, dv = 128; float32 with dn + dr <= 256,
  * dv <= 128; others return FA_ERR_UNSUPPORTED.
  */
