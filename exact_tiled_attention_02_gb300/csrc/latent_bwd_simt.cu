@@ -11,7 +11,8 @@
 //   prep   -lse_i log2 e and -D_i of every row (padded to 128 rows a head);
 //   dkdv   one CTA per 64 (32, 16) keys of a head over the 64-row query tiles that see
 //          them; the rotary part of dk goes to an fp32 array per head;
-//   dq     one CTA per 64 (32, 16) queries over the key tiles they see;
+//   dq     one CTA per 64 (32, 16) queries over the key tiles they see, beside dkdv
+//          on the room that leaves (6 heads of 333 tokens: 124 us so 101);
 //   dkr    sums the rotary parts over the heads, in head order.
 // No atomics: every sum has one fixed order.  A row that sees no key has
 // P = 0 throughout.  The CTA's own tile stays in shared memory; the other
@@ -114,6 +115,13 @@ constexpr int bwd_smem() {
   return (DEPTH * CHUNK + CHUNK + (NK + NV + 2) * BR * LD) * 4;  // ring, partial sums, own rows, P and dS
 }
 
+// CTAs of dkdv an SM, or of dkdv and dq: two where shared memory holds them and
+// 128 registers a thread do
+template <int NK, int NV, int BR>
+constexpr int bwd_ctas() {
+  return NK <= 2 && bwd_smem<NK, NV, BR>() <= 113 * 1024 ? 2 : 1;
+}
+
 // The ring: chunk after chunk of a stream, copied DEPTH - 1 ahead of its use.
 // F: f(n, dst) copies this thread's share of the n-th chunk to dst.
 template <typename F>
@@ -141,8 +149,9 @@ struct Ring {
 };
 
 template <int NK, int NV, int BR>
-__global__ void __launch_bounds__(kThreads) fa_latent_bwd_dkdv_kernel(const LatentBwd p, int vec) {
+__global__ void __launch_bounds__(kThreads, bwd_ctas<NK, NV, BR>()) fa_latent_bwd_dkdv_kernel(const LatentBwd p, int vec) {
   constexpr int R = BR / 16, OWN = BR * LD;
+  seq::pdl_launch();  // dq reads nothing of this kernel's: it starts on the SMs that are left
   const Block<BR> blk;
   extern __shared__ float4 smem4[];
   float* base = reinterpret_cast<float*>(smem4);
@@ -410,6 +419,7 @@ __global__ void __launch_bounds__(kThreads) fa_latent_bwd_dq_kernel(const Latent
         if (d < dk) dq[row * dk + d] = aq[c][i][m] * p.scale;
       }
   }
+  seq::pdl_wait();  // dkr, which waits for this kernel, reads what dkdv wrote
 }
 
 template <typename T>
@@ -440,17 +450,19 @@ cudaError_t launch_rows(const LatentBwd& p, cudaStream_t s) {
   fa_latent_bwd_dkdv_kernel<NK, NV, BR><<<static_cast<unsigned>(kb), kThreads, SMEM, s>>>(p, vec);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fa_latent_bwd_dq_kernel<NK, NV, BR><<<static_cast<unsigned>(qb), kThreads, SMEM, s>>>(p, vec);
-  return cudaGetLastError();
+  return seq::launch_after(fa_latent_bwd_dq_kernel<NK, NV, BR>, static_cast<unsigned>(qb), kThreads, SMEM, s, p, vec);
 }
-// 64 rows a CTA where that fills the SMs, else 32 or 16, which take less time
-// each.  Forward and backward with 64, 32, 16 rows: 6 heads of 333 tokens (68 +
-// 40 wide) 219, 156, 124 us; of 1500, 886, 847, 873; 64 heads of 1000 (96 + 64
-// wide) 2524, 2653, 3249; 16 heads of 1500 (192 + 128 wide) 3131, 3241, 4080.
+// Rows a CTA: 32 where that fills the SMs, else 16, which take less time each;
+// 64 where that fills them and two CTAs of 32 do not fit an SM.  Forward and
+// backward with 64, 32, 16 rows, 68 + 40 wide: 6 heads of 333 tokens 148, 114,
+// 101 us, of 1500 tokens 925, 739, 749; 96 + 64 wide: 64 heads of 1000 tokens
+// 2424, 2267, 2692; 192 + 128 wide (one CTA an SM): 16 heads of 1000 tokens
+// 1445, 1548, 1823.
 template <int NK, int NV>
 cudaError_t launch_nkv(const LatentBwd& p, cudaStream_t s) {
   const long long n = p.Nk < p.Nq ? p.Nk : p.Nq, bh = static_cast<long long>(p.B) * p.H;
-  if (bh * ((n + 63) / 64) >= 152) return launch_rows<NK, NV, 64>(p, s);
+  if constexpr (bwd_ctas<NK, NV, 32>() == 1)
+    if (bh * ((n + 63) / 64) >= 152) return launch_rows<NK, NV, 64>(p, s);
   return bh * ((n + 31) / 32) >= 152 ? launch_rows<NK, NV, 32>(p, s) : launch_rows<NK, NV, 16>(p, s);
 }
 
