@@ -65,23 +65,26 @@ struct PrefixLayout {
 // other, by measured rates: the first as seq_rows_time, the second 5 us and a
 // time an SM for a 64-key tile by its row columns (16, 32, 64), up to 6.2 TB/s
 // of keys and values (taking every sequence as three quarters of its room), the
-// merge 4 us and 5 TB/s of partial results.  (128 x 32 heads x 4 tokens, 32768 +
-// 2048 keys, d = 128: 332 us one after the other; the sum of both alone is
-// 318 + 16.)
+// merge 4 us and 5 TB/s of partial results.  While the second runs, the first
+// takes 1.5 times as long where one item reads a prefix tile (2.2 us a tile
+// for 1.45), 1.25 times where two share it, and so on.  (128 x 32 heads x 4
+// tokens, 32768 + 2048 keys, d = 128: 332 us one after the other, 264 side by
+// side; 64 x 32 x 1, 16384 + 1024 keys: 84 and 60.)
 PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   PrefixLayout w{};
   const int G = Hq / Hkv, R = B * G * Nq, block = G * Nq, kSms = 152;
   const size_t rows = static_cast<size_t>(B) * Hq * Nq;
-  const double own = 0.75 * 4.0 * B * Hkv * d * Ns;  // bytes of the sequences' keys and values
+  const double own_bytes = 0.75 * 4.0 * B * Hkv * d * Ns;  // the sequences' keys and values
   const int nr = decode_plan(B, Hkv, block, false, 64, kSms).nr;
   const double sm_rate = 256.0 * d / (nr == 16 ? 0.36 : nr == 32 ? 0.42 : 0.69);  // bytes a us
   auto own_time = [&](int sms) {
     const double rate = sm_rate * sms < 6.2e6 ? sm_rate * sms : 6.2e6;
-    return own > 0 ? 5.0 + own / rate : 0.0;
+    return own_bytes > 0 ? 5.0 + own_bytes / rate : 0.0;
   };
   int own_sms = kSms;
   if (Np > 0) {
     const int items = seq_rows_items(Hkv, R, block), tiles = (Np + 127) / 128;
+    const double slow = 0.5 * Hkv / items;  // items a head read the same prefix through L2
     double best = 1e30;
     for (int n = kSms; n >= 8; n -= 8) {
       if (n < kSms && Ns == 0) break;
@@ -90,9 +93,10 @@ PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, 
         if (s < 1) s = 1;
         if (s > tiles) s = tiles;
         if (s > 64) s = 64;
-        const double r = seq_rows_time(Hkv, R, block, Np, d, n, s);
+        const double r = seq_rows_time(Hkv, R, block, Np, d, n, s), own = own_time(n == kSms ? kSms : kSms - n);
         const double merge = 4.0 + static_cast<double>(s) * rows * d * 8.0 / 5e6;
-        const double t = merge + (n == kSms ? r + own_time(kSms) : r > own_time(kSms - n) ? r : own_time(kSms - n));
+        const double all = r * (1.0 + slow), part = r + own * slow / (1.0 + slow), beside = all < part ? all : part;
+        const double t = merge + (n == kSms ? r + own : beside > own ? beside : own);
         if (t < best) {
           best = t;
           w.splits = s;
