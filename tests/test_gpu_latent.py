@@ -54,6 +54,14 @@ EXPANDED = [
     ("f32", 1, 2, 40, 133, 65, 7, 128, True),
     ("f32", 1, 2, 90, 30, 128, 64, 64, True),
     ("f32", 2, 2, 33, 65, 192, 64, 33, False),
+    # heads enough that a CTA takes 32 or 64 rows, at every register width of the backward
+    ("f32", 8, 10, 65, 65, 20, 7, 40, True),
+    ("f32", 8, 10, 65, 65, 48, 20, 40, True),
+    ("f32", 8, 10, 65, 100, 64, 64, 128, False),
+    ("f32", 8, 10, 70, 65, 96, 64, 128, True),
+    ("f32", 8, 10, 65, 65, 96, 64, 60, True),
+    ("f32", 8, 10, 65, 65, 192, 64, 60, True),
+    ("f32", 8, 10, 65, 65, 192, 64, 128, True),
 ]
 
 

@@ -62,6 +62,11 @@ CASES = [
     ("bf16", 40, 16, 2, 1, 1000, 33, 128, [i % 34 for i in range(40)]),  # 320 rows share the prefix
     ("bf16", 33, 8, 8, 2, 513, 20, 64, [i % 21 for i in range(33)]),
     ("bf16", 2, 8, 1, 40, 200, 50, 128, [50, 41]),          # 320 rows of one sequence
+    ("bf16", 3, 8, 1, 6, 100, 130, 64, [130, 70, 0]),       # 48 rows a sequence
+    ("bf16", 3, 10, 2, 7, 0, 130, 96, [64, 129, 1]),        # 35 rows, no prefix
+    ("bf16", 24, 16, 2, 8, 130, 700, 128, [700 - 29 * i for i in range(24)]),  # 64 rows, many pieces
+    ("bf16", 24, 16, 2, 4, 130, 700, 64, [700 - 29 * i for i in range(24)]),   # 32 rows
+    ("f32", 1, 8, 8, 40, 100, 130, 64, [130]),              # rows enough for wider tiles
     ("bf16", 1, 2, 1, 1, 5000, 3000, 128, [2999]),          # many splits of both parts
     ("f32", 1, 1, 1, 1, 1, 0, 1, [0]),
     ("f32", 3, 6, 2, 1, 65, 40, 80, [0, 1, 40]),
