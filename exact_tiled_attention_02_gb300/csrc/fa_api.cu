@@ -370,7 +370,7 @@ fa_status fa_last_device_status(void* stream) {
   if (cudaStreamSynchronize(s) != cudaSuccess) return FA_ERR_CUDA;
   if (host & sm103::kStatusTimeout) return FA_ERR_TIMEOUT;
   if (host & sm103::kStatusLayout) return FA_ERR_CUDA;
-  if (host & sm103::kStatusInput) return FA_ERR_INVALID;
+  if (host & kStatusInput) return FA_ERR_INVALID;
   return FA_OK;
 }
 

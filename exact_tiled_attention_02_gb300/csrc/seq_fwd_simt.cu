@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, NCV <= 2 ? 2 : 1) fa_seq_fwd_simt_ke
   if (p.lens != nullptr) {
     const int n = p.lens[g / p.lens_div];
     nk = min(max(n, 0), p.n_keys);
-    if (n != nk && tid == 0) atomicOr(p.status, sm103::kStatusInput);
+    if (n != nk && tid == 0) atomicOr(p.status, kStatusInput);
   }
   // keys that some row of this CTA sees
   int seen = nk;
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, NCV <= 2 ? 2 : 1) fa_seq_fwd_simt_ke
         const int at = j / p.page_size;
         const int page = p.table != nullptr ? p.table[static_cast<long long>(g) * p.max_pages + at] : g;
         if (page < 0 || page >= p.n_pages) {
-          atomicOr(p.status, sm103::kStatusInput);
+          atomicOr(p.status, kStatusInput);
           continue;
         }
         row = static_cast<long long>(page) * p.page_size + (j - at * p.page_size);

@@ -8,6 +8,8 @@
 
 namespace fa {
 
+// Status bit: a length or page index in device memory was out of range (not read past).
+constexpr unsigned int kStatusInput = 1u;  // matches FA_ERR_INVALID
 constexpr int kAllRows = 0x7fffffff;  // SeqAttn::row_block of a problem whose rows are one block
 
 // One attention problem family: groups of query rows, each group against its

@@ -102,7 +102,6 @@ struct WaitCtl {
 };
 
 constexpr unsigned int kStatusTimeout = 4u;  // matches FA_ERR_TIMEOUT
-constexpr unsigned int kStatusInput = 1u;    // a length or page index in device memory was out of range (not read past)
 constexpr unsigned int kStatusLayout = 8u;   // a kernel refused to run: shared memory layout would not fit
 
 __device__ __forceinline__ void record_timeout(const WaitCtl& w) {
