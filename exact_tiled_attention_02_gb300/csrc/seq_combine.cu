@@ -9,7 +9,8 @@
 // is not read; a row without keys gives O = 0 and lse = -inf.
 //
 // One warp per row and 32 of its columns; lane i holds the weight of part i,
-// so that the parts' loads do not wait for one another.
+// so that the parts' loads do not wait for one another.  Bound by latency: two
+// dependent rounds of loads, a few microseconds for a decoding batch.
 #include <cmath>
 
 #include "seq_sm103.cuh"

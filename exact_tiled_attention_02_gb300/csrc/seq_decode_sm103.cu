@@ -38,6 +38,12 @@
 // Shared memory: Q, P, a ring of M units (64 tokens x 128 dimensions; shared
 // form: key and value, otherwise values) and one of X units (shared form: the
 // rotary part; otherwise keys).
+//
+// 64 sequences of 500 to 8200 tokens of 512 + 64, 16 heads: 60 us, 5.4 TB/s.
+// 128 heads x 2 tokens, up to 16384: 411 us the call, 753 TFLOP/s; there the
+// cache passes to four groups of rows, 21 bytes a cycle into every SM (25 to 27
+// were the most seen), and the ring of two tiles that fits beside 64 rows of
+// queries covers no more: 3170 cycles a tile for 1918 of products.
 #include <cmath>
 
 #include "seq_sm103.cuh"
