@@ -140,6 +140,13 @@ long long absorbed_keys(int page_size, int max_pages) {
   const long long n = static_cast<long long>(page_size) * max_pages;
   return n <= 0x7fffff00LL ? n : -1;
 }
+// What the layouts and plans above count on (rows and tiles in 32 bits): the
+// workspace query's check and part of the call's.
+bool absorbed_sizes_ok(int B, int H, int Nq, int page_size, int max_pages, int dc) {
+  if (!sizes_ok(B, H, Nq, dc) || dc > 4096 || !sizes_ok(B, max_pages) || page_size < 1) return false;
+  const long long keys = absorbed_keys(page_size, max_pages);
+  return static_cast<long long>(B) * H * Nq <= 0x7fffffffLL / 8 && keys > 0 && tiles_ok(B, keys);
+}
 
 bool expanded_sizes_ok(int B, int H, int Nq, int Nk, int dn, int dr, int dv) {
   return sizes_ok(B, H, Nq, dn) && sizes_ok(B, H, Nq, dr) && sizes_ok(B, H, Nq, dv) && sizes_ok(B, H, Nk, dn) &&
@@ -258,9 +265,7 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
 }
 
 size_t fa_fwd_latent_absorbed_workspace_bytes(int B, int H, int Nq, int page_size, int max_pages, int dc) {
-  if (!sizes_ok(B, H, Nq, dc) || page_size < 1 || max_pages < 1 || absorbed_keys(page_size, max_pages) < 0 ||
-      !tiles_ok(B, absorbed_keys(page_size, max_pages)))
-    return 0;
+  if (!absorbed_sizes_ok(B, H, Nq, page_size, max_pages, dc)) return 0;
   const size_t f32 = absorbed_layout(B, H, Nq, static_cast<int>(absorbed_keys(page_size, max_pages)), dc).bytes;
   const size_t bf16 = absorbed_layout_bf16(absorbed_plan(B, H, Nq, page_size, true), dc).bytes;
   return f32 > bf16 ? f32 : bf16;
@@ -273,11 +278,8 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
   if (!q || !cache || !lens || !o || !workspace) return FA_ERR_INVALID;
   if (!aligned(q, 16) || !aligned(cache, 16) || !aligned(o, 16) || !aligned(workspace, 256)) return FA_ERR_INVALID;
   if (!aligned(block_table, 4) || !aligned(lens, 4) || !aligned(lse, 4)) return FA_ERR_INVALID;
-  if (!sizes_ok(B, H, Nq, dc) || !sizes_ok(B, H, Nq, dr) || dc > 4096 || dr > 4096) return FA_ERR_INVALID;
-  if (!sizes_ok(n_pages, page_size, dc + dr) || !sizes_ok(B, max_pages)) return FA_ERR_INVALID;
-  if (static_cast<long long>(B) * H * Nq > 0x7fffffffLL / 8 || absorbed_keys(page_size, max_pages) < 0 ||
-      !tiles_ok(B, absorbed_keys(page_size, max_pages)))
-    return FA_ERR_INVALID;
+  if (!absorbed_sizes_ok(B, H, Nq, page_size, max_pages, dc)) return FA_ERR_INVALID;
+  if (!sizes_ok(B, H, Nq, dr) || dr > 4096 || !sizes_ok(n_pages, page_size, dc + dr)) return FA_ERR_INVALID;
   if (!block_table && (max_pages != 1 || n_pages < B)) return FA_ERR_INVALID;
   if (!scale_ok(scale) || !dtype_ok(dt)) return FA_ERR_INVALID;
   if (dt == FA_DTYPE_BF16 && !((dc == 256 || dc == 512) && dr == 64)) return FA_ERR_UNSUPPORTED;

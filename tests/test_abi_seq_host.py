@@ -99,3 +99,14 @@ def test_workspace_sizes(b):
         assert n > 0 and n % 256 == 0
     # two padded row arrays, then the rotary gradient of each head
     assert b.fa_bwd_latent_workspace_bytes(1, 2, 100, 70, 128, 64, 128) == 2 * (2 * 128 * 4) + 2 * 70 * 64 * 4
+
+
+def test_absorbed_refuses_too_many_rows_before_it_plans(b):
+    """B H Nq of 2^28 and more, among them products past 32 bits: the query
+    answers 0, as the call refuses; one row fewer than 2^28 is planned."""
+    for B, H, Nq in ((1, 65536, 65536), (1, 65536, 32768), (1 << 20, 1 << 9, 1), (1, 1 << 28, 1), (4, 1 << 26, 1)):
+        assert b.lib.fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, 64, 4, 192) == 0, (B, H, Nq)
+        assert absorbed(b, B=B, H=H, Nq=Nq) == 1, (B, H, Nq)
+    assert 0 < b.lib.fa_fwd_latent_absorbed_workspace_bytes(1, (1 << 28) - 1, 1, 64, 4, 192) < 1 << 44
+    # a table past 2^40 entries, a latent past 4096: the call's other refusals
+    assert b.lib.fa_fwd_latent_absorbed_workspace_bytes(1, 1, 1, 64, 4, 4097) == 0
