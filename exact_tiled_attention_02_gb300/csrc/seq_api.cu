@@ -117,7 +117,8 @@ PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, 
 // the sequences' 64-key tiles, times the most ranges they are cut into, stay below 2^31
 bool tiles_ok(int n_seq, long long n_keys) { return n_seq * ((n_keys + 63) / 64) * 305 <= 0x7fffffffLL; }
 bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
-  if (Np < 0 || Ns < 0 || Hkv < 1 || Hq % Hkv != 0) return false;
+  // (Np past 2^31 - 256 would round up to tiles past 32 bits; Ns is held lower by tiles_ok)
+  if (Np < 0 || Np > 0x7fffff00 || Ns < 0 || Hkv < 1 || Hq % Hkv != 0) return false;
   return sizes_ok(B, Hq, Nq, d) && sizes_ok(B, Hkv, Ns > 0 ? Ns : 1, d) && sizes_ok(Hkv, Np > 0 ? Np : 1, d) &&
          static_cast<long long>(B) * Hq * Nq <= 0x7fffffffLL / 8 && tiles_ok(B, Ns);
 }

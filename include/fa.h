@@ -226,7 +226,7 @@ fa_status fa_bwd_static_workspace(const void* q, const void* k, const void* v, c
  * batch.  Query head h uses key/value head h / (Hq / Hkv).
  *   q            [B,Hq,Nq,d], a sequence's Nq new tokens.
  *   k_prefix, v_prefix  [Hkv,Np,d]: seen by every query row.  Np may be 0
- *                (then both may be NULL).
+ *                (then both may be NULL), at most 2^31 - 256.
  *   k, v         [B,Hkv,Ns,d]: each sequence's own keys and values after the
  *                prefix, those of the new tokens included; positions
  *                j < lens[b] are valid.  Ns may be 0 (then both may be NULL).

@@ -110,3 +110,14 @@ def test_absorbed_refuses_too_many_rows_before_it_plans(b):
     assert 0 < b.lib.fa_fwd_latent_absorbed_workspace_bytes(1, (1 << 28) - 1, 1, 64, 4, 192) < 1 << 44
     # a table past 2^40 entries, a latent past 4096: the call's other refusals
     assert b.lib.fa_fwd_latent_absorbed_workspace_bytes(1, 1, 1, 64, 4, 4097) == 0
+
+
+def test_prefix_length_ends_at_the_rooms_of_the_other_lengths(b):
+    """Np above 2^31 - 256, where counts of 64- or 128-key tiles pass 32 bits:
+    the query answers 0 and the call refuses, whatever workspace it is given."""
+    size = b.lib.fa_fwd_shared_prefix_workspace_bytes
+    for Np in ((1 << 31) - 255, (1 << 31) - 128, (1 << 31) - 127, (1 << 31) - 1):
+        for ws in (BIG, (1 << 64) - 1):
+            assert prefix(b, B=1, Hq=1, Hkv=1, Np=Np, Ns=1, wsb=ws) == 1, Np
+        assert size(1, 1, 1, 1, Np, 1, 64) == 0, Np
+    assert 0 < size(1, 1, 1, 1, (1 << 31) - 256, 1, 64) < 1 << 30
