@@ -121,3 +121,30 @@ def test_prefix_length_ends_at_the_rooms_of_the_other_lengths(b):
             assert prefix(b, B=1, Hq=1, Hkv=1, Np=Np, Ns=1, wsb=ws) == 1, Np
         assert size(1, 1, 1, 1, Np, 1, 64) == 0, Np
     assert 0 < size(1, 1, 1, 1, (1 << 31) - 256, 1, 64) < 1 << 30
+
+
+def test_room_of_a_batch_is_limited_in_whole_tiles(b):
+    """The documented limit: 7,040,929 tiles of 64 tokens, each sequence's room rounded up."""
+    most = 7040929
+    prefix_bytes, absorbed_bytes = b.lib.fa_fwd_shared_prefix_workspace_bytes, b.lib.fa_fwd_latent_absorbed_workspace_bytes
+    for n, Ns in ((most, 1), (most, 64), (1, most * 64), (most // 2, 65)):
+        assert prefix_bytes(n, 1, 1, 1, 0, Ns, 64) > 0, (n, Ns)
+    for n, Ns in ((most + 1, 1), (most, 65), (1, most * 64 + 1), (most // 2 + 1, 65)):
+        assert prefix_bytes(n, 1, 1, 1, 0, Ns, 64) == 0, (n, Ns)
+        for dt in (0, 1):
+            assert prefix(b, B=n, Hq=1, Hkv=1, Np=0, Ns=Ns, dt=dt) == 1, (n, Ns)
+    for n, page, pages in ((most, 1, 1), (most, 16, 4), (1, 64, most), (most // 2, 5, 13)):
+        assert absorbed_bytes(n, 1, 1, page, pages, 512) > 0, (n, page, pages)
+    for n, page, pages in ((most + 1, 1, 1), (most, 5, 13), (1, 64, most + 1)):
+        assert absorbed_bytes(n, 1, 1, page, pages, 512) == 0, (n, page, pages)
+        for dt in (0, 1):
+            assert absorbed(b, B=n, H=1, page=page, max_pages=pages, n_pages=1, dt=dt) == 1, (n, page, pages)
+
+
+def test_expanded_lengths_are_limited(b):
+    size = b.lib.fa_bwd_latent_workspace_bytes
+    for Nq, Nk in ((1 << 30, 1), (1, 1 << 30)):
+        assert latent(b, B=1, H=1, Nq=Nq, Nk=Nk, dn=1, dr=1, dv=1, dt=0) == 1
+        assert latent_bwd(b, B=1, H=1, Nq=Nq, Nk=Nk, dn=1, dr=1, dv=1, dt=0) == 1
+        assert size(1, 1, Nq, Nk, 1, 1, 1) == 0
+        assert size(1, 1, max(1, Nq - 1), max(1, Nk - 1), 1, 1, 1) > 0
