@@ -509,9 +509,10 @@ def fa_fwd_latent(q, k_nope, k_rope, v, scale: float | None = None, causal: bool
 
     ``q``: [B, H, Nq, dn+dr]; ``k_nope``: [B, H, Nk, dn]; ``k_rope``: [B, Nk,
     dr], shared by the heads; ``v``: [B, H, Nk, dv]; ``o``: [B, H, Nq, dv].
-    ``causal``: row i sees keys j <= i + Nk - Nq.  bf16 (dn = 128, dr = 64, dv =
-    128) or float32 (dn + dr <= 256, dv <= 128).  ``scale`` defaults to
-    1/sqrt(dn + dr).
+    ``causal``: row i sees keys j <= i + Nk - Nq (sequences padded on the right
+    may share a call where their pasts, keys less queries, are equal).  bf16
+    (dn = 128, dr = 64, dv = 128) or float32 (dn + dr <= 256, dv <= 128).
+    ``scale`` defaults to 1/sqrt(dn + dr).
     """
     torch = _torch()
     code, (B, H, Nq, Nk, dn, dr, dv) = _check_latent(q, k_nope, k_rope, v)

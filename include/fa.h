@@ -289,9 +289,12 @@ size_t fa_fwd_latent_absorbed_workspace_bytes(int B, int H, int Nq, int page_siz
  *   causal       1: query row i sees keys j <= i + Nk - Nq (rows are the last
  *                Nq of Nk tokens; with Nq > Nk the first Nq - Nk rows see
  *                none); 0: every key.
- * A batch of unequal lengths is padded on the right, with finite values: with
- * causal = 1 no real token sees the padding behind it, and rows whose dO is 0
- * add nothing to the gradients.
+ * A batch of unequal lengths after pasts of one length (Nk - Nq tokens, 0 with
+ * Nq = Nk) is padded on the right, with finite values: with causal = 1 no real
+ * token sees the padding behind it, and rows whose dO is 0 add nothing to the
+ * gradients.  Sequences whose pasts differ cannot share a call: the mask is
+ * aligned at the end of the padded lengths, so that a row of a shorter past
+ * would see the padding, or miss keys of its own.
  * bf16 with dn = 128, dr = 64, dv = 128; float32 with dn + dr <= 256,
  * dv <= 128; others return FA_ERR_UNSUPPORTED.
  */

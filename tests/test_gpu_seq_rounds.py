@@ -83,3 +83,26 @@ def test_prefix_over_several_items_a_cta(fa, B, Hq, Hkv, Nq, Np, Ns, d, step):
         o_ref, lse_ref, tol_o, tol_l = expect("bf16", q[b:b + 1], kp, vp, k[b:b + 1], v[b:b + 1], lens[b:b + 1], d ** -0.5)
         sb.check(f"o[{b}]", sb.f64(o[b:b + 1]), o_ref, tol_o)
         sb.check(f"lse[{b}]", sb.f64(lse[b:b + 1]), lse_ref, tol_l)
+
+
+def test_expanded_chunk_padded_on_the_right(fa):
+    """Chunks of unequal length after pasts of one length, padded on the right
+    (finite values, dO = 0): results and gradients of the real tokens are those
+    of the call without padding, bit for bit for the forward and dq."""
+    past, Nq, real = 90, 200, 133
+    Nk = past + Nq
+    q, kn, kr, v, do = (t.cuda() for t in expanded("bf16", 2, 3, Nq, Nk, 128, 64, 128, seed=21))
+    do[:, :, real:] = 0
+    o, lse = fa.fa_fwd_latent(q, kn, kr, v)
+    grads = fa.fa_bwd_latent(q, kn, kr, v, o, lse, do)
+    n = past + real
+    cut = [t.contiguous() for t in (q[:, :, :real], kn[:, :, :n], kr[:, :n], v[:, :, :n])]
+    o2, lse2 = fa.fa_fwd_latent(*cut)
+    want = fa.fa_bwd_latent(*cut, o2, lse2, do[:, :, :real].contiguous())
+    assert torch.equal(o[:, :, :real], o2) and torch.equal(lse[:, :, :real], lse2)
+    assert torch.equal(grads[0][:, :, :real], want[0])
+    # dk and dv: the padded rows add products with zeros, so that only the sign of a zero could differ
+    for got, ref in ((grads[1][:, :, :n], want[1]), (grads[2][:, :n], want[2]), (grads[3][:, :, :n], want[3])):
+        assert (got == ref).all()
+    for g in (grads[1][:, :, n:], grads[2][:, n:], grads[3][:, :, n:]):
+        assert (g == 0).all()
