@@ -39,10 +39,17 @@
 // 384 threads: warps 0-7 element-wise (thread = row, warpgroup = half of the
 // 64 columns), warp 8 MMA issuer and TMEM owner, warp 9 TMA producer.
 //
-// Bound by the tensor core's shared-memory reads: a 128 x 64 product reads
-// (128 + 64) x 32 bytes of operands a K step (48 cycles at 128 bytes a cycle)
-// for 32 cycles of multiplying.  Forward and backward of 2 x 16 x 4096, causal:
-// 626 us, 990 TFLOP/s by the formulas' products, at the power limit.
+// Within an item, bound by the tensor core's shared-memory reads: a 128 x 64
+// product reads (128 + 64) x 32 bytes of operands a K step (48 cycles at 128
+// bytes a cycle) for 32 cycles of multiplying; a step of the keys form takes
+// 1545 cycles.  That is three quarters of the kernel: the keys form of 2 x 16 x
+// 4096, causal, has 222 steps an SM, 170 to 180 us, and takes 240.  By this count
+// the rest, some 9 us for each of a CTA's seven items, goes to their ends: the
+// element-wise warps write 128 x 320 outputs before they take up the next item,
+// whose stationary rows come into the one buffer that the last item's products
+// held.
+// Forward and backward of 2 x 16 x 4096: 632 us, 980 TFLOP/s by the formulas'
+// products, at the power limit (605 us before it bites).
 #include <cmath>
 
 #include "seq_sm103.cuh"
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (KEYS) {
           uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(pr[2 * c], pr[2 * c + 1]);
+          for (int c = 0; c < 16; ++c) pk[c] = pack_bf16x2(pr[2 * c], pr[2 * c + 1]);  // one rounding, for P^T dO
           tmem_st_32x32b_x16(tS, pk);
         }
         if (!warp_wait(bar.dp_full(), g & 1, wc) ||

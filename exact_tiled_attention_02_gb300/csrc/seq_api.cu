@@ -64,12 +64,19 @@ struct PrefixLayout {
 // SMs of their own (n and 152 - n) where that is faster than one after the
 // other, by measured rates: the first as seq_rows_time, the second 5 us and a
 // time an SM for a 64-key tile by its row columns (16, 32, 64), up to 6.2 TB/s
-// of keys and values (taking every sequence as three quarters of its room), the
-// merge 4 us and 5 TB/s of partial results.  While the second runs, the first
-// takes 1.5 times as long where one item reads a prefix tile (2.2 us a tile
-// for 1.45), 1.25 times where two share it, and so on.  (128 x 32 heads x 4
-// tokens, 32768 + 2048 keys, d = 128: 332 us one after the other, 264 side by
-// side; 64 x 32 x 1, 16384 + 1024 keys: 84 and 60.)
+// of keys and values, the merge 4 us and 5 TB/s of partial results.  While the
+// second runs, the first takes 1.5 times as long where one item reads a prefix
+// tile (2.2 us a tile for 1.45), 1.25 times where two share it, and so on.
+// The host does not see the lengths: the plan takes every sequence as three
+// quarters of its room, and the kernels keep its division whatever they are.
+// us, side by side by that plan and one after the other, with lengths of 2, 25,
+// 50, 75 and 100% of the room:
+//   128 x 32 heads x 4 tokens, 32768 + 2048 keys, d = 128:
+//     255 258 260 265 300   and   213 248 286 322 360
+//   64 x 32 x 1, 16384 + 1024:
+//     45 50 55 60 71        and   51 61 74 83 93
+// So a batch of drafted tokens that has just begun to generate in a large room
+// loses by the division up to about a third of the room, and gains from there on.
 PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   PrefixLayout w{};
   const int G = Hq / Hkv, R = B * G * Nq, block = G * Nq, kSms = 152;
@@ -124,7 +131,13 @@ bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
 }
 
 PartLayout absorbed_layout(int B, int H, int Nq, int n_keys, int dc) {
-  // (5 x 12 heads, up to 2047 tokens of 192 + 40: 25.3 us; one CTA an SM, 31.0)
+  // Twice as many CTAs as SMs.  Past 128 value columns one CTA fills an SM, and
+  // these are two rounds: that evens ragged lengths out where a CTA has few
+  // tiles, and costs parts to merge where it has many.  us with two and with one
+  // CTA an SM, lengths from 0 to the room and (in brackets) all equal to it:
+  // 5 x 12 heads, 2047 tokens of 192 + 40: 25 33 (33 34); of 512 + 64: 40 62 (60
+  // 62); 2 x 48, 3000 of 512 + 64: 62 81 (82 83); 4 x 20, 6000 of 192 + 40: 58 51
+  // (69 51); 8 x 16, 2500 of 512 + 64: 84 79 (110 79).
   const int sp = seq_simt_splits(B, H * Nq, n_keys, 2);
   return part_layout(sp, 0, static_cast<long long>(B) * H * Nq, dc);
 }

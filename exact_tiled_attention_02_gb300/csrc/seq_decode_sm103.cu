@@ -635,6 +635,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<DM, DX, SHARED, NR>::CTAS)
           const float4 nr = *reinterpret_cast<const float4*>(s_nref + col + c);
           const float p0 = ex2_approx(fmaf(s[c], sl, nr.x)), p1 = ex2_approx(fmaf(s[c + 1], sl, nr.y));
           const float p2 = ex2_approx(fmaf(s[c + 2], sl, nr.z)), p3 = ex2_approx(fmaf(s[c + 3], sl, nr.w));
+          // P is rounded to bf16, the products' type, half a step of 2^-8 each; O is
+          // divided by the sum of the rounded values, lse takes the unrounded ones
           const uint32_t a = pack_bf16x2(p0, p1), bq = pack_bf16x2(p2, p3);
           l[c] += p0;
           l[c + 1] += p1;

@@ -15,7 +15,7 @@
 // softmax takes them a half-warp a row.
 // Calls with few rows are bound by the latency of one tile's chunks (the keys
 // are split until every CTA has about one tile), many rows by the multiply-adds
-// (16 heads of 2500 tokens, 96 + 64 wide, causal: 804 us, 20 TFLOP/s).
+// (16 heads of 2500 tokens, q and k 96 wide, v 64, causal: 809 us, 20 TFLOP/s).
 #include <cmath>
 
 #include "seq_kernels.h"
@@ -304,15 +304,16 @@ cudaError_t launch_tr(const SeqAttn& p, bool beside, cudaStream_t s) {
 // Rows of a CTA: 32, or 16 where that leaves SMs idle (a chunk costs such a CTA
 // less, though more for each row).  Causal, 68 + 40 wide, 6 heads: 333 tokens
 // 33 us with 32 rows, 27 with 16; 1500 tokens 168 and 181.  (64 rows: 48 and
-// 169; 16 heads of 2500 tokens, 96 + 64 wide: 804 us with 32 rows, 875 with 64.)
+// 169; 16 heads of 2500 tokens, 96 and 64 wide: 804 us with 32 rows, 875 with 64.)
 int rows_per_cta(long long groups, int rows, int splits) {
   return rows > 16 && groups * ((rows + 31) / 32) * splits >= 152 ? 32 : 16;
 }
 
 }  // namespace
 
-// Splits of the keys: one round of CTAs, `ctas` an SM (a second round costs more
-// than a second tile), or a tile a split.
+// Splits of the keys: `ctas` CTAs an SM of 152, or a tile a split.  Where as many
+// fit an SM at once this is one round (a second one costs more than a second
+// tile); past 128 value columns only one does (absorbed_layout has both sides).
 int seq_simt_splits(long long groups, int rows, int max_keys, int ctas) {
   const int tr = rows <= 16 ? 16 : 32;
   const long long blocks = groups * ((rows + tr - 1) / tr);

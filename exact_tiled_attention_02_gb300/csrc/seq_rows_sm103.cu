@@ -29,7 +29,10 @@
 //
 // Bound by the tensor core and, beside it, the exponentials: per 128 x 128
 // scores 64 (DQK + DV) / 16 cycles of products against 16,384 exponentials.
-// 16 heads of 8192 tokens, 192 + 128 wide, causal: 235 us, 1465 TFLOP/s.
+// 16 heads of 8192 tokens, 192 + 128 wide, causal: 241 us, 1430 TFLOP/s, call
+// after call at the power limit (225 us in short runs before it bites).  The
+// prefix part: 8 groups of 2048 rows over 32768 keys, d = 128, on every SM: 197
+// us with its merge, 1395 TFLOP/s.
 #include <cmath>
 
 #include "seq_sm103.cuh"
