@@ -86,3 +86,34 @@ def test_absorbed_sequences_may_share_pages(fa, dtype):
     assert fa.fa_last_device_status() == fa.FA_OK
     sb.check("o", sb.f64(o), o_ref, tol_o)
     sb.check("lse", sb.f64(lse), lse_ref, tol_l)
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,Nq,Np,d,lens", [
+    ("bf16", 8, 2, 200, 0, 64, [200, 130]),    # a prompt: every token new, the second row of rows before its sequence
+    ("bf16", 4, 4, 150, 70, 128, [150, 400]),  # a chunk behind a prefix, one with a past of its own
+    ("f32", 6, 2, 70, 0, 40, [70, 20]),
+])
+def test_prompt_through_the_prefix_call(fa, dtype, Hq, Hkv, Nq, Np, d, lens):
+    """Nq new tokens with as many own keys: causal attention of a prompt with shared key heads."""
+    _prefix(fa, dtype, len(lens), Hq, Hkv, Nq, Np, max(lens), d, lens, seed=Nq)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_without_lse(fa, dtype):
+    """No lse wanted: the same O, bit for bit, whichever kernel writes it."""
+    host = make(dtype, 3, 8, 2, 1, 300, 90, 64, [90, 0, 7], seed=1)
+    args = [t.cuda() for t in host] + [torch.tensor([90, 0, 7], dtype=torch.int32, device="cuda")]
+    o, lse = fa.fa_fwd_shared_prefix(*args)
+    bare, none = fa.fa_fwd_shared_prefix(*args, want_lse=False)
+    assert none is None and lse is not None and torch.equal(o, bare)
+    q, cache, tab, _ = absorbed(dtype, 3, 16, 1, 16, 512, 64, [300, 0, 20], seed=2)  # merged, empty and whole pieces
+    args = (q.cuda(), cache.cuda(), torch.tensor([300, 0, 20], dtype=torch.int32, device="cuda"), 512, 0.07)
+    o, _ = fa.fa_fwd_latent_absorbed(*args, block_table=tab.cuda())
+    bare, none = fa.fa_fwd_latent_absorbed(*args, block_table=tab.cuda(), want_lse=False)
+    assert none is None and torch.equal(o, bare)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator().manual_seed(3)
+    q, kn, kr, v = (torch.randn(s, generator=g).to(t).cuda() for s in ((2, 3, 150, 192), (2, 3, 150, 128), (2, 150, 64), (2, 3, 150, 128)))
+    o, _ = fa.fa_fwd_latent(q, kn, kr, v)
+    bare, none = fa.fa_fwd_latent(q, kn, kr, v, want_lse=False)
+    assert none is None and torch.equal(o, bare)
