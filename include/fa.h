@@ -195,8 +195,9 @@ fa_status fa_bwd_static_workspace(const void* q, const void* k, const void* v, c
  * The calls below compute the same softmax attention with the head layouts,
  * caches and masks of a language model.  The pages describe none of them;
  * they are written from the formulas given here.  Common to all:
- *   - bf16 runs on the tensor cores (fp32 accumulation, P rounded to bf16
- *     before it multiplies V), float32 on CUDA cores in plain fp32.
+ *   - bf16 runs on the tensor cores (fp32 accumulation; P and, in the backward,
+ *     dS are rounded to bf16, the products' type, before they multiply, and D
+ *     comes from the rounded o), float32 on CUDA cores in plain fp32.
  *   - "New tokens": a sequence's Nq query tokens are its last ones, so query
  *     token t sees the keys j < n - (Nq - 1 - t) of its n keys.  A query row
  *     that sees no key (t too early, or an empty sequence) gets O = 0 and
