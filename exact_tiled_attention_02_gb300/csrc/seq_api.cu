@@ -167,6 +167,11 @@ bool expanded_sizes_ok(int B, int H, int Nq, int Nk, int dn, int dr, int dv) {
          sizes_ok(B, H, Nk, dr) && sizes_ok(B, H, Nk, dv) && dn <= 4096 && dr <= 4096 && dv <= 4096 &&
          static_cast<long long>(B) * H <= 0x7fffffffLL && Nq <= 0x3fffffff && Nk <= 0x3fffffff;
 }
+// and the backward's rows, padded to 128 a head: four a block of the float32 prep
+bool expanded_bwd_sizes_ok(int B, int H, int Nq, int Nk, int dn, int dr, int dv) {
+  return expanded_sizes_ok(B, H, Nq, Nk, dn, dr, dv) &&
+         static_cast<long long>(B) * H <= ((1LL << 33) - 1) / ((Nq + 127) / 128 * 128LL);
+}
 fa_status expanded_check(int B, int H, int Nq, int Nk, int dn, int dr, int dv, float scale, int causal, fa_dtype dt) {
   if (!expanded_sizes_ok(B, H, Nq, Nk, dn, dr, dv)) return FA_ERR_INVALID;
   if (!scale_ok(scale) || !dtype_ok(dt) || (causal != 0 && causal != 1)) return FA_ERR_INVALID;
@@ -389,7 +394,7 @@ fa_status fa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, c
 }
 
 size_t fa_bwd_latent_workspace_bytes(int B, int H, int Nq, int Nk, int dn, int dr, int dv) {
-  if (!expanded_sizes_ok(B, H, Nq, Nk, dn, dr, dv)) return 0;
+  if (!expanded_bwd_sizes_ok(B, H, Nq, Nk, dn, dr, dv)) return 0;
   return latent_bwd_workspace_layout(B, H, Nq, Nk, dr, nullptr, nullptr);
 }
 
@@ -401,6 +406,7 @@ fa_status fa_bwd_latent(const void* q, const void* k_nope, const void* k_rope, c
   for (const void* x : ptrs)
     if (!x || !aligned(x, 16)) return FA_ERR_INVALID;
   if (!lse || !aligned(lse, 4) || !workspace || !aligned(workspace, 256)) return FA_ERR_INVALID;
+  if (!expanded_bwd_sizes_ok(B, H, Nq, Nk, dn, dr, dv)) return FA_ERR_INVALID;
   const fa_status c = expanded_check(B, H, Nq, Nk, dn, dr, dv, scale, causal, dt);
   if (c != FA_OK) return c;
   if (workspace_bytes < fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dv)) return FA_ERR_INVALID;

@@ -215,11 +215,12 @@ fa_status fa_bwd_static_workspace(const void* q, const void* k, const void* v, c
  *     serves one call at a time: calls (and replays of graphs) that share one
  *     must run in order.
  *   - Sizes: every tensor at most 2^40 elements; expanded also B H < 2^31 and
- *     Nq, Nk < 2^30; shared prefix and absorbed B H Nq < 2^28 rows and, for
- *     float32 as for bf16, at most 7,040,929 tiles of 64 tokens in the batch's
- *     rooms, every sequence's room (Ns, or max_pages * page_size) rounded up to
- *     whole tiles (4.5e8 tokens where rooms are long, 7,040,929 sequences where
- *     they are short).  Past these FA_ERR_INVALID, and 0 from the queries.
+ *     Nq, Nk < 2^30, and in the backward B H Nq, Nq rounded up to 128, < 2^33;
+ *     shared prefix and absorbed B H Nq < 2^28 rows and, for float32 as for
+ *     bf16, at most 7,040,929 tiles of 64 tokens in the batch's rooms, every
+ *     sequence's room (Ns, or max_pages * page_size) rounded up to whole tiles
+ *     (4.5e8 tokens where rooms are long, 7,040,929 sequences where they are
+ *     short).  Past these FA_ERR_INVALID, and 0 from the queries.
  *   - The order of every sum is fixed by the shapes and the lengths: results
  *     repeat bit for bit.
  */

@@ -148,3 +148,13 @@ def test_expanded_lengths_are_limited(b):
         assert latent_bwd(b, B=1, H=1, Nq=Nq, Nk=Nk, dn=1, dr=1, dv=1, dt=0) == 1
         assert size(1, 1, Nq, Nk, 1, 1, 1) == 0
         assert size(1, 1, max(1, Nq - 1), max(1, Nk - 1), 1, 1, 1) > 0
+
+
+def test_latent_backward_limits_its_padded_rows(b):
+    """B H Nq, Nq rounded up to 128, below 2^33: where the first launch would be refused, the query and the call refuse."""
+    size = b.lib.fa_bwd_latent_workspace_bytes
+    assert size(1 << 13, (1 << 13) - 1, 128, 1, 1, 1, 1) > 0
+    for B, H, Nq in ((1 << 13, 1 << 13, 1), (1 << 13, (1 << 13) - 1, 129), (1 << 10, 1 << 20, 1)):
+        assert size(B, H, Nq, 1, 1, 1, 1) == 0, (B, H, Nq)
+        for dt in (0, 1):
+            assert latent_bwd(b, B=B, H=H, Nq=Nq, Nk=1, dn=1, dr=1, dv=1, dt=dt, wsb=(1 << 64) - 1) == 1, (B, H, Nq)
