@@ -26,7 +26,8 @@ EXPORTS = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_bytes", "fa_bwd_static_workspac
            "fa_fwd_key_major_workspace_bytes", "fa_fwd_f32_3xtf32", "fa_fwd_f32_3xtf32_workspace_bytes",
            "fa_fwd_shared_prefix", "fa_fwd_shared_prefix_workspace_bytes", "fa_fwd_latent_absorbed",
            "fa_fwd_latent_absorbed_workspace_bytes", "fa_fwd_latent", "fa_bwd_latent", "fa_bwd_latent_workspace_bytes",
-           "fa_last_device_status", "fa_set_wait_limit_us", "fa_selftest_wait_timeout", "fa_status_string",
+           "fa_cache_fp4_bytes", "fa_cache_fp4_write", "fa_cache_fp4_read", "fa_fwd_cache_fp4",
+           "fa_fwd_cache_fp4_workspace_bytes", "fa_last_device_status", "fa_set_wait_limit_us", "fa_selftest_wait_timeout", "fa_status_string",
            "fa_version")
 
 
@@ -72,6 +73,16 @@ def _load() -> ctypes.CDLL:
     L.fa_bwd_latent.restype = i
     L.fa_bwd_latent_workspace_bytes.argtypes = [i] * 7
     L.fa_bwd_latent_workspace_bytes.restype = sz
+    L.fa_cache_fp4_bytes.argtypes = [i] * 4
+    L.fa_cache_fp4_bytes.restype = sz
+    L.fa_cache_fp4_write.argtypes = [vp] * 6 + [i] * 7 + [f, f, i, vp]
+    L.fa_cache_fp4_write.restype = i
+    L.fa_cache_fp4_read.argtypes = [vp] * 6 + [i] * 7 + [f, f, i, vp]
+    L.fa_cache_fp4_read.restype = i
+    L.fa_fwd_cache_fp4.argtypes = [vp] * 6 + [i] * 8 + [f, f, f, i, vp, sz, vp]
+    L.fa_fwd_cache_fp4.restype = i
+    L.fa_fwd_cache_fp4_workspace_bytes.argtypes = [i] * 7
+    L.fa_fwd_cache_fp4_workspace_bytes.restype = sz
     L.fa_last_device_status.argtypes = [vp]
     L.fa_last_device_status.restype = i
     L.fa_set_wait_limit_us.argtypes = [ctypes.c_longlong]
@@ -330,6 +341,14 @@ def fa_bwd_latent_workspace_bytes(B: int, H: int, Nq: int, Nk: int, dn: int, dr:
     return lib.fa_bwd_latent_workspace_bytes(B, H, Nq, Nk, dn, dr, dv)
 
 
+def fa_cache_fp4_bytes(n_pages: int, Hkv: int, page_size: int, d: int) -> int:
+    return lib.fa_cache_fp4_bytes(n_pages, Hkv, page_size, d)
+
+
+def fa_fwd_cache_fp4_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, page_size: int, max_pages: int, d: int) -> int:
+    return lib.fa_fwd_cache_fp4_workspace_bytes(B, Hq, Hkv, Nq, page_size, max_pages, d)
+
+
 def _at(t):
     return 0 if t is None else t.data_ptr()
 
@@ -560,3 +579,123 @@ def fa_bwd_latent(q, k_nope, k_rope, v, o, lse, do, scale: float | None = None, 
     if st != FA_OK:
         raise FaError(st, "fa_bwd_latent")
     return dq, dk_nope, dk_rope, dv
+
+
+def _check_cache(cache, lens, block_table, B, Hkv, d, dev):
+    """The sizes of a 4-bit cache: pages, tokens a page, pages a sequence."""
+    torch = _torch()
+    if cache.dim() != 4:
+        raise ValueError("cache must be [pages, Hkv, page_size, 9 d / 8]")
+    pages, _, page_size, _ = cache.shape
+    _need("cache", cache, (pages, Hkv, page_size, 9 * d // 8), torch.uint8, dev)
+    _need("lens", lens, (B,), torch.int32, dev)
+    if block_table is None:
+        return pages, page_size, 1
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    max_pages = block_table.shape[1]
+    _need("block_table", block_table, (B, max_pages), torch.int32, dev)
+    return pages, page_size, max_pages
+
+
+def fa_cache_fp4_write(k, v, cache, lens, block_table=None, n_new=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                       stream=None):
+    """Writes new tokens' keys and values into a 4-bit paged cache, in place.
+
+    ``k, v``: [B, Hkv, Nn, d], bf16 or float32, row t of sequence b the token
+    at position ``lens[b] - Nn + t``; ``cache``: uint8 [pages, Hkv, page_size,
+    9 d / 8] (page_size and d multiples of 16, d <= 256); ``lens``: int32 [B],
+    tokens in the cache, the new ones included; ``block_table``: int32 [B,
+    max_pages], or None when sequence b is page b; ``n_new``: int32 [B], how
+    many of the last rows are tokens of sequence b, or None for all.
+    ``k_scale, v_scale``: what the stored numbers are multiples of (the header
+    has the format).
+    """
+    torch = _torch()
+    code = _first("k", k, 4)
+    dev = k.device
+    sp = _current_stream(dev, stream)
+    if sp is None:
+        with _made_current(dev, stream):
+            return fa_cache_fp4_write(k, v, cache, lens, block_table, n_new, k_scale, v_scale)
+    B, Hkv, Nn, d = k.shape
+    _need("v", v, (B, Hkv, Nn, d), k.dtype, dev)
+    pages, page_size, max_pages = _check_cache(cache, lens, block_table, B, Hkv, d, dev)
+    if n_new is not None:
+        _need("n_new", n_new, (B,), torch.int32, dev)
+    st = lib.fa_cache_fp4_write(_at(k), _at(v), _at(cache), _at(block_table), _at(lens), _at(n_new), B, Hkv, Nn, pages,
+                                page_size, max_pages, d, k_scale, v_scale, code, sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_fp4_write")
+
+
+def fa_cache_fp4_read(cache, lens, N: int, dtype=None, block_table=None, first=None, k_scale: float = 1.0,
+                      v_scale: float = 1.0, k=None, v=None, stream=None):
+    """Cached tokens as the numbers they stand for; returns ``(k, v)``, [B, Hkv, N, d].
+
+    Row t of sequence b is position ``first[b] + t`` (int32 [B]; None: 0);
+    positions below 0 or from ``lens[b]`` on are zeros.  Other arguments as
+    ``fa_cache_fp4_write``.  ``dtype``: torch.bfloat16 (default) or
+    torch.float32, unless ``k`` and ``v`` are given to be written to.
+    """
+    torch = _torch()
+    if cache.dim() != 4 or lens.dim() != 1:
+        raise ValueError("cache must be [pages, Hkv, page_size, 9 d / 8] and lens [B]")
+    if not cache.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    dev = cache.device
+    sp = _current_stream(dev, stream)
+    if sp is None:
+        with _made_current(dev, stream):
+            return fa_cache_fp4_read(cache, lens, N, dtype, block_table, first, k_scale, v_scale, k, v)
+    B, Hkv, d = lens.shape[0], cache.shape[1], cache.shape[3] * 8 // 9
+    if dtype is None:
+        dtype = torch.bfloat16 if k is None else k.dtype
+    pages, page_size, max_pages = _check_cache(cache, lens, block_table, B, Hkv, d, dev)
+    if first is not None:
+        _need("first", first, (B,), torch.int32, dev)
+    shape = (B, Hkv, N, d)
+    k, v = (torch.empty(shape, dtype=dtype, device=dev) if x is None else _need(name, x, shape, dtype, dev)
+            for name, x in (("k", k), ("v", v)))
+    st = lib.fa_cache_fp4_read(_at(cache), _at(block_table), _at(lens), _at(first), _at(k), _at(v), B, Hkv, N, pages,
+                               page_size, max_pages, d, k_scale, v_scale, _dtype_code(k), sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_fp4_read")
+    return k, v
+
+
+def fa_fwd_cache_fp4(q, cache, lens, scale: float | None = None, block_table=None, k_scale: float = 1.0,
+                     v_scale: float = 1.0, o=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """Attention of each sequence's last Nq tokens over a 4-bit paged cache; returns ``(o, lse)``.
+
+    ``q``: [B, Hq, Nq, d], bf16 or float32; query token t sees the keys j <
+    lens[b] - (Nq - 1 - t), query head h key/value head h // (Hq // Hkv).
+    ``cache, lens, block_table, k_scale, v_scale`` as ``fa_cache_fp4_write``
+    takes them.  ``scale`` defaults to 1/sqrt(d).  ``workspace``: at least
+    ``fa_fwd_cache_fp4_workspace_bytes`` bytes, or allocated here.
+    """
+    torch = _torch()
+    code = _first("q", q, 4)
+    dev = q.device
+    sp = _current_stream(dev, stream)
+    if sp is None:
+        with _made_current(dev, stream):
+            return fa_fwd_cache_fp4(q, cache, lens, scale, block_table, k_scale, v_scale, o, lse, want_lse, workspace)
+    B, Hq, Nq, d = q.shape
+    if cache.dim() != 4:
+        raise ValueError("cache must be [pages, Hkv, page_size, 9 d / 8]")
+    Hkv = cache.shape[1]
+    pages, page_size, max_pages = _check_cache(cache, lens, block_table, B, Hkv, d, dev)
+    o = torch.empty_like(q) if o is None else _need("o", o, (B, Hq, Nq, d), q.dtype, dev)
+    if lse is not None:
+        _need("lse", lse, (B, Hq, Nq), torch.float32, dev)
+    elif want_lse:
+        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+    need = fa_fwd_cache_fp4_workspace_bytes(B, Hq, Hkv, Nq, page_size, max_pages, d)
+    with _Workspace(workspace, need, dev, sp) as ws:
+        st = lib.fa_fwd_cache_fp4(_at(q), _at(cache), _at(block_table), _at(lens), _at(o), _at(lse), B, Hq, Hkv, Nq,
+                                  pages, page_size, max_pages, d, 1.0 / math.sqrt(d) if scale is None else scale,
+                                  k_scale, v_scale, code, ws.at, ws.bytes, sp)
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_cache_fp4")
+    return o, lse

@@ -1,0 +1,130 @@
+// cache4_api.cu -- the C ABI of the 4-bit key/value cache declared in
+// include/fa.h: writing new tokens, reading tokens back, attention over it.
+// Argument checks, workspace layouts, dispatch.  Nothing here allocates device
+// memory or synchronises.
+#include "seq_checks.h"
+
+namespace fa {
+namespace {
+
+constexpr int kMaxD = 256;
+
+fa_status cache_check(const void* cache, const int* table, const int* lens, int B, int Hkv, int n_pages, int page_size,
+                      int max_pages, int d, float k_scale, float v_scale, fa_dtype dt) {
+  if (!cache || !lens || !aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4)) return FA_ERR_INVALID;
+  if (!sizes_ok(n_pages, Hkv, page_size, d) || !sizes_ok(B, Hkv) || max_pages < 1) return FA_ERR_INVALID;
+  if (!sizes_ok(B, max_pages) || paged_keys(page_size, max_pages) < 0) return FA_ERR_INVALID;
+  if (!table && (max_pages != 1 || n_pages < B)) return FA_ERR_INVALID;
+  if (!scale_ok(k_scale) || !scale_ok(v_scale) || !dtype_ok(dt)) return FA_ERR_INVALID;
+  if (page_size % 16 != 0 || d % 16 != 0 || d > kMaxD) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+// a warp a block of 16 tokens and head, four a CTA
+bool blocks_ok(int B, int Hkv, int n) {
+  return sizes_ok(B, Hkv, n) && n <= 0x3fffffff &&
+         static_cast<double>(B) * Hkv * ((n + 14) / 16 + 1) < 4.0 * 0x7ffffff0;
+}
+Cache4 cache_of(const void* cache, const int* table, const int* lens, int B, int Hkv, int n_pages, int page_size,
+                int max_pages, int d, float k_scale, float v_scale) {
+  Cache4 c{};
+  c.cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+  c.table = table;
+  c.lens = lens;
+  c.B = B;
+  c.Hkv = Hkv;
+  c.d = d;
+  c.page_size = page_size;
+  c.max_pages = max_pages;
+  c.n_pages = n_pages;
+  c.k_scale = k_scale;
+  c.v_scale = v_scale;
+  return c;
+}
+
+bool attn_sizes_ok(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages, int d) {
+  if (Hkv < 1 || Hq % Hkv != 0 || page_size < 1 || d > kMaxD) return false;
+  const long long keys = paged_keys(page_size, max_pages);
+  return sizes_ok(B, Hq, Nq, d) && sizes_ok(B, max_pages) && keys > 0 &&
+         static_cast<long long>(B) * Hq * Nq <= 0x7fffffffLL / 8 && tiles_ok(B, keys);
+}
+PartLayout attn_layout(int B, int Hq, int Hkv, int Nq, int n_keys, int d) {
+  return part_layout(cache4_simt_splits(B, Hq, Hkv, Nq, n_keys, d), 0, static_cast<long long>(B) * Hq * Nq, d);
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_cache_fp4_bytes(int n_pages, int Hkv, int page_size, int d) {
+  if (!sizes_ok(n_pages, Hkv, page_size, d) || page_size % 16 != 0 || d % 16 != 0 || d > kMaxD) return 0;
+  return static_cast<size_t>(n_pages) * Hkv * page_size * (9 * d / 8);
+}
+
+fa_status fa_cache_fp4_write(const void* k, const void* v, void* cache, const int* block_table, const int* lens,
+                             const int* n_new, int B, int Hkv, int Nn, int n_pages, int page_size, int max_pages,
+                             int d, float k_scale, float v_scale, fa_dtype dt, void* stream) {
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(n_new, 4)) return FA_ERR_INVALID;
+  const fa_status st =
+      cache_check(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale, dt);
+  if (st != FA_OK) return st;
+  if (!sizes_ok(B, Hkv, Nn, d) || !blocks_ok(B, Hkv, Nn)) return FA_ERR_INVALID;
+  Cache4 c = cache_of(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale);
+  if (device_status_ptr(&c.status) != cudaSuccess) return FA_ERR_CUDA;
+  return of(launch_cache4_write(c, k, v, n_new, Nn, dt, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_cache_fp4_read(const void* cache, const int* block_table, const int* lens, const int* first, void* k,
+                            void* v, int B, int Hkv, int N, int n_pages, int page_size, int max_pages, int d,
+                            float k_scale, float v_scale, fa_dtype dt, void* stream) {
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16) || !aligned(first, 4)) return FA_ERR_INVALID;
+  const fa_status st =
+      cache_check(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale, dt);
+  if (st != FA_OK) return st;
+  if (!sizes_ok(B, Hkv, N, d) || !blocks_ok(B, Hkv, N)) return FA_ERR_INVALID;
+  Cache4 c = cache_of(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale);
+  if (device_status_ptr(&c.status) != cudaSuccess) return FA_ERR_CUDA;
+  return of(launch_cache4_read(c, first, k, v, N, dt, static_cast<cudaStream_t>(stream)));
+}
+
+size_t fa_fwd_cache_fp4_workspace_bytes(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages, int d) {
+  if (!attn_sizes_ok(B, Hq, Hkv, Nq, page_size, max_pages, d)) return 0;
+  return attn_layout(B, Hq, Hkv, Nq, static_cast<int>(paged_keys(page_size, max_pages)), d).bytes;
+}
+
+fa_status fa_fwd_cache_fp4(const void* q, const void* cache, const int* block_table, const int* lens, void* o,
+                           float* lse, int B, int Hq, int Hkv, int Nq, int n_pages, int page_size, int max_pages,
+                           int d, float scale, float k_scale, float v_scale, fa_dtype dt, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  if (!q || !o || !workspace || !aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return FA_ERR_INVALID;
+  if (!attn_sizes_ok(B, Hq, Hkv, Nq, page_size, max_pages, d) && d <= kMaxD) return FA_ERR_INVALID;
+  const fa_status st =
+      cache_check(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale, dt);
+  if (st != FA_OK) return st;
+  if (!scale_ok(scale) || !scale_ok(scale * k_scale)) return FA_ERR_INVALID;
+  if (workspace_bytes < fa_fwd_cache_fp4_workspace_bytes(B, Hq, Hkv, Nq, page_size, max_pages, d))
+    return FA_ERR_INVALID;
+  Cache4 c = cache_of(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale);
+  if (device_status_ptr(&c.status) != cudaSuccess) return FA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const PartLayout w = attn_layout(B, Hq, Hkv, Nq, page_size * max_pages, d);
+  Cache4Attn p{};
+  p.c = c;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.Hq = Hq;
+  p.n_new = Nq;
+  p.scale = scale;
+  p.splits = w.splits_a;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.off_lse);
+  const cudaError_t e = launch_cache4_simt(p, dt, s);
+  if (e != cudaSuccess || p.splits == 1) return of(e);
+  return of(launch_seq_combine(p.part_o, p.part_lse, p.splits, static_cast<long long>(B) * Hq * Nq, d, o, dt, lse, s));
+}
+
+}  // extern "C"

@@ -5,45 +5,10 @@
 #include <cmath>
 #include <cstdint>
 
-#include "fa.h"
-#include "seq_kernels.h"
+#include "seq_checks.h"
 
 namespace fa {
 namespace {
-
-bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-
-// a * b * ... of positive ints, or -1 past 2^40
-long long product(const int* x, int n) {
-  long long r = 1;
-  for (int i = 0; i < n; ++i) {
-    if (x[i] < 1) return -1;
-    if (r > (1LL << 40) / x[i]) return -1;
-    r *= x[i];
-  }
-  return r;
-}
-template <typename... I>
-bool sizes_ok(I... x) {
-  const int v[] = {x...};
-  return product(v, sizeof...(x)) > 0;
-}
-bool scale_ok(float scale) { return std::isfinite(scale) && scale > 0.f; }
-bool dtype_ok(fa_dtype dt) { return dt == FA_DTYPE_F32 || dt == FA_DTYPE_BF16; }
-
-// partial results [splits][rows] of dv entries and their lse
-struct PartLayout {
-  int splits_a, splits_b;
-  size_t off_lse, bytes;
-};
-PartLayout part_layout(int sa, int sb, long long rows, int dv) {
-  PartLayout w{sa, sb, 0, 0};
-  const size_t n = static_cast<size_t>(sa + sb) * rows;
-  w.off_lse = up256(n * dv * 4);
-  w.bytes = w.off_lse + up256(n * 4);
-  return w;
-}
 
 PartLayout prefix_layout(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   const int G = Hq / Hkv;
@@ -121,8 +86,6 @@ PrefixLayout prefix_layout_bf16(int B, int Hq, int Hkv, int Nq, int Np, int Ns, 
   w.bytes = w.off_lse + up256(slots * 4);
   return w;
 }
-// the sequences' 64-key tiles, times the most ranges they are cut into, stay below 2^31
-bool tiles_ok(int n_seq, long long n_keys) { return n_seq * ((n_keys + 63) / 64) * 305 <= 0x7fffffffLL; }
 bool prefix_sizes_ok(int B, int Hq, int Hkv, int Nq, int Np, int Ns, int d) {
   // (Np past 2^31 - 256 would round up to tiles past 32 bits; Ns is held lower by tiles_ok)
   if (Np < 0 || Np > 0x7fffff00 || Ns < 0 || Hkv < 1 || Hq % Hkv != 0) return false;
@@ -149,16 +112,11 @@ DecodePlan absorbed_plan(int B, int H, int Nq, int page_size, bool table) {
   const int box = !table || page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
   return decode_plan(B, 1, H * Nq, true, box, 152);
 }
-// tokens a sequence can hold, or -1
-long long absorbed_keys(int page_size, int max_pages) {
-  const long long n = static_cast<long long>(page_size) * max_pages;
-  return n <= 0x7fffff00LL ? n : -1;
-}
 // What the layouts and plans above count on (rows and tiles in 32 bits): the
 // workspace query's check and part of the call's.
 bool absorbed_sizes_ok(int B, int H, int Nq, int page_size, int max_pages, int dc) {
   if (!sizes_ok(B, H, Nq, dc) || dc > 4096 || !sizes_ok(B, max_pages) || page_size < 1) return false;
-  const long long keys = absorbed_keys(page_size, max_pages);
+  const long long keys = paged_keys(page_size, max_pages);
   return static_cast<long long>(B) * H * Nq <= 0x7fffffffLL / 8 && keys > 0 && tiles_ok(B, keys);
 }
 
@@ -179,8 +137,6 @@ fa_status expanded_check(int B, int H, int Nq, int Nk, int dn, int dr, int dv, f
   if (dt == FA_DTYPE_F32 && (dn + dr > 256 || dv > 128)) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
-
-fa_status of(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
 }  // namespace
 }  // namespace fa
@@ -279,13 +235,13 @@ fa_status fa_fwd_shared_prefix(const void* q, const void* k_prefix, const void* 
   cudaError_t e = launch_seq_simt(a, false, s);
   if (e == cudaSuccess) e = launch_seq_simt(b, true, s);
   if (e == cudaSuccess)
-    e = launch_seq_combine(a.part_o, a.part_lse, w.splits_a + w.splits_b, p.total, d, static_cast<float*>(o), lse, s);
+    e = launch_seq_combine(a.part_o, a.part_lse, w.splits_a + w.splits_b, p.total, d, o, dt, lse, s);
   return of(e);
 }
 
 size_t fa_fwd_latent_absorbed_workspace_bytes(int B, int H, int Nq, int page_size, int max_pages, int dc) {
   if (!absorbed_sizes_ok(B, H, Nq, page_size, max_pages, dc)) return 0;
-  const size_t f32 = absorbed_layout(B, H, Nq, static_cast<int>(absorbed_keys(page_size, max_pages)), dc).bytes;
+  const size_t f32 = absorbed_layout(B, H, Nq, static_cast<int>(paged_keys(page_size, max_pages)), dc).bytes;
   const size_t bf16 = absorbed_layout_bf16(absorbed_plan(B, H, Nq, page_size, true), dc).bytes;
   return f32 > bf16 ? f32 : bf16;
 }
@@ -304,7 +260,7 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
   if (dt == FA_DTYPE_BF16 && !((dc == 256 || dc == 512) && dr == 64)) return FA_ERR_UNSUPPORTED;
   if (dt == FA_DTYPE_BF16 && block_table && page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
   if (dt == FA_DTYPE_F32 && (dc > 512 || dr > 128)) return FA_ERR_UNSUPPORTED;
-  const int n_keys = static_cast<int>(absorbed_keys(page_size, max_pages));
+  const int n_keys = static_cast<int>(paged_keys(page_size, max_pages));
   if (workspace_bytes < fa_fwd_latent_absorbed_workspace_bytes(B, H, Nq, page_size, max_pages, dc))
     return FA_ERR_INVALID;
 
@@ -351,7 +307,7 @@ fa_status fa_fwd_latent_absorbed(const void* q, const void* cache, const int* bl
   if (w.splits_a == 1) p.part_o = p.part_lse = nullptr;
   const cudaError_t e = launch_seq_simt(p, false, s);
   if (e != cudaSuccess || w.splits_a == 1) return of(e);
-  return of(launch_seq_combine(p.part_o, p.part_lse, w.splits_a, p.total, dc, static_cast<float*>(o), lse, s));
+  return of(launch_seq_combine(p.part_o, p.part_lse, w.splits_a, p.total, dc, o, dt, lse, s));
 }
 
 fa_status fa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, void* o, float* lse,

@@ -1,5 +1,5 @@
 // seq_combine.cu -- merges partial attention results of one query row over
-// disjoint sets of keys (float32 outputs).
+// disjoint sets of keys.
 //
 // Partial result s of a row is (O_s, lse_s), normalised over its own keys.
 // With M = max_s lse_s and w_s = exp(lse_s - M):  O = sum_s w_s O_s / sum_s w_s,
@@ -20,9 +20,10 @@ namespace {
 
 constexpr int kWarps = 4;
 
+template <typename T>
 __global__ void __launch_bounds__(kWarps * 32)
     fa_seq_combine_kernel(const float* __restrict__ part_o, const float* __restrict__ part_lse, int splits,
-                          long long total, int dv, float* __restrict__ o, float* __restrict__ lse) {
+                          long long total, int dv, T* __restrict__ o, float* __restrict__ lse) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int slices = (dv + 31) / 32;
   const long long idx = static_cast<long long>(blockIdx.x) * kWarps + warp;
@@ -53,18 +54,27 @@ __global__ void __launch_bounds__(kWarps * 32)
       if (wi != 0.f && c < dv) acc = fmaf(wi, part_o[((s0 + i) * total + row) * dv + c], acc);
     }
   }
-  if (c < dv) o[row * dv + c] = acc;
+  if (c < dv) {
+    if constexpr (sizeof(T) == 4)
+      o[row * dv + c] = acc;
+    else
+      o[row * dv + c] = __float2bfloat16_rn(acc);
+  }
   if (slice == 0 && lane == 0 && lse != nullptr) lse[row] = m + logf(n);
 }
 
 }  // namespace
 
 cudaError_t launch_seq_combine(const float* part_o, const float* part_lse, int splits, long long total, int dv,
-                               float* o, float* lse, cudaStream_t s) {
+                               void* o, fa_dtype dt, float* lse, cudaStream_t s) {
   const long long blocks = (total * ((dv + 31) / 32) + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return seq::launch_after(fa_seq_combine_kernel, static_cast<unsigned>(blocks), kWarps * 32, 0, s, part_o, part_lse,
-                           splits, total, dv, o, lse);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  if (dt == FA_DTYPE_BF16)
+    return seq::launch_after(fa_seq_combine_kernel<__nv_bfloat16>, grid, kWarps * 32, 0, s, part_o, part_lse, splits,
+                             total, dv, static_cast<__nv_bfloat16*>(o), lse);
+  return seq::launch_after(fa_seq_combine_kernel<float>, grid, kWarps * 32, 0, s, part_o, part_lse, splits, total, dv,
+                           static_cast<float*>(o), lse);
 }
 
 }  // namespace fa

@@ -92,9 +92,49 @@ cudaError_t launch_seq_decode(const SeqAttn& p, const DecodePlan& w, bool beside
 cudaError_t launch_seq_decode_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse,
                                     int pre, bool after, cudaStream_t s);
 
-// float32 o, lse = the merged partial results [splits][total] (seq_combine.cu).
+// o, lse = the merged partial results [splits][total] (seq_combine.cu).
 cudaError_t launch_seq_combine(const float* part_o, const float* part_lse, int splits, long long total, int dv,
-                               float* o, float* lse, cudaStream_t s);
+                               void* o, fa_dtype dt, float* lse, cudaStream_t s);
+
+// A key/value cache in 4 bits (layout and helpers: cache4.cuh).
+struct Cache4 {
+  uint8_t* cache;    // [n_pages][Hkv][page_size / 16] blocks of 18 d bytes
+  const int* table;  // [B][max_pages], or null: sequence b is page b
+  const int* lens;   // [B]
+  int B, Hkv, d;
+  int page_size, max_pages, n_pages;
+  float k_scale, v_scale;
+  unsigned int* status;
+};
+// New tokens k, v [B,Hkv,Nn,d] to the positions before lens (cache4_rw.cu).
+cudaError_t launch_cache4_write(const Cache4& c, const void* k, const void* v, const int* n_new, int Nn, fa_dtype dt,
+                                cudaStream_t s);
+// Positions first[b] .. first[b] + N - 1 (from 0 where first is null) to k, v [B,Hkv,N,d].
+cudaError_t launch_cache4_read(const Cache4& c, const int* first, void* k, void* v, int N, fa_dtype dt, cudaStream_t s);
+
+// Attention of each sequence's last n_new tokens, q and o [B,Hq,n_new,d], over
+// the cache.
+struct Cache4Attn {
+  Cache4 c;
+  const void* q;
+  void* o;
+  float* lse;  // may be null
+  int Hq, n_new;
+  float scale;
+  // splits > 1: results go to part_o [split][B Hq n_new][d] and part_lse [split][B Hq n_new] instead of o and lse
+  int splits;
+  float* part_o;
+  float* part_lse;
+};
+// On CUDA cores, any type and d (cache4_fwd_simt.cu).
+cudaError_t launch_cache4_simt(const Cache4Attn& p, fa_dtype dt, cudaStream_t s);
+int cache4_simt_splits(int B, int Hq, int Hkv, int n_new, int n_keys, int d);
+
+// bf16 on the tensor cores, d = 64, 96 or 128 (cache4_decode_sm103.cu).  p: as for
+// launch_seq_decode, groups (sequence, key/value head), page fields and k1, v unused.
+DecodePlan cache4_plan(int n_seq, int heads, int rows, int sms);
+cudaError_t launch_cache4_decode(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s);
+cudaError_t launch_cache4_merge(const SeqAttn& p, const DecodePlan& w, cudaStream_t s);
 
 // Expanded latent attention's backward.
 struct LatentBwd {

@@ -321,6 +321,85 @@ fa_status fa_bwd_latent(const void* q, const void* k_nope, const void* k_rope, c
 size_t fa_bwd_latent_workspace_bytes(int B, int H, int Nq, int Nk, int dn, int dr, int dv);
 
 /*
+ * A key/value cache in 4 bits, and the attention that reads it
+ * ------------------------------------------------------------
+ * Keys and values of a decoding batch with key/value heads shared by query
+ * heads, held at 4.5 bits an entry (9 d bytes for 8 tokens of a head, keys and
+ * values together: bf16 takes 32 d).
+ *   Format     16 neighbouring entries x of a token's key (or value) of one head
+ *              are a group.  With y = x / k_scale (x / v_scale; float32), the
+ *              group's scale is s = amax |y| / 6 rounded to e4m3 (nearest, ties
+ *              to even, at most 448; below 2^-10 it is 0, and so is the group),
+ *              and an entry's code is the e2m1 number nearest to y / s: one of
+ *              +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}, ties to even, at most 6.  It
+ *              stands for code * s * k_scale.  So an entry is off by at most
+ *              amax / 6 but for what s is rounded (1/16).  k_scale and v_scale
+ *              map the tensors onto what a scale can hold, 2^-9 to 448: entries
+ *              up to 2688 k_scale, larger ones (infinities too) become that.  A
+ *              group that holds a NaN is NaN.
+ *   cache      uint8 [n_pages][Hkv][page_size][9 d / 8], 16-byte aligned.  Of
+ *              every page and head, 16 tokens are a block of 18 d bytes: key
+ *              codes [d/16][16 tokens][8], key scales [16 tokens][d/16], value
+ *              codes [d][8] (a channel's 16 tokens), value scales [d/16][16
+ *              tokens].  The first of the two codes in a byte is in its low half.
+ *   block_table, lens  as for the absorbed form: int32 [B,max_pages] (NULL:
+ *              sequence b is page b; then max_pages must be 1 and n_pages >= B)
+ *              and int32 [B], the tokens in the cache, new ones included.  Of
+ *              the conventions above those on new tokens, device-side lengths
+ *              and pages, uncovered positions (any bytes), workspaces and sizes
+ *              hold here too, with Nq for new queries, unless stated otherwise.
+ *   Sizes      page_size and d multiples of 16, d <= 256 (others return
+ *              FA_ERR_UNSUPPORTED).
+ */
+
+/* Bytes of a cache, or 0 for sizes that the calls refuse. */
+size_t fa_cache_fp4_bytes(int n_pages, int Hkv, int page_size, int d);
+
+/*
+ * Writes a step's keys and values into the cache.
+ *   k, v         [B,Hkv,Nn,d], bf16 or float32: row t of sequence b is the token
+ *                at position lens[b] - Nn + t.
+ *   n_new        int32 [B], or NULL: how many of the Nn rows, the last ones, are
+ *                tokens of sequence b (0 <= n_new[b] <= Nn; clamped and reported
+ *                as lens is); the rows before them are padding and not read.
+ *                NULL: all.  Rows whose position is below 0 are padding too.
+ *   lens         a length out of range is reported, and nothing of that
+ *                sequence written.
+ * Other tokens of the cache keep their bits.  A byte holds codes of two
+ * neighbouring tokens: calls that write to one page must run in order, and a
+ * page must not appear twice among those that a call writes to.
+ */
+fa_status fa_cache_fp4_write(const void* k, const void* v, void* cache, const int* block_table, const int* lens,
+                             const int* n_new, int B, int Hkv, int Nn, int n_pages, int page_size, int max_pages,
+                             int d, float k_scale, float v_scale, fa_dtype dt, void* stream);
+
+/*
+ * Reads cached tokens back as the numbers they stand for.
+ *   first        int32 [B], or NULL (0): row t of sequence b is position
+ *                first[b] + t.
+ *   k, v         [B,Hkv,N,d], bf16 or float32; rows at positions below 0 or from
+ *                lens[b] on are zeros.
+ */
+fa_status fa_cache_fp4_read(const void* cache, const int* block_table, const int* lens, const int* first, void* k,
+                            void* v, int B, int Hkv, int N, int n_pages, int page_size, int max_pages, int d,
+                            float k_scale, float v_scale, fa_dtype dt, void* stream);
+
+/*
+ * Attention of each sequence's last Nq tokens over the cache: query token t
+ * sees the keys j < lens[b] - (Nq - 1 - t), query head h uses key/value head
+ * h / (Hq / Hkv).
+ *   q, o         [B,Hq,Nq,d], bf16 or float32.   lse  float32 [B,Hq,Nq] or NULL.
+ *   workspace    at least fa_fwd_cache_fp4_workspace_bytes() bytes, 256-byte
+ *                aligned, as above.
+ * Hq must be a multiple of Hkv.  Forward only: a serving call.
+ */
+fa_status fa_fwd_cache_fp4(const void* q, const void* cache, const int* block_table, const int* lens, void* o,
+                           float* lse, int B, int Hq, int Hkv, int Nq, int n_pages, int page_size, int max_pages,
+                           int d, float scale, float k_scale, float v_scale, fa_dtype dt, void* workspace,
+                           size_t workspace_bytes, void* stream);
+size_t fa_fwd_cache_fp4_workspace_bytes(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages, int d);
+
+/*
  * Synchronises `stream` (as void* cudaStream_t), then reads and clears the
  * device status word that the kernels set when a bounded wait runs out.
  * Returns FA_OK, FA_ERR_TIMEOUT, FA_ERR_INVALID (a length or page index in

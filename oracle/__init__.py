@@ -42,3 +42,9 @@ from .sequence import (  # noqa: F401
     masked_forward,
     masked_backward,
 )
+from .cache4 import (  # noqa: F401
+    cache4_quantise,
+    cache4_values,
+    cache4_pack,
+    cache4_unpack,
+)
