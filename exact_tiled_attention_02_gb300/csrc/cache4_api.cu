@@ -50,8 +50,8 @@ bool attn_sizes_ok(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages,
 PartLayout attn_layout(int B, int Hq, int Hkv, int Nq, int n_keys, int d) {
   return part_layout(cache4_simt_splits(B, Hq, Hkv, Nq, n_keys, d), 0, static_cast<long long>(B) * Hq * Nq, d);
 }
-// bf16 on the tensor cores: the pieces of sequences that several CTAs share
-bool tensor_cores(int d, fa_dtype dt) { return dt == FA_DTYPE_BF16 && (d == 64 || d == 96 || d == 128); }
+// on the tensor cores: the pieces of sequences that several CTAs share
+bool tensor_cores(int d) { return d == 64 || d == 96 || d == 128; }
 DecodePlan attn_plan(int B, int Hq, int Hkv, int Nq) { return cache4_plan(B, Hkv, Hq / Hkv * Nq, 152); }
 PartLayout attn_layout_tc(const DecodePlan& plan, int d) {
   return part_layout(1, 0, static_cast<long long>(decode_slots(plan)), d);
@@ -97,9 +97,8 @@ fa_status fa_cache_fp4_read(const void* cache, const int* block_table, const int
 
 size_t fa_fwd_cache_fp4_workspace_bytes(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages, int d) {
   if (!attn_sizes_ok(B, Hq, Hkv, Nq, page_size, max_pages, d)) return 0;
-  const size_t f32 = attn_layout(B, Hq, Hkv, Nq, static_cast<int>(paged_keys(page_size, max_pages)), d).bytes;
-  const size_t bf16 = tensor_cores(d, FA_DTYPE_BF16) ? attn_layout_tc(attn_plan(B, Hq, Hkv, Nq), d).bytes : 0;
-  return f32 > bf16 ? f32 : bf16;
+  if (tensor_cores(d)) return attn_layout_tc(attn_plan(B, Hq, Hkv, Nq), d).bytes;
+  return attn_layout(B, Hq, Hkv, Nq, static_cast<int>(paged_keys(page_size, max_pages)), d).bytes;
 }
 
 fa_status fa_fwd_cache_fp4(const void* q, const void* cache, const int* block_table, const int* lens, void* o,
@@ -118,7 +117,7 @@ fa_status fa_fwd_cache_fp4(const void* q, const void* cache, const int* block_ta
   Cache4 c = cache_of(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale);
   if (device_status_ptr(&c.status) != cudaSuccess) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (tensor_cores(d, dt)) {
+  if (tensor_cores(d)) {
     const DecodePlan plan = attn_plan(B, Hq, Hkv, Nq);
     SeqAttn a{};
     a.q = q;
@@ -142,8 +141,8 @@ fa_status fa_fwd_cache_fp4(const void* q, const void* cache, const int* block_ta
     a.total = static_cast<long long>(B) * Hq * Nq;
     a.status = c.status;
     a.wait_ns = device_wait_ns();
-    cudaError_t e = launch_cache4_decode(a, c, plan, s);
-    if (e == cudaSuccess) e = launch_cache4_merge(a, plan, s);
+    cudaError_t e = launch_cache4_decode(a, c, plan, dt, s);
+    if (e == cudaSuccess) e = launch_cache4_merge(a, plan, dt, s);
     return of(e);
   }
   const PartLayout w = attn_layout(B, Hq, Hkv, Nq, page_size * max_pages, d);

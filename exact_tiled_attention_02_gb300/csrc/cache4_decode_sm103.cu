@@ -15,12 +15,13 @@
 // two that brings its largest entry to 2^14 .. 2^15, exact down to 2^-31 of that;
 // P is rounded to 11 bits where bf16 would keep 8.
 //
-// W warpgroups take the tiles in turn, each with operands, scores and an O of
-// its own in tensor memory and its own running reference, so that one's
+// W teams of eight warps take the tiles in turn, each with operands, scores and
+// an O of its own in tensor memory and its own running reference, so that one's
 // products and waits overlap another's unpacking; they meet at the end of a
-// piece (a CTA's share of a sequence) only, where every warpgroup adds up some
-// columns of all O.  Per tile a warpgroup: unpacks K, starts S^T, unpacks V
-// meanwhile, takes the softmax, writes P, starts O^T.
+// piece (a CTA's share of a sequence) only, where all O are added up.  Per tile
+// a team unpacks K (two threads a key), then V while S^T is computed (two a
+// channel), takes the softmax (two a key) and writes P.  One more warp issues
+// every product, told by mbarriers, so that no team waits for its own warps.
 //
 // Statistics run down the columns, across lanes.  Per tile a thread (one key)
 // only checks whether any of its scores exceeds its column's reference by 2^8;
@@ -31,6 +32,7 @@
 // a page, into a ring of as many tiles as fit.  The work is split as
 // seq_ranges.cuh says; a sequence that is one whole piece goes straight to o.
 #include <cmath>
+#include <type_traits>
 
 #include "cache4.cuh"
 #include "seq_ranges.cuh"
@@ -42,35 +44,44 @@ using namespace seq;
 
 constexpr int BC = 128;  // keys per tile
 constexpr float kUnset = 3e38f;  // negated reference of a row that has seen no key
-constexpr float kRescaleThreshold = 8.0f;
+// A row's reference is 2^7 below the largest score when it was set, and rises
+// once a score is 2^8 above that: P is at most 2^15, and fp16's least step at
+// least 2^-32 of the largest P.
+constexpr float kBelow = 7.0f, kRescaleThreshold = kBelow + 8.0f;
 
-template <int D, int NR>
+// F32: float32 q and o.  Q is then three fp16 terms and P two, which the
+// products take one after the other: 2^-33 and 2^-22 relative.
+template <int D, int NR, bool F32>
 struct Cfg {
+  static constexpr int QT = F32 ? 3 : 1, PT = F32 ? 2 : 1;
   static constexpr int KC = D / 2;                   // columns of K in tensor memory, then 64 of V^T, S^T, O^T
-  static constexpr int COLS = KC + 64 + 2 * NR;      // of a warpgroup
-  static constexpr int W = 512 / COLS < 4 ? 512 / COLS : 4;
-  static constexpr int THREADS = W * 128 + 32;
+  static constexpr int COLS = KC + 64 + 2 * NR;      // of a team
+  static constexpr int W = 512 / COLS < 3 ? 512 / COLS : 3;
+  static constexpr int NH = NR / 2;                  // columns of a thread
+  static constexpr int THREADS = W * 256 + 64;
   static constexpr int QC = (D + 63) / 64;           // 64-channel chunks of Q
   static constexpr int RB = NR * 2;                  // bytes of a key's row of P
   static constexpr int TILE = 144 * D;               // bytes: 8 blocks of 18 D
-  static constexpr int Q_BYTES = QC * NR * 128;
-  static constexpr int P_BYTES = 128 * RB;           // a warpgroup
-  static constexpr int STATS = (2 + 3 * W) * NR * 4  // lag, column scale; reference, sum and factor of each warpgroup
+  static constexpr int Q_BYTES = QC * NR * 128;      // a term
+  static constexpr int P_BYTES = 128 * RB;           // a term of a team
+  static constexpr int VS_BYTES = W * 8 * 256;       // a warp's value scales in fp16: [2 groups][64 tokens]
+  static constexpr int STATS = (2 + 3 * W) * NR * 4  // lag, column scale; reference, sum and factor of each team
                                + W * 4 * NR * 4;     // warps' column results
-  static constexpr int MISC = STATS + 512;
-  static constexpr int SLOTS_FIT = (227 * 1024 - 1024 - Q_BYTES - W * P_BYTES - MISC) / TILE;
+  static constexpr int MISC = VS_BYTES + STATS + 512;
+  static constexpr int SLOTS_FIT = (227 * 1024 - 1024 - QT * Q_BYTES - W * PT * P_BYTES - MISC) / TILE;
   static constexpr int SLOTS = SLOTS_FIT < 12 ? SLOTS_FIT : 12;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_P = OFF_Q + Q_BYTES;
-  static constexpr int OFF_RING = OFF_P + W * P_BYTES;
-  static constexpr int OFF_STAT = OFF_RING + SLOTS * TILE;
+  static constexpr int OFF_P = OFF_Q + QT * Q_BYTES;
+  static constexpr int OFF_RING = OFF_P + W * PT * P_BYTES;
+  static constexpr int OFF_VS = OFF_RING + SLOTS * TILE;
+  static constexpr int OFF_STAT = OFF_VS + VS_BYTES;
   static constexpr int OFF_BAR = OFF_STAT + STATS;
-  static constexpr int NBAR = 2 * SLOTS + 3 * W;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory base, abort flag, start, then the slots' missing blocks
-  static constexpr int SMEM_USED = OFF_MISC + 24 + SLOTS * 4;
+  static constexpr int NBAR = 2 * SLOTS + 4 * W + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory base, abort flag, start; teams' first-tile flags; slots' missing blocks
+  static constexpr int SMEM_USED = OFF_MISC + 24 + W * 4 + SLOTS * 4;
   static constexpr int SMEM_BYTES = SMEM_USED + 1024;
   static constexpr int TM_K = 0, TM_V = KC, TM_S = KC + 64, TM_O = TM_S + NR;
-  static_assert(W >= 2 && SLOTS >= 2 * W, "two tiles a warpgroup in flight");
+  static_assert(W >= 2 && SLOTS >= 2 * W, "two tiles a team in flight");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
   static_assert(OFF_P % 1024 == 0 && P_BYTES % 1024 == 0 && OFF_RING % 1024 == 0 && TILE % 16 == 0, "alignment");
 };
@@ -123,10 +134,27 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+// N consecutive bytes (2, 3 or 4), the first in the lowest; 2 and 4 are aligned to their size.
+template <int N>
+__device__ __forceinline__ uint32_t ld_shared_bytes(uint32_t addr) {
+  uint32_t v;
+  if constexpr (N == 4) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile("{\n.reg .u16 t;\nld.shared.u16 t, [%1];\ncvt.u32.u16 %0, t;\n}" : "=r"(v) : "r"(addr) : "memory");
+  } else {
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      uint32_t x;
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr + i) : "memory");
+      v |= x << (8 * i);
+    }
+  }
   return v;
+}
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
@@ -134,13 +162,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-template <int D, int NR>
-__global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
+template <int D, int NR, bool F32>
+__global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
     fa_cache4_decode_kernel(const __grid_constant__ SeqAttn p, const __grid_constant__ Cache4 cache,
                             const DecodePlan plan) {
-  using C = Cfg<D, NR>;
-  constexpr int W = C::W, SLOTS = C::SLOTS, GROUPS = D / 16;
-  constexpr int kConsumers = W * 128;
+  using C = Cfg<D, NR, F32>;
+  using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+  constexpr int W = C::W, SLOTS = C::SLOTS, GROUPS = D / 16, NH = C::NH;
+  constexpr int kConsumers = W * 256;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
@@ -161,13 +190,16 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
   const uint32_t bars = sb + C::OFF_BAR;
   auto full = [&](int s) { return bars + 8 * s; };
   auto free_ = [&](int s) { return bars + 8 * (SLOTS + s); };
-  auto s_done = [&](int w) { return bars + 8 * (2 * SLOTS + w); };
-  auto o_done = [&](int w) { return bars + 8 * (2 * SLOTS + W + w); };
-  auto drain_bar = [&](int w) { return bars + 8 * (2 * SLOTS + 2 * W + w); };
+  auto k_ready = [&](int w) { return bars + 8 * (2 * SLOTS + w); };
+  auto s_done = [&](int w) { return bars + 8 * (2 * SLOTS + W + w); };
+  auto p_ready = [&](int w) { return bars + 8 * (2 * SLOTS + 2 * W + w); };
+  auto o_done = [&](int w) { return bars + 8 * (2 * SLOTS + 3 * W + w); };
+  const uint32_t drain_bar = bars + 8 * (2 * SLOTS + 4 * W);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* s_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // first sequence, its first tile, tiles of this CTA
-  volatile int* s_missing = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 24);  // [SLOTS] blocks without a page
+  volatile int* s_first = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 24);  // [W] a team's tile is its first of a piece
+  volatile int* s_missing = s_first + W;                                             // [SLOTS] blocks without a page
   const WaitCtl wc{p.status, abort_flag, p.wait_ns};
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
@@ -179,22 +211,24 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(free_(s), 4);
+      mbar_init(free_(s), 8);
     }
     for (int w = 0; w < W; ++w) {
+      mbar_init(k_ready(w), 8);
       mbar_init(s_done(w), 1);
+      mbar_init(p_ready(w), 8);
       mbar_init(o_done(w), 1);
-      mbar_init(drain_bar(w), 1);
     }
+    mbar_init(drain_bar, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
     fence_proxy_async_smem();
   }
-  if (warp == 4 * W) {
+  if (warp == 8 * W) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp == 4 * W - 1) {
+  if (warp == 8 * W + 1) {
     int b0, first, count;
     find_range<BC>(p, plan, cut, b0, first, count);
     if (lane == 0) {
@@ -232,7 +266,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
     }
   };
 
-  if (warp == 4 * W) {
+  if (warp == 8 * W + 1) {
     // ---------------------------------------------------------------- loads
     // Lane i (of 8) looks block i of a tile up; the first lane of every run of
     // blocks that lie side by side in a page copies the run.
@@ -240,7 +274,7 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
     const int per_page = cache.page_size / 16;
     pieces([&](int b, int nk, int t0, int n, int) -> bool {
       const int blocks = (nk + 15) / 16;
-      // this lane's block of a tile: its page as the table has it (-1: past the end), its place there
+      // this lane's block of a tile: its page as the table has it (-1: past the end, -2: no such page), its place there
       auto place = [&](int tile, int& page, int& at) {
         const int i = tile * 8 + lane;
         page = at = -1;
@@ -287,60 +321,128 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
       for (int k = max(0, g - SLOTS); k < g; ++k) mbar_wait(full(k % SLOTS), (k / SLOTS) & 1, drain);
     }
     __syncwarp();
+  } else if (warp == 8 * W) {
+    // ------------------------------------------------------------- products
+    // The whole warp runs it, converged (see mma_ts_w): S^T of a team's tile
+    // once its K is in place, O^T once its V^T and P are, whichever is ready.
+    constexpr uint32_t idesc_s = idesc_f16(128, NR, 0), idesc_o = idesc_f16(128, NR, 1);
+    const Desc2 dq = desc_sw128(sQ, 16, 1024), dp = desc_p<C::RB>(sb + C::OFF_P);
+    int left = 2 * n_tiles;
+    uint32_t s_par = 0, o_par = 0;  // a bit a team: the phase it waits for next
+    unsigned long long since = 0;
+    while (left > 0) {
+      bool moved = false;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const uint32_t tw = tmem + w * C::COLS;
+        if (warp_test(k_ready(w), (s_par >> w) & 1)) {
+          tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < C::QT; ++t)
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_ts_w(tw + C::TM_S, tw + C::TM_K + 8 * kk, dq,
+                       (t * C::Q_BYTES + (kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, t > 0 || kk > 0);
+          mma_commit_w(s_done(w));
+          s_par ^= 1u << w;
+          moved = true;
+          --left;
+        }
+        if (warp_test(p_ready(w), (o_par >> w) & 1)) {
+          tc_fence_after();
+          const uint32_t more = s_first[w] == 0;
+#pragma unroll
+          for (int t = 0; t < C::PT; ++t)
+#pragma unroll
+            for (int kk = 0; kk < BC / 16; ++kk)
+              mma_ts_w(tw + C::TM_O, tw + C::TM_V + 8 * kk, dp,
+                       ((w * C::PT + t) * C::P_BYTES + kk * 16 * C::RB) >> 4, idesc_o, t > 0 || kk > 0 ? 1u : more);
+          mma_commit_w(o_done(w));
+          o_par ^= 1u << w;
+          moved = true;
+          --left;
+        }
+      }
+      if (moved) {
+        since = 0;
+      } else if (since == 0) {
+        since = globaltimer_ns();
+      } else {
+        // no team has moved: the wait is bounded like every other
+        const bool late = __any_sync(0xffffffffu, globaltimer_ns() - since > wc.limit_ns);
+        if (late) record_timeout(wc);
+        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) break;
+      }
+    }
+    // every product must finish before tensor memory is freed
+    mma_commit_w(drain_bar);
+    WaitCtl drain{nullptr, nullptr, wc.limit_ns};
+    mbar_wait(drain_bar, 0, drain);
+    __syncwarp();
   } else {
-    // -------------------------------------------------- unpacking, products, softmax
+    // ----------------------------------------------------- unpacking, softmax
     // Once a wait has run out, waits return at once and the loops run on to
     // their ends (barriers count every warp); nothing is written out then.
-    const int w = warp >> 2, quarter = warp & 3, id = threadIdx.x & 127;  // id: a key, then a channel
-    const uint32_t tw = tmem + w * C::COLS;                               // this warpgroup's columns
-    const uint32_t tl = tw + (static_cast<uint32_t>(quarter * 32) << 16);  // and this warp's lanes
-    const uint32_t sP = sb + C::OFF_P + w * C::P_BYTES;
-    const Desc2 dq = desc_sw128(sQ, 16, 1024), dp = desc_p<C::RB>(sP);
-    constexpr uint32_t idesc_s = idesc_f16(128, NR, 0), idesc_o = idesc_f16(128, NR, 1);
+    const int w = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
+    const int id = threadIdx.x & 127;                                      // a key, then a channel
+    const uint32_t tl = tmem + w * C::COLS + (static_cast<uint32_t>(quarter * 32) << 16);  // this team's columns, this warp's lanes
+    const uint32_t sP = sb + C::OFF_P + w * C::PT * C::P_BYTES;
+    const uint32_t sVS = sb + C::OFF_VS + warp * 256;
+    const int c0 = half * NH;  // this thread's columns: c0 .. c0 + NH - 1
     float* ref = s_ref + w * NR;
     float* fac = s_fac + w * NR;
     float* red = s_red + w * 4 * NR;
-    constexpr int RCOLS = NR > 32 ? NR / 32 : 1;  // columns that a lane owns after a reduction
-    const int my_col = first_col<NR>();
-    auto put = [&](float* dst, const float* v) {  // this warp's column results
-#pragma unroll
-      for (int i = 0; i < RCOLS; ++i) dst[quarter * NR + my_col + i] = v[i];
-    };
-    auto wg_sync = [&]() { named_bar_sync(1 + w, 128); };
+    constexpr int RCOLS = NH > 32 ? NH / 32 : 1;  // columns that a lane owns after a reduction
+    const int my_col = c0 + first_col<NH>();
+    const int tid = threadIdx.x & 255;  // within the team
+    auto team_sync = [&]() { named_bar_sync(1 + w, 256); };
     auto all_sync = [&]() { named_bar_sync(8, kConsumers); };
-    int g = 0, mine = 0;  // tiles of the CTA so far, and of this warpgroup
+    int g = 0, mine = 0;  // tiles of the CTA so far, and of this team
 
-    // Q rows of a sequence: a warp takes rows warp, warp + 4 W, ...; a lane 4 channels of one
-    constexpr int QR = (NR + 4 * W - 1) / (4 * W);
-    uint2 qv[QR];
+    // Q rows of a sequence: a warp takes rows warp, warp + 8 W, ...; a lane 4 channels of one
+    constexpr int QR = (NR + 8 * W - 1) / (8 * W);
+    using Four = typename std::conditional<F32, uint4, uint2>::type;
+    Four qv[QR];
     auto load_q = [&](int b) {
       const long long row0 = (b * plan.heads + head) / p.group_div * p.q_s1 + (b * plan.heads + head) % p.group_div * p.q_s2 + r0;
 #pragma unroll
       for (int i = 0; i < QR; ++i) {
-        const int r = warp + 4 * W * i;
-        qv[i] = make_uint2(0, 0);
+        const int r = warp + 8 * W * i;
+        qv[i] = Four{};
         if (r < n_rows && 4 * lane < D)
-          qv[i] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q) + (row0 + r) * D + 4 * lane);
+          qv[i] = *reinterpret_cast<const Four*>(static_cast<const T*>(p.q) + (row0 + r) * D + 4 * lane);
       }
     };
     auto put_q = [&]() {
 #pragma unroll
       for (int i = 0; i < QR; ++i) {
-        const int r = warp + 4 * W * i;
+        const int r = warp + 8 * W * i;
         if (r >= NR) break;
-        const uint32_t m2 = __vmaxu2(qv[i].x & 0x7fff7fffu, qv[i].y & 0x7fff7fffu);
-        const uint32_t amax = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+        float x[4];
+        if constexpr (F32) {
+          x[0] = __uint_as_float(qv[i].x), x[1] = __uint_as_float(qv[i].y);
+          x[2] = __uint_as_float(qv[i].z), x[3] = __uint_as_float(qv[i].w);
+        } else {
+          x[0] = __uint_as_float(qv[i].x << 16), x[1] = __uint_as_float(qv[i].x & 0xffff0000u);
+          x[2] = __uint_as_float(qv[i].y << 16), x[3] = __uint_as_float(qv[i].y & 0xffff0000u);
+        }
+        const uint32_t amax = __reduce_max_sync(
+            0xffffffffu, __float_as_uint(fmaxf(fmax3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]))));
         // the power of two that brings the row's largest entry to 2^14 .. 2^15 (its
         // exponent field is e; rows below 2^-112 are brought as far as fp32 reaches)
-        const int e = amax >> 7;
+        const int e = amax >> 23;
         const int up = amax == 0 ? 0 : min(141 - e, 126);
         const float f = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-        const uint32_t lo = pack_f16x2(__uint_as_float(qv[i].x << 16) * f, __uint_as_float(qv[i].x & 0xffff0000u) * f);
-        const uint32_t hi = pack_f16x2(__uint_as_float(qv[i].y << 16) * f, __uint_as_float(qv[i].y & 0xffff0000u) * f);
-        if (4 * lane < D) {
-          const int ch = 4 * lane, c16 = (ch & 63) >> 3;
-          const uint32_t at = sQ + (ch >> 6) * NR * 128 + r * 128 + ((c16 ^ (r & 7)) << 4) + (ch & 4) * 2;
-          asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(lo), "r"(hi) : "memory");
+#pragma unroll
+        for (int y = 0; y < 4; ++y) x[y] *= f;
+        const int ch = 4 * lane, c16 = (ch & 63) >> 3;
+        const uint32_t at = sQ + (ch >> 6) * NR * 128 + r * 128 + ((c16 ^ (r & 7)) << 4) + (ch & 4) * 2;
+#pragma unroll
+        for (int t = 0; t < C::QT; ++t) {
+          const uint32_t lo = pack_f16x2(x[0], x[1]), hi = pack_f16x2(x[2], x[3]);
+          if (ch < D) st_shared_v2(at + t * C::Q_BYTES, lo, hi);
+          const float2 a = cache4::floats(lo), b = cache4::floats(hi);
+          x[0] -= a.x, x[1] -= a.y, x[2] -= b.x, x[3] -= b.y;
         }
         if (lane == 0)
           s_cs[r] = fmaxf(p.scale * cache.k_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - up) << 23),
@@ -359,11 +461,11 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
         all_sync();
       }
       if (next >= 0) load_q(next);  // lands while this piece goes on
-      float l[NR];
+      float l[NH];
 #pragma unroll
-      for (int c = 0; c < NR; ++c) l[c] = 0.f;
-      if (id < NR) ref[id] = kUnset;
-      bool any = false;  // this warpgroup has had a tile of the piece
+      for (int c = 0; c < NH; ++c) l[c] = 0.f;
+      if (tid < NR) ref[tid] = kUnset;
+      bool any = false;  // this team has had a tile of the piece
       for (int i = 0; i < n; ++i, ++g) {
         if (g % W != w) continue;
         const int slot = g % SLOTS;
@@ -371,181 +473,200 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
         const uint32_t base = sRing + slot * C::TILE;
         const int missing = s_missing[slot];
         const int j0 = (t0 + i) * BC, valid = min(BC, nk - j0);
-        // ---- K: a thread a key
+        // ---- K: a thread half the channels of a key
         {
-          const uint32_t blk = base + (id >> 4) * (18 * D), t = id & 15;
-          const bool gone = (missing >> (id >> 4)) & 1;  // no page: zeros
+          constexpr int GH = GROUPS / 2;
+          const uint32_t t = id & 15, blk = base + (id >> 4) * (18 * D) + half * GH * 128 + t * 8;
+          uint32_t sc[2];
+          uint32_t s4 = ld_shared_bytes<GH>(base + (id >> 4) * (18 * D) + 8 * D + t * GROUPS + half * GH);
+          if ((missing >> (id >> 4)) & 1) s4 = 0;  // no page: zeros
+          cache4::scales_f16(s4, sc);
+          const uint32_t to = tl + C::TM_K + half * GH * 8;
+          uint32_t o[16];
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            const uint2 a = ld_shared_v2(blk + (2 * c) * 128 + t * 8), e = ld_shared_v2(blk + (2 * c + 1) * 128 + t * 8);
-            uint32_t sc[2];
-            cache4::scales_f16(gone ? 0u : ld_shared_u16(blk + 8 * D + t * GROUPS + 2 * c), sc);
-            const uint32_t s0 = __byte_perm(sc[0], 0, 0x1010), s1 = __byte_perm(sc[0], 0, 0x3232);
-            uint32_t o[16];
-            cache4::codes_f16(a.x, o);
-            cache4::codes_f16(a.y, o + 4);
-            cache4::codes_f16(e.x, o + 8);
-            cache4::codes_f16(e.y, o + 12);
+          for (int c = 0; c < GH; ++c) {
+            const uint2 a = ld_shared_v2(blk + c * 128);
+            const uint32_t s2 = __byte_perm(sc[c >> 1], 0, c & 1 ? 0x3232 : 0x1010);
+            uint32_t* x = o + 8 * (c & 1);
+            cache4::codes_f16(a.x, x);
+            cache4::codes_f16(a.y, x + 4);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              o[x] = cache4::mul_f16x2(o[x], s0);
-              o[8 + x] = cache4::mul_f16x2(o[8 + x], s1);
-            }
-            tmem_st_32x32b_x16(tl + C::TM_K + 16 * c, o);
+            for (int y = 0; y < 8; ++y) x[y] = cache4::mul_f16x2(x[y], s2);
+            if (c & 1)
+              tmem_st_32x32b_x16(to + 8 * (c - 1), o);
+            else if (c == GH - 1)
+              tmem_st_32x32b_x8(to + 8 * c, o);
           }
         }
         tmem_wait_st();
         tc_fence_before();
-        wg_sync();
-        if (quarter == 0) {
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ts_w(tw + C::TM_S, tw + C::TM_K + 8 * kk, dq, ((kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, kk > 0);
-          mma_commit_w(s_done(w));
-        }
-        // ---- V: a thread a channel.  The last product of this warpgroup has read V^T and P.
-        if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);
-        tc_fence_after();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_ready(w));
+        // ---- V: a thread half the keys of a channel
         if (quarter * 32 < D) {
-          const uint32_t cb = base + 9 * D + id * 8, cs = base + 17 * D + (id >> 4) * 16;
-          const int part = valid < BC || missing != 0 ? 0 : BC;  // below: some tokens are to be zeros
+          // the scales of the warp's two groups and 64 keys, zeros past the sequence's end and in missing pages
+          {
+            const int k = half * 4 + ((lane >> 2) & 3), t = (lane & 3) * 4;  // block, first of four keys
+            uint32_t sc[2];
+            cache4::scales_f16(ld_shared_bytes<4>(base + k * 18 * D + 17 * D + (2 * quarter + (lane >> 4)) * 16 + t), sc);
+            if (valid < BC || missing != 0) {
+              const int room = (missing >> k) & 1 ? 0 : valid - 16 * k - t;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
+              for (int y = 0; y < 2; ++y)
+                sc[y] &= (2 * y < room ? 0xffffu : 0u) | (2 * y + 1 < room ? 0xffff0000u : 0u);
+            }
+            st_shared_v2(sVS + lane * 8, sc[0], sc[1]);
+          }
+          __syncwarp();
+          // the last product of this team has read V^T and P
+          if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);
+          tc_fence_after();
+          const uint32_t cb = base + half * 4 * 18 * D + 9 * D + id * 8, cs = sVS + (lane >> 4) * 128;
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
             uint32_t o[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int k = 2 * x + h;
               const uint2 a = ld_shared_v2(cb + k * 18 * D);
-              const uint4 s4 = ld_shared_v4(cs + k * 18 * D);
-              uint32_t sc[8];
-              cache4::scales_f16(s4.x, sc);
-              cache4::scales_f16(s4.y, sc + 2);
-              cache4::scales_f16(s4.z, sc + 4);
-              cache4::scales_f16(s4.w, sc + 6);
-              if (part == 0) {
-                const int room = (missing >> k) & 1 ? 0 : valid - 16 * k;
-#pragma unroll
-                for (int y = 0; y < 8; ++y)
-                  sc[y] &= (2 * y < room ? 0xffffu : 0u) | (2 * y + 1 < room ? 0xffff0000u : 0u);
-              }
-              cache4::codes_f16(a.x, o + 8 * h);
-              cache4::codes_f16(a.y, o + 8 * h + 4);
-#pragma unroll
-              for (int y = 0; y < 8; ++y) o[8 * h + y] = cache4::mul_f16x2(o[8 * h + y], sc[y]);
+              const uint4 sa = ld_shared_v4(cs + k * 32), se = ld_shared_v4(cs + k * 32 + 16);
+              uint32_t* y = o + 8 * h;
+              cache4::codes_f16(a.x, y);
+              cache4::codes_f16(a.y, y + 4);
+              y[0] = cache4::mul_f16x2(y[0], sa.x);
+              y[1] = cache4::mul_f16x2(y[1], sa.y);
+              y[2] = cache4::mul_f16x2(y[2], sa.z);
+              y[3] = cache4::mul_f16x2(y[3], sa.w);
+              y[4] = cache4::mul_f16x2(y[4], se.x);
+              y[5] = cache4::mul_f16x2(y[5], se.y);
+              y[6] = cache4::mul_f16x2(y[6], se.z);
+              y[7] = cache4::mul_f16x2(y[7], se.w);
             }
-            tmem_st_32x32b_x16(tl + C::TM_V + 16 * x, o);
+            tmem_st_32x32b_x16(tl + C::TM_V + half * 32 + 16 * x, o);
           }
+        } else if (mine > 0) {
+          warp_wait(o_done(w), (mine - 1) & 1, wc);
+          tc_fence_after();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(free_(slot));
         // ---- scores
         warp_wait(s_done(w), mine & 1, wc);
         tc_fence_after();
-        float s[NR];
-#pragma unroll
-        for (int c = 0; c < NR; c += 16) {
-          uint32_t r[16];
-          tmem_ld_32x32b_x16(tl + C::TM_S + c, r);
+        float s[NH];
+        {
+          uint32_t r[NH];
+          tmem_ld<NH>(tl + C::TM_S + c0, r);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) s[c + x] = __uint_as_float(r[x]);
+          for (int x = 0; x < NH; ++x) s[x] = __uint_as_float(r[x]);
         }
         if (j0 + BC > nk - (p.n_new - 1)) {
           const int room = nk - (j0 + id);  // > lag: the row sees this key
 #pragma unroll
-          for (int c = 0; c < NR; ++c) s[c] = s_lag[c] < room ? s[c] : -INFINITY;
+          for (int c = 0; c < NH; ++c) s[c] = s_lag[c0 + c] < room ? s[c] : -INFINITY;
         }
         float over = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < NR; c += 4) {
-          const float4 nr = *reinterpret_cast<const float4*>(ref + c), cs = *reinterpret_cast<const float4*>(s_cs + c);
+        for (int c = 0; c < NH; c += 4) {
+          const float4 nr = *reinterpret_cast<const float4*>(ref + c0 + c);
+          const float4 cs = *reinterpret_cast<const float4*>(s_cs + c0 + c);
           over = fmax3(over, fmaf(s[c], cs.x, nr.x), fmaf(s[c + 1], cs.y, nr.y));
           over = fmax3(over, fmaf(s[c + 2], cs.z, nr.z), fmaf(s[c + 3], cs.w, nr.w));
         }
-        if (bar_any(1 + w, 128, over > kRescaleThreshold)) {
+        if (bar_any(1 + w, 256, over > kRescaleThreshold)) {
           // some row's reference rises: column maxima over the 128 keys
           {
-            float v[NR];
+            float v[NH];
 #pragma unroll
-            for (int c = 0; c < NR; ++c) v[c] = s[c] * s_cs[c];
-            reduce_step<NR / 2, 16>(v, [](float x, float y) { return fmaxf(x, y); });
-            put(red, v);
+            for (int c = 0; c < NH; ++c) v[c] = s[c] * s_cs[c0 + c];
+            reduce_step<NH / 2, 16>(v, [](float x, float y) { return fmaxf(x, y); });
+#pragma unroll
+            for (int x = 0; x < RCOLS; ++x) red[quarter * NR + my_col + x] = v[x];
           }
-          wg_sync();
-          if (id < NR) {
-            const float mx = fmaxf(fmaxf(red[id], red[NR + id]), fmaxf(red[2 * NR + id], red[3 * NR + id]));
-            const float old = ref[id];
+          team_sync();
+          if (tid < NR) {
+            const float mx = fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid]));
+            const float old = ref[tid];
             float alpha = 1.f;
             if (mx + old > kRescaleThreshold) {  // old = kUnset: the first key that the row sees
-              alpha = old == kUnset ? 0.f : ex2_approx(-old - mx);
-              ref[id] = -mx;
+              alpha = old == kUnset ? 0.f : ex2_approx(kBelow - old - mx);
+              ref[tid] = kBelow - mx;
             }
-            fac[id] = alpha;
+            fac[tid] = alpha;
           }
-          wg_sync();
+          team_sync();
 #pragma unroll
-          for (int c = 0; c < NR; ++c) l[c] *= fac[c];
+          for (int c = 0; c < NH; ++c) l[c] *= fac[c0 + c];
           if (any) {
 #pragma unroll 1
-            for (int c = 0; c < NR; c += 16) {
-              uint32_t o[16];
-              tmem_ld_32x32b_x16(tl + C::TM_O + c, o);
+            for (int c = c0; c < c0 + NH; c += 8) {
+              uint32_t o[8];
+              tmem_ld_32x32b_x8(tl + C::TM_O + c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fac[c + x]);
-              tmem_st_32x32b_x16(tl + C::TM_O + c, o);
+              for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fac[c + x]);
+              tmem_st_32x32b_x8(tl + C::TM_O + c, o);
             }
           }
         }
         // ---- P
 #pragma unroll
-        for (int c = 0; c < NR; c += 8) {
-          uint32_t pk[4];
+        for (int c = 0; c < NH; c += 8) {
+          float x[8];
 #pragma unroll
-          for (int x = 0; x < 8; x += 4) {
-            const float4 nr = *reinterpret_cast<const float4*>(ref + c + x);
-            const float4 cs = *reinterpret_cast<const float4*>(s_cs + c + x);
-            const float p0 = ex2_approx(fmaf(s[c + x], cs.x, nr.x)), p1 = ex2_approx(fmaf(s[c + x + 1], cs.y, nr.y));
-            const float p2 = ex2_approx(fmaf(s[c + x + 2], cs.z, nr.z)), p3 = ex2_approx(fmaf(s[c + x + 3], cs.w, nr.w));
-            l[c + x] += p0;
-            l[c + x + 1] += p1;
-            l[c + x + 2] += p2;
-            l[c + x + 3] += p3;
-            // P is rounded to fp16, the products' type: half a step of 2^-11 each
-            pk[x / 2] = pack_f16x2(p0, p1);
-            pk[x / 2 + 1] = pack_f16x2(p2, p3);
+          for (int y = 0; y < 8; y += 4) {
+            const float4 nr = *reinterpret_cast<const float4*>(ref + c0 + c + y);
+            const float4 cs = *reinterpret_cast<const float4*>(s_cs + c0 + c + y);
+            x[y] = ex2_approx(fmaf(s[c + y], cs.x, nr.x));
+            x[y + 1] = ex2_approx(fmaf(s[c + y + 1], cs.y, nr.y));
+            x[y + 2] = ex2_approx(fmaf(s[c + y + 2], cs.z, nr.z));
+            x[y + 3] = ex2_approx(fmaf(s[c + y + 3], cs.w, nr.w));
           }
-          st_shared_v4(sP + id * C::RB + p_chunk<C::RB>(id, c / 8) * 16, pk[0], pk[1], pk[2], pk[3]);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) l[c + y] += x[y];
+          // P is rounded to fp16, the products' type: half a step of 2^-11 each
+          // (of a second term too, where there is one: 2^-22)
+          const uint32_t at = sP + id * C::RB + p_chunk<C::RB>(id, (c0 + c) / 8) * 16;
+#pragma unroll
+          for (int t = 0; t < C::PT; ++t) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              pk[y] = pack_f16x2(x[2 * y], x[2 * y + 1]);
+              if (t + 1 < C::PT) {
+                const float2 h = cache4::floats(pk[y]);
+                x[2 * y] -= h.x;
+                x[2 * y + 1] -= h.y;
+              }
+            }
+            st_shared_v4(at + t * C::P_BYTES, pk[0], pk[1], pk[2], pk[3]);
+          }
         }
+        if (tid == 0) s_first[w] = !any;
         fence_proxy_async_smem();
         tmem_wait_st();
         tc_fence_before();
-        wg_sync();
-        if (quarter == 0) {
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < BC / 16; ++kk)
-            mma_ts_w(tw + C::TM_O, tw + C::TM_V + 8 * kk, dp, (kk * 16 * C::RB) >> 4, idesc_o, any || kk > 0);
-          mma_commit_w(o_done(w));
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready(w));
         any = true;
         ++mine;
       }
       // ------------------------------------------------------------ output
       if (any) warp_wait(o_done(w), (mine - 1) & 1, wc);
       tc_fence_after();
-      reduce_step<NR / 2, 16>(l, [](float x, float y) { return x + y; });
-      put(red, l);
-      wg_sync();
-      if (id < NR) s_sum[w * NR + id] = (red[id] + red[NR + id]) + (red[2 * NR + id] + red[3 * NR + id]);
+      reduce_step<NH / 2, 16>(l, [](float x, float y) { return x + y; });
+#pragma unroll
+      for (int x = 0; x < RCOLS; ++x) red[quarter * NR + my_col + x] = l[x];
+      team_sync();
+      if (tid < NR) s_sum[w * NR + tid] = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
       tc_fence_before();
       all_sync();
       tc_fence_after();
       const bool whole = t0 == 0 && n == tiles_of<BC>(nk);
       const long long slot = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + cut + b;
       const long long orow0 = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r0;
-      if (threadIdx.x < NR) {  // the warpgroups' O share one reference: the largest
+      if (threadIdx.x < NR) {  // the teams' O share one reference: the largest
         const int c = threadIdx.x;
         float m = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -571,14 +692,14 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
       if (next >= 0) put_q();  // every product with this piece's Q has completed
       all_sync();
 #pragma unroll 1
-      for (int c = 8 * w; c < n_rows; c += 8 * W) {
+      for (int c = 8 * (warp >> 2); c < n_rows; c += 16 * W) {
         float acc[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) acc[x] = 0.f;
 #pragma unroll
         for (int y = 0; y < W; ++y) {
           __syncwarp();
-          if (n < W && (g - 1 - y + W * (n + W)) % W >= n) continue;  // warpgroup y had no tile
+          if (n < W && (g - 1 - y + W * (n + W)) % W >= n) continue;  // team y had no tile
           uint32_t o[8];
           tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + y * C::COLS + C::TM_O + c, o);
           tmem_wait_ld();
@@ -592,46 +713,49 @@ __global__ void __launch_bounds__(Cfg<D, NR>::THREADS, 1)
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           if (c + x >= n_rows) break;
-          if (whole)
-            static_cast<__nv_bfloat16*>(p.o)[(orow0 + c + x) * D + id] = __float2bfloat16_rn(acc[x]);
-          else
+          if (!whole)
             p.part_o[(slot * NR + c + x) * D + id] = acc[x];
+          else if constexpr (F32)
+            static_cast<float*>(p.o)[(orow0 + c + x) * D + id] = acc[x];
+          else
+            static_cast<__nv_bfloat16*>(p.o)[(orow0 + c + x) * D + id] = __float2bfloat16_rn(acc[x]);
         }
       }
       tc_fence_before();
       all_sync();  // statistics and accumulators are free for the next piece
       return true;
     });
-    // every product this warp issued must finish before tensor memory is freed
-    if (quarter == 0) {
-      mma_commit_w(drain_bar(w));
-      WaitCtl drain{nullptr, nullptr, wc.limit_ns};
-      mbar_wait(drain_bar(w), 0, drain);
-    }
-    __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 4 * W) {
+  if (warp == 8 * W) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-template <int D, int NR>
+template <int D, int NR, bool F32>
 cudaError_t launch_nr(const SeqAttn& p, const Cache4& c, const DecodePlan& plan, cudaStream_t s) {
-  using C = Cfg<D, NR>;
+  using C = Cfg<D, NR, F32>;
   static SmemOnce once;
-  const cudaError_t e = once(fa_cache4_decode_kernel<D, NR>, C::SMEM_BYTES);
+  const cudaError_t e = once(fa_cache4_decode_kernel<D, NR, F32>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(plan.heads) * plan.row_groups * plan.cuts;
-  fa_cache4_decode_kernel<D, NR><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(p, c, plan);
+  fa_cache4_decode_kernel<D, NR, F32><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(p, c, plan);
   return cudaGetLastError();
 }
-template <int D>
+template <int D, bool F32>
 cudaError_t launch_d(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s) {
-  return w.nr == 16 ? launch_nr<D, 16>(p, c, w, s) : w.nr == 32 ? launch_nr<D, 32>(p, c, w, s) : launch_nr<D, 64>(p, c, w, s);
+  if (w.nr == 16) return launch_nr<D, 16, F32>(p, c, w, s);
+  return w.nr == 32 ? launch_nr<D, 32, F32>(p, c, w, s) : launch_nr<D, 64, F32>(p, c, w, s);
+}
+template <bool F32>
+cudaError_t launch_type(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s) {
+  if (c.d == 64) return launch_d<64, F32>(p, c, w, s);
+  if (c.d == 96) return launch_d<96, F32>(p, c, w, s);
+  if (c.d == 128) return launch_d<128, F32>(p, c, w, s);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -648,21 +772,22 @@ DecodePlan cache4_plan(int n_seq, int heads, int rows, int sms) {
   return w;
 }
 
-cudaError_t launch_cache4_decode(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s) {
+cudaError_t launch_cache4_decode(const SeqAttn& p, const Cache4& c, const DecodePlan& w, fa_dtype dt, cudaStream_t s) {
   if (static_cast<long long>(w.heads) * w.row_groups * w.cuts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   // tile counts are summed, and multiplied by the number of cuts, in 32 bits
   if (static_cast<long long>(w.n_seq) * tiles_of<BC>(p.n_keys) * (w.cuts + 1LL) > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;
-  if (c.d == 64) return launch_d<64>(p, c, w, s);
-  if (c.d == 96) return launch_d<96>(p, c, w, s);
-  if (c.d == 128) return launch_d<128>(p, c, w, s);
-  return cudaErrorInvalidValue;
+  return dt == FA_DTYPE_F32 ? launch_type<true>(p, c, w, s) : launch_type<false>(p, c, w, s);
 }
 
-cudaError_t launch_cache4_merge(const SeqAttn& p, const DecodePlan& w, cudaStream_t s) {
-  if (w.nr == 16) return launch_merge<BC, 16>(p, w, nullptr, nullptr, 0, true, s);
-  if (w.nr == 32) return launch_merge<BC, 32>(p, w, nullptr, nullptr, 0, true, s);
-  return launch_merge<BC, 64>(p, w, nullptr, nullptr, 0, true, s);
+template <typename T>
+static cudaError_t merge_of(const SeqAttn& p, const DecodePlan& w, cudaStream_t s) {
+  if (w.nr == 16) return launch_merge<BC, 16, T>(p, w, nullptr, nullptr, 0, true, s);
+  if (w.nr == 32) return launch_merge<BC, 32, T>(p, w, nullptr, nullptr, 0, true, s);
+  return launch_merge<BC, 64, T>(p, w, nullptr, nullptr, 0, true, s);
+}
+cudaError_t launch_cache4_merge(const SeqAttn& p, const DecodePlan& w, fa_dtype dt, cudaStream_t s) {
+  return dt == FA_DTYPE_F32 ? merge_of<float>(p, w, s) : merge_of<__nv_bfloat16>(p, w, s);
 }
 
 }  // namespace fa

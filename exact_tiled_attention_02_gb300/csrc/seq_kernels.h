@@ -130,11 +130,11 @@ struct Cache4Attn {
 cudaError_t launch_cache4_simt(const Cache4Attn& p, fa_dtype dt, cudaStream_t s);
 int cache4_simt_splits(int B, int Hq, int Hkv, int n_new, int n_keys, int d);
 
-// bf16 on the tensor cores, d = 64, 96 or 128 (cache4_decode_sm103.cu).  p: as for
+// On the tensor cores, d = 64, 96 or 128 (cache4_decode_sm103.cu).  p: as for
 // launch_seq_decode, groups (sequence, key/value head), page fields and k1, v unused.
 DecodePlan cache4_plan(int n_seq, int heads, int rows, int sms);
-cudaError_t launch_cache4_decode(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s);
-cudaError_t launch_cache4_merge(const SeqAttn& p, const DecodePlan& w, cudaStream_t s);
+cudaError_t launch_cache4_decode(const SeqAttn& p, const Cache4& c, const DecodePlan& w, fa_dtype dt, cudaStream_t s);
+cudaError_t launch_cache4_merge(const SeqAttn& p, const DecodePlan& w, fa_dtype dt, cudaStream_t s);
 
 // Expanded latent attention's backward.
 struct LatentBwd {

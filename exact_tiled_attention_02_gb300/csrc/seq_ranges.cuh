@@ -101,7 +101,7 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool x) {
 // slices (all of them where there are rows enough to fill the GPU); lane i
 // holds the weight of part i, so that the parts' loads do not wait for one
 // another.  Rows of a sequence that was written directly are left alone.
-template <int BC, int NR, int W>
+template <int BC, int NR, int W, typename T>
 __global__ void __launch_bounds__(128)
     fa_seq_decode_merge_kernel(const __grid_constant__ SeqAttn p, const DecodePlan plan, const float* __restrict__ pre_o,
                                const float* __restrict__ pre_lse, int pre) {
@@ -172,14 +172,18 @@ __global__ void __launch_bounds__(128)
     }
   }
 #pragma unroll
-  for (int w = 0; w < W; ++w)
-    if (c + 128 * w < p.dv)
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + row * p.dv + c + 128 * w) =
-          make_uint2(pack_bf16x2(acc[w].x, acc[w].y), pack_bf16x2(acc[w].z, acc[w].w));
+  for (int w = 0; w < W; ++w) {
+    if (c + 128 * w >= p.dv) break;
+    T* dst = static_cast<T*>(p.o) + row * p.dv + c + 128 * w;
+    if constexpr (sizeof(T) == 4)
+      *reinterpret_cast<float4*>(dst) = acc[w];
+    else
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc[w].x, acc[w].y), pack_bf16x2(acc[w].z, acc[w].w));
+  }
   if (slice == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = m + logf(sum);
 }
 
-template <int BC, int NR>
+template <int BC, int NR, typename T = __nv_bfloat16>
 cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse, int pre,
                          bool after, cudaStream_t s) {
   // A warp takes a whole row of 512 where the rows alone give every SM 32 warps
@@ -191,12 +195,12 @@ cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre
   if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
   if (!after) {  // no kernel of this call before it: the lengths may only now be complete
-    fa_seq_decode_merge_kernel<BC, NR, 1><<<static_cast<unsigned>((rows * ((p.dv + 127) / 128) + 3) / 4), 128, 0, s>>>(
+    fa_seq_decode_merge_kernel<BC, NR, 1, T><<<static_cast<unsigned>((rows * ((p.dv + 127) / 128) + 3) / 4), 128, 0, s>>>(
         p, w, pre_o, pre_lse, pre);
     return cudaGetLastError();
   }
-  return wide ? launch_after(fa_seq_decode_merge_kernel<BC, NR, 4>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre)
-              : launch_after(fa_seq_decode_merge_kernel<BC, NR, 1>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
+  return wide ? launch_after(fa_seq_decode_merge_kernel<BC, NR, 4, T>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre)
+              : launch_after(fa_seq_decode_merge_kernel<BC, NR, 1, T>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
 }
 
 }  // namespace seq

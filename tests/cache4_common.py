@@ -66,11 +66,14 @@ def forward(q, k, v, scale, dtype):
     """(O, lse, tolerance of O, tolerance of lse) of a sequence's new tokens q [Hq, Nq, d] over k, v [Hkv, n, d].
 
     K, V = code * scale * tensor's scale; code * scale is exact in fp16 and
-    fp32, so what is rounded is q (fp16 relative to its row's largest entry:
-    2^-40 of that, less than the sums' steps), the fp32 sums (seq_bounds), P in
-    bf16 calls, to fp16: half a step 2^-11 relative, or 2^-25 absolute of a
-    largest P of 1 or more, and the output's own type.  The tensors' scales
-    cost two fp32 roundings more, within the sums' margin.
+    fp32, so what is rounded is q (fp16 terms relative to its row's largest
+    entry: 2^-39 of that at most, less than the sums' steps), the fp32 sums
+    (seq_bounds), P, and the output's own type.  P is taken 2^7 times as large,
+    as one fp16 number in bf16 calls, half a step 2^-11 relative, and as two in
+    float32 ones, 2^-22, and in both no finer than fp16's least half step, 2^-25
+    of 2^7 P: for each of n keys 2^-32, relative to a sum of P of at least its
+    largest, 1.  The tensors' scales cost two fp32 roundings more, within the
+    sums' margin.
     """
     G = q.shape[0] // k.shape[0]
     k, v = k.repeat(G, 0), v.repeat(G, 0)
@@ -79,8 +82,7 @@ def forward(q, k, v, scale, dtype):
     o = np.matmul(p, v)
     _, e = sb._score_errors(q, k, scale, sees)
     av = np.matmul(p, np.abs(v))
-    tol = (e + 2.0 ** -22) * av + sb.HALF[dtype] * np.abs(o) + 1e-30
-    if dtype == "bf16":
-        n = sees.sum(-1)[:, None]
-        tol = tol + 2.0 ** -11 * av + n * 2.0 ** -25 * (np.abs(v).max(1, keepdims=True) if v.shape[1] else 0.0)
+    n = sees.sum(-1)[:, None]
+    least = n * 2.0 ** -32 * (np.abs(v).max(1, keepdims=True) if v.shape[1] else 0.0)
+    tol = (e + 2.0 ** -22 + (2.0 ** -11 if dtype == "bf16" else 2.0 ** -22)) * av + least + sb.HALF[dtype] * np.abs(o) + 1e-30
     return o, lse, tol, e[..., 0] + 2.0 ** -22 + 2.0 ** -24 * np.abs(np.where(np.isfinite(lse), lse, 0.0))
