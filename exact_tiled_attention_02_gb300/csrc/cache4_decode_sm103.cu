@@ -51,20 +51,24 @@ constexpr float kBelow = 7.0f, kRescaleThreshold = kBelow + 8.0f;
 
 // F32: float32 q and o.  Q is then three fp16 terms and P two, which the
 // products take one after the other: 2^-33 and 2^-22 relative.
-template <int D, int NR, bool F32>
+template <int D, int NR, int NA, bool F32>
 struct Cfg {
   static constexpr int QT = F32 ? 3 : 1, PT = F32 ? 2 : 1;
   static constexpr int KC = D / 2;                   // columns of K in tensor memory, then 64 of V^T, S^T, O^T
   static constexpr int COLS = KC + 64 + 2 * NR;      // of a team
   static constexpr int W = 512 / COLS < 3 ? 512 / COLS : 3;
-  static constexpr int NH = NR / 2;                  // columns of a thread
+  // Query rows in use: NA of the product's NR columns (16 is the narrowest; what
+  // stands in the others reaches no row).  Past 16 both halves of a team take
+  // half of the softmax, else the half that unpacks K takes all of it.
+  static constexpr bool SPLIT = NR > 16;
+  static constexpr int NH = SPLIT ? NR / 2 : NA;     // columns of a thread
   static constexpr int THREADS = W * 256 + 64;
   static constexpr int QC = (D + 63) / 64;           // 64-channel chunks of Q
   static constexpr int RB = NR * 2;                  // bytes of a key's row of P
   static constexpr int TILE = 144 * D;               // bytes: 8 blocks of 18 D
   static constexpr int Q_BYTES = QC * NR * 128;      // a term
   static constexpr int P_BYTES = 128 * RB;           // a term of a team
-  static constexpr int VS_BYTES = W * 8 * 256;       // a warp's value scales in fp16: [2 groups][64 tokens]
+  static constexpr int VS_BYTES = W * 4 * 512;       // a warp's value scales in fp16: [2 groups][128 keys]
   static constexpr int STATS = (2 + 3 * W) * NR * 4  // lag, column scale; reference, sum and factor of each team
                                + W * 4 * NR * 4;     // warps' column results
   static constexpr int MISC = VS_BYTES + STATS + 512;
@@ -134,23 +138,9 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-// N consecutive bytes (2, 3 or 4), the first in the lowest; 2 and 4 are aligned to their size.
-template <int N>
-__device__ __forceinline__ uint32_t ld_shared_bytes(uint32_t addr) {
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
   uint32_t v;
-  if constexpr (N == 4) {
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  } else if constexpr (N == 2) {
-    asm volatile("{\n.reg .u16 t;\nld.shared.u16 t, [%1];\ncvt.u32.u16 %0, t;\n}" : "=r"(v) : "r"(addr) : "memory");
-  } else {
-    v = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      uint32_t x;
-      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(addr + i) : "memory");
-      v |= x << (8 * i);
-    }
-  }
+  asm volatile("{\n.reg .u16 t;\nld.shared.u16 t, [%1];\ncvt.u32.u16 %0, t;\n}" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
@@ -162,11 +152,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-template <int D, int NR, bool F32>
-__global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
+template <int D, int NR, int NA, bool F32>
+__global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     fa_cache4_decode_kernel(const __grid_constant__ SeqAttn p, const __grid_constant__ Cache4 cache,
                             const DecodePlan plan) {
-  using C = Cfg<D, NR, F32>;
+  using C = Cfg<D, NR, NA, F32>;
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   constexpr int W = C::W, SLOTS = C::SLOTS, GROUPS = D / 16, NH = C::NH;
   constexpr int kConsumers = W * 256;
@@ -214,7 +204,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
       mbar_init(free_(s), 8);
     }
     for (int w = 0; w < W; ++w) {
-      mbar_init(k_ready(w), 8);
+      mbar_init(k_ready(w), C::SPLIT ? 8 : 4);
       mbar_init(s_done(w), 1);
       mbar_init(p_ready(w), 8);
       mbar_init(o_done(w), 1);
@@ -383,21 +373,26 @@ __global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
     // ----------------------------------------------------- unpacking, softmax
     // Once a wait has run out, waits return at once and the loops run on to
     // their ends (barriers count every warp); nothing is written out then.
-    const int w = warp >> 3, half = (warp >> 2) & 1, quarter = warp & 3;
-    const int id = threadIdx.x & 127;                                      // a key, then a channel
+    const int w = warp >> 3, quarter = warp & 3;
+    const bool keys = (warp & 4) == 0;     // this half of the team unpacks K, the other V
+    const bool rows = keys || C::SPLIT;    // and has columns of the softmax
+    const int id = threadIdx.x & 127;      // a key, or a channel
     const uint32_t tl = tmem + w * C::COLS + (static_cast<uint32_t>(quarter * 32) << 16);  // this team's columns, this warp's lanes
     const uint32_t sP = sb + C::OFF_P + w * C::PT * C::P_BYTES;
-    const uint32_t sVS = sb + C::OFF_VS + warp * 256;
-    const int c0 = half * NH;  // this thread's columns: c0 .. c0 + NH - 1
+    const uint32_t sVS = sb + C::OFF_VS + (w * 4 + quarter) * 512;
+    const int c0 = C::SPLIT && !keys ? NH : 0;  // this thread's columns: c0 .. c0 + NH - 1
     float* ref = s_ref + w * NR;
     float* fac = s_fac + w * NR;
     float* red = s_red + w * 4 * NR;
+    constexpr int kRows = C::SPLIT ? 256 : 128;   // threads of a team with columns
     constexpr int RCOLS = NH > 32 ? NH / 32 : 1;  // columns that a lane owns after a reduction
     const int my_col = c0 + first_col<NH>();
     const int tid = threadIdx.x & 255;  // within the team
-    auto team_sync = [&]() { named_bar_sync(1 + w, 256); };
+    auto rows_sync = [&]() { named_bar_sync(1 + w, kRows); };
     auto all_sync = [&]() { named_bar_sync(8, kConsumers); };
-    int g = 0, mine = 0;  // tiles of the CTA so far, and of this team
+    // the team's tiles are w, w + W, ... of the CTA's: the next one, its ring slot, and that slot's phase
+    int g0 = 0, next_tile = w, mine = 0, slot = w;
+    uint32_t phase = 0;
 
     // Q rows of a sequence: a warp takes rows warp, warp + 8 W, ...; a lane 4 channels of one
     constexpr int QR = (NR + 8 * W - 1) / (8 * W);
@@ -465,65 +460,71 @@ __global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
 #pragma unroll
       for (int c = 0; c < NH; ++c) l[c] = 0.f;
       if (tid < NR) ref[tid] = kUnset;
+      if (rows) rows_sync();
       bool any = false;  // this team has had a tile of the piece
-      for (int i = 0; i < n; ++i, ++g) {
-        if (g % W != w) continue;
-        const int slot = g % SLOTS;
-        warp_wait(full(slot), (g / SLOTS) & 1, wc);
+      for (; next_tile < g0 + n; next_tile += W) {
+        warp_wait(full(slot), phase, wc);
         const uint32_t base = sRing + slot * C::TILE;
         const int missing = s_missing[slot];
-        const int j0 = (t0 + i) * BC, valid = min(BC, nk - j0);
-        // ---- K: a thread half the channels of a key
-        {
-          constexpr int GH = GROUPS / 2;
-          const uint32_t t = id & 15, blk = base + (id >> 4) * (18 * D) + half * GH * 128 + t * 8;
-          uint32_t sc[2];
-          uint32_t s4 = ld_shared_bytes<GH>(base + (id >> 4) * (18 * D) + 8 * D + t * GROUPS + half * GH);
-          if ((missing >> (id >> 4)) & 1) s4 = 0;  // no page: zeros
-          cache4::scales_f16(s4, sc);
-          const uint32_t to = tl + C::TM_K + half * GH * 8;
-          uint32_t o[16];
+        const int j0 = (t0 + next_tile - g0) * BC, valid = min(BC, nk - j0);
+        // (the other half has read the last tile's scores, which S^T is to replace)
+        if (C::SPLIT && !keys && lane == 0) mbar_arrive(k_ready(w));
+        if (keys) {
+          // ---- K: a thread a key
+          const uint32_t t = id & 15, blk = base + (id >> 4) * (18 * D);
+          const bool gone = (missing >> (id >> 4)) & 1;  // no page: zeros
+          const uint32_t sa = blk + 8 * D + t * GROUPS, ka = blk + t * 8;
 #pragma unroll
-          for (int c = 0; c < GH; ++c) {
-            const uint2 a = ld_shared_v2(blk + c * 128);
-            const uint32_t s2 = __byte_perm(sc[c >> 1], 0, c & 1 ? 0x3232 : 0x1010);
-            uint32_t* x = o + 8 * (c & 1);
-            cache4::codes_f16(a.x, x);
-            cache4::codes_f16(a.y, x + 4);
-#pragma unroll
-            for (int y = 0; y < 8; ++y) x[y] = cache4::mul_f16x2(x[y], s2);
-            if (c & 1)
-              tmem_st_32x32b_x16(to + 8 * (c - 1), o);
-            else if (c == GH - 1)
-              tmem_st_32x32b_x8(to + 8 * c, o);
-          }
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_ready(w));
-        // ---- V: a thread half the keys of a channel
-        if (quarter * 32 < D) {
-          // the scales of the warp's two groups and 64 keys, zeros past the sequence's end and in missing pages
-          {
-            const int k = half * 4 + ((lane >> 2) & 3), t = (lane & 3) * 4;  // block, first of four keys
+          for (int c = 0; c < GROUPS; c += 2) {
+            const uint2 a = ld_shared_v2(ka + c * 128), e = ld_shared_v2(ka + (c + 1) * 128);
             uint32_t sc[2];
-            cache4::scales_f16(ld_shared_bytes<4>(base + k * 18 * D + 17 * D + (2 * quarter + (lane >> 4)) * 16 + t), sc);
+            cache4::scales_f16(gone ? 0u : ld_shared_u16(sa + c), sc);
+            const uint32_t s0 = __byte_perm(sc[0], 0, 0x1010), s1 = __byte_perm(sc[0], 0, 0x3232);
+            uint32_t o[16];
+            cache4::codes_f16(a.x, o);
+            cache4::codes_f16(a.y, o + 4);
+            cache4::codes_f16(e.x, o + 8);
+            cache4::codes_f16(e.y, o + 12);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              o[x] = cache4::mul_f16x2(o[x], s0);
+              o[8 + x] = cache4::mul_f16x2(o[8 + x], s1);
+            }
+            tmem_st_32x32b_x16(tl + C::TM_K + 8 * c, o);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(k_ready(w));
+            mbar_arrive(free_(slot));
+          }
+        } else if (quarter * 32 >= D) {
+          if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);  // arrive for this tile, not for the last one
+        } else {
+          // ---- V: a thread a channel.  First the scales of the warp's two groups,
+          // zeros past the sequence's end and in missing pages.
+          {
+            const int k = (lane & 15) >> 1, t = (lane & 1) * 8;  // block, first of eight keys
+            uint32_t sc[4];
+            const uint2 s8 = ld_shared_v2(base + k * 18 * D + 17 * D + (2 * quarter + (lane >> 4)) * 16 + t);
+            cache4::scales_f16(s8.x, sc);
+            cache4::scales_f16(s8.y, sc + 2);
             if (valid < BC || missing != 0) {
               const int room = (missing >> k) & 1 ? 0 : valid - 16 * k - t;
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
+              for (int y = 0; y < 4; ++y)
                 sc[y] &= (2 * y < room ? 0xffffu : 0u) | (2 * y + 1 < room ? 0xffff0000u : 0u);
             }
-            st_shared_v2(sVS + lane * 8, sc[0], sc[1]);
+            st_shared_v4(sVS + lane * 16, sc[0], sc[1], sc[2], sc[3]);
           }
           __syncwarp();
-          // the last product of this team has read V^T and P
+          // the last product of this team has read V^T
           if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);
           tc_fence_after();
-          const uint32_t cb = base + half * 4 * 18 * D + 9 * D + id * 8, cs = sVS + (lane >> 4) * 128;
+          const uint32_t cb = base + 9 * D + id * 8, cs = sVS + (lane >> 4) * 256;
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
+          for (int x = 0; x < 4; ++x) {
             uint32_t o[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -542,131 +543,153 @@ __global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
               y[6] = cache4::mul_f16x2(y[6], se.z);
               y[7] = cache4::mul_f16x2(y[7], se.w);
             }
-            tmem_st_32x32b_x16(tl + C::TM_V + half * 32 + 16 * x, o);
+            tmem_st_32x32b_x16(tl + C::TM_V + 16 * x, o);
           }
-        } else if (mine > 0) {
-          warp_wait(o_done(w), (mine - 1) & 1, wc);
+        }
+        if (!keys) {
+          if (!C::SPLIT) {
+            tmem_wait_st();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(free_(slot));
+            if (!C::SPLIT) mbar_arrive(p_ready(w));
+          }
+        }
+        if (rows) {
+          // ---- scores, in the log2 domain and against the row's reference
+          warp_wait(s_done(w), mine & 1, wc);
           tc_fence_after();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(free_(slot));
-        // ---- scores
-        warp_wait(s_done(w), mine & 1, wc);
-        tc_fence_after();
-        float s[NH];
-        {
-          uint32_t r[NH];
-          tmem_ld<NH>(tl + C::TM_S + c0, r);
-          tmem_wait_ld();
+          const bool edge = j0 + BC > nk - (p.n_new - 1);  // some row does not see the whole tile
+          const int room = nk - (j0 + id);                 // > lag: the row sees this key
+          float x[NH];
+          auto scores = [&]() {
+            uint32_t r[NH];
+            tmem_ld<NH>(tl + C::TM_S + c0, r);
+            tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < NH; ++x) s[x] = __uint_as_float(r[x]);
-        }
-        if (j0 + BC > nk - (p.n_new - 1)) {
-          const int room = nk - (j0 + id);  // > lag: the row sees this key
+            for (int c = 0; c < NH; ++c) x[c] = __uint_as_float(r[c]);
+            if (edge) {
 #pragma unroll
-          for (int c = 0; c < NH; ++c) s[c] = s_lag[c0 + c] < room ? s[c] : -INFINITY;
-        }
-        float over = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < NH; c += 4) {
-          const float4 nr = *reinterpret_cast<const float4*>(ref + c0 + c);
-          const float4 cs = *reinterpret_cast<const float4*>(s_cs + c0 + c);
-          over = fmax3(over, fmaf(s[c], cs.x, nr.x), fmaf(s[c + 1], cs.y, nr.y));
-          over = fmax3(over, fmaf(s[c + 2], cs.z, nr.z), fmaf(s[c + 3], cs.w, nr.w));
-        }
-        if (bar_any(1 + w, 256, over > kRescaleThreshold)) {
-          // some row's reference rises: column maxima over the 128 keys
-          {
-            float v[NH];
-#pragma unroll
-            for (int c = 0; c < NH; ++c) v[c] = s[c] * s_cs[c0 + c];
-            reduce_step<NH / 2, 16>(v, [](float x, float y) { return fmaxf(x, y); });
-#pragma unroll
-            for (int x = 0; x < RCOLS; ++x) red[quarter * NR + my_col + x] = v[x];
-          }
-          team_sync();
-          if (tid < NR) {
-            const float mx = fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid]));
-            const float old = ref[tid];
-            float alpha = 1.f;
-            if (mx + old > kRescaleThreshold) {  // old = kUnset: the first key that the row sees
-              alpha = old == kUnset ? 0.f : ex2_approx(kBelow - old - mx);
-              ref[tid] = kBelow - mx;
+              for (int c = 0; c < NH; ++c) x[c] = s_lag[c0 + c] < room ? x[c] : -INFINITY;
             }
-            fac[tid] = alpha;
-          }
-          team_sync();
+          };
+          auto against = [&]() {
 #pragma unroll
-          for (int c = 0; c < NH; ++c) l[c] *= fac[c0 + c];
-          if (any) {
+            for (int c = 0; c < NH; c += 4) {
+              const float4 nr = *reinterpret_cast<const float4*>(ref + c0 + c);
+              const float4 cs = *reinterpret_cast<const float4*>(s_cs + c0 + c);
+              x[c] = fmaf(x[c], cs.x, nr.x);
+              x[c + 1] = fmaf(x[c + 1], cs.y, nr.y);
+              x[c + 2] = fmaf(x[c + 2], cs.z, nr.z);
+              x[c + 3] = fmaf(x[c + 3], cs.w, nr.w);
+            }
+          };
+          scores();
+          against();
+          float over = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < NH; c += 2) over = fmax3(over, x[c], x[c + 1]);
+          const bool rises = bar_any(1 + w, kRows, over > kRescaleThreshold);
+          // the last product of this team has read P (and O is complete)
+          if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);
+          if (rises) {
+            // some row's reference rises: column maxima over the 128 keys
+            tc_fence_after();
+            scores();
+#pragma unroll
+            for (int c = 0; c < NH; ++c) x[c] *= s_cs[c0 + c];
+            reduce_step<NH / 2, 16>(x, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+            for (int y = 0; y < RCOLS; ++y) red[quarter * NR + my_col + y] = x[y];
+            rows_sync();
+            if (tid < NA) {
+              const float mx = fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid]));
+              const float old = ref[tid];
+              float alpha = 1.f;
+              if (mx + old > kRescaleThreshold) {  // old = kUnset: the first key that the row sees
+                alpha = old == kUnset ? 0.f : ex2_approx(kBelow - old - mx);
+                ref[tid] = kBelow - mx;
+              }
+              fac[tid] = alpha;
+            }
+            rows_sync();
+#pragma unroll
+            for (int c = 0; c < NH; ++c) l[c] *= fac[c0 + c];
+            if (any) {
 #pragma unroll 1
-            for (int c = c0; c < c0 + NH; c += 8) {
-              uint32_t o[8];
-              tmem_ld_32x32b_x8(tl + C::TM_O + c, o);
-              tmem_wait_ld();
+              for (int c = c0; c < c0 + NH; c += 8) {
+                uint32_t o[8];
+                tmem_ld_32x32b_x8(tl + C::TM_O + c, o);
+                tmem_wait_ld();
 #pragma unroll
-              for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fac[c + x]);
-              tmem_st_32x32b_x8(tl + C::TM_O + c, o);
-            }
-          }
-        }
-        // ---- P
-#pragma unroll
-        for (int c = 0; c < NH; c += 8) {
-          float x[8];
-#pragma unroll
-          for (int y = 0; y < 8; y += 4) {
-            const float4 nr = *reinterpret_cast<const float4*>(ref + c0 + c + y);
-            const float4 cs = *reinterpret_cast<const float4*>(s_cs + c0 + c + y);
-            x[y] = ex2_approx(fmaf(s[c + y], cs.x, nr.x));
-            x[y + 1] = ex2_approx(fmaf(s[c + y + 1], cs.y, nr.y));
-            x[y + 2] = ex2_approx(fmaf(s[c + y + 2], cs.z, nr.z));
-            x[y + 3] = ex2_approx(fmaf(s[c + y + 3], cs.w, nr.w));
-          }
-#pragma unroll
-          for (int y = 0; y < 8; ++y) l[c + y] += x[y];
-          // P is rounded to fp16, the products' type: half a step of 2^-11 each
-          // (of a second term too, where there is one: 2^-22)
-          const uint32_t at = sP + id * C::RB + p_chunk<C::RB>(id, (c0 + c) / 8) * 16;
-#pragma unroll
-          for (int t = 0; t < C::PT; ++t) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              pk[y] = pack_f16x2(x[2 * y], x[2 * y + 1]);
-              if (t + 1 < C::PT) {
-                const float2 h = cache4::floats(pk[y]);
-                x[2 * y] -= h.x;
-                x[2 * y + 1] -= h.y;
+                for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * fac[c + y]);
+                tmem_st_32x32b_x8(tl + C::TM_O + c, o);
               }
             }
-            st_shared_v4(at + t * C::P_BYTES, pk[0], pk[1], pk[2], pk[3]);
+            scores();
+            against();
           }
+          // ---- P
+#pragma unroll
+          for (int c = 0; c < NH; c += 8) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              x[c + y] = ex2_approx(x[c + y]);
+              l[c + y] += x[c + y];
+            }
+            // P is rounded to fp16, the products' type: half a step of 2^-11 each
+            // (of a second term too, where there is one: 2^-22)
+            const uint32_t at = sP + id * C::RB + p_chunk<C::RB>(id, (c0 + c) / 8) * 16;
+#pragma unroll
+            for (int t = 0; t < C::PT; ++t) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                pk[y] = pack_f16x2(x[c + 2 * y], x[c + 2 * y + 1]);
+                if (t + 1 < C::PT) {
+                  const float2 h = cache4::floats(pk[y]);
+                  x[c + 2 * y] -= h.x;
+                  x[c + 2 * y + 1] -= h.y;
+                }
+              }
+              st_shared_v4(at + t * C::P_BYTES, pk[0], pk[1], pk[2], pk[3]);
+            }
+          }
+          if (tid == 0) s_first[w] = !any;
+          fence_proxy_async_smem();
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready(w));
         }
-        if (tid == 0) s_first[w] = !any;
-        fence_proxy_async_smem();
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready(w));
         any = true;
         ++mine;
+        slot += W;
+        if (slot >= SLOTS) {
+          slot -= SLOTS;
+          phase ^= 1;
+        }
       }
       // ------------------------------------------------------------ output
       if (any) warp_wait(o_done(w), (mine - 1) & 1, wc);
       tc_fence_after();
-      reduce_step<NH / 2, 16>(l, [](float x, float y) { return x + y; });
+      if (rows) {
+        reduce_step<NH / 2, 16>(l, [](float x, float y) { return x + y; });
 #pragma unroll
-      for (int x = 0; x < RCOLS; ++x) red[quarter * NR + my_col + x] = l[x];
-      team_sync();
-      if (tid < NR) s_sum[w * NR + tid] = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
+        for (int x = 0; x < RCOLS; ++x) red[quarter * NR + my_col + x] = l[x];
+        rows_sync();
+        if (tid < NA) s_sum[w * NR + tid] = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
+      }
+      g0 += n;
       tc_fence_before();
       all_sync();
       tc_fence_after();
       const bool whole = t0 == 0 && n == tiles_of<BC>(nk);
-      const long long slot = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + cut + b;
+      const long long part = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + cut + b;
       const long long orow0 = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r0;
-      if (threadIdx.x < NR) {  // the teams' O share one reference: the largest
+      if (threadIdx.x < NA) {  // the teams' O share one reference: the largest
         const int c = threadIdx.x;
         float m = -INFINITY, sum = 0.f;
 #pragma unroll
@@ -684,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
         const float lse = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994531f;
         if (c < n_rows && !*abort_flag) {
           if (!whole)
-            p.part_lse[slot * NR + c] = lse;
+            p.part_lse[part * NR + c] = lse;
           else if (p.lse != nullptr)
             p.lse[orow0 + c] = lse;
         }
@@ -699,7 +722,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
 #pragma unroll
         for (int y = 0; y < W; ++y) {
           __syncwarp();
-          if (n < W && (g - 1 - y + W * (n + W)) % W >= n) continue;  // team y had no tile
+          if (n < W && (g0 - 1 - y + W * (n + W)) % W >= n) continue;  // team y had no tile
           uint32_t o[8];
           tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + y * C::COLS + C::TM_O + c, o);
           tmem_wait_ld();
@@ -714,7 +737,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
         for (int x = 0; x < 8; ++x) {
           if (c + x >= n_rows) break;
           if (!whole)
-            p.part_o[(slot * NR + c + x) * D + id] = acc[x];
+            p.part_o[(part * NR + c + x) * D + id] = acc[x];
           else if constexpr (F32)
             static_cast<float*>(p.o)[(orow0 + c + x) * D + id] = acc[x];
           else
@@ -735,20 +758,20 @@ __global__ void __launch_bounds__(Cfg<D, NR, F32>::THREADS, 1)
   }
 }
 
-template <int D, int NR, bool F32>
+template <int D, int NR, int NA, bool F32>
 cudaError_t launch_nr(const SeqAttn& p, const Cache4& c, const DecodePlan& plan, cudaStream_t s) {
-  using C = Cfg<D, NR, F32>;
+  using C = Cfg<D, NR, NA, F32>;
   static SmemOnce once;
-  const cudaError_t e = once(fa_cache4_decode_kernel<D, NR, F32>, C::SMEM_BYTES);
+  const cudaError_t e = once(fa_cache4_decode_kernel<D, NR, NA, F32>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(plan.heads) * plan.row_groups * plan.cuts;
-  fa_cache4_decode_kernel<D, NR, F32><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(p, c, plan);
+  fa_cache4_decode_kernel<D, NR, NA, F32><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(p, c, plan);
   return cudaGetLastError();
 }
 template <int D, bool F32>
 cudaError_t launch_d(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s) {
-  if (w.nr == 16) return launch_nr<D, 16, F32>(p, c, w, s);
-  return w.nr == 32 ? launch_nr<D, 32, F32>(p, c, w, s) : launch_nr<D, 64, F32>(p, c, w, s);
+  if (w.nr == 16) return p.rows <= 8 ? launch_nr<D, 16, 8, F32>(p, c, w, s) : launch_nr<D, 16, 16, F32>(p, c, w, s);
+  return w.nr == 32 ? launch_nr<D, 32, 32, F32>(p, c, w, s) : launch_nr<D, 64, 64, F32>(p, c, w, s);
 }
 template <bool F32>
 cudaError_t launch_type(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s) {
