@@ -45,14 +45,17 @@ bool attn_sizes_ok(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages,
   if (Hkv < 1 || Hq % Hkv != 0 || page_size < 1 || d > kMaxD) return false;
   const long long keys = paged_keys(page_size, max_pages);
   return sizes_ok(B, Hq, Nq, d) && sizes_ok(B, max_pages) && keys > 0 &&
-         static_cast<long long>(B) * Hq * Nq <= 0x7fffffffLL / 8 && tiles_ok(B, keys);
+         static_cast<long long>(B) * Hq * Nq <= 0x7fffffffLL / 8 &&
+         B * ((keys + 127) / 128) * 457 <= 0x7fffffffLL;  // tiles of 128 times the most ranges they are cut into
 }
 PartLayout attn_layout(int B, int Hq, int Hkv, int Nq, int n_keys, int d) {
   return part_layout(cache4_simt_splits(B, Hq, Hkv, Nq, n_keys, d), 0, static_cast<long long>(B) * Hq * Nq, d);
 }
 // on the tensor cores: the pieces of sequences that several CTAs share
 bool tensor_cores(int d) { return d == 64 || d == 96 || d == 128; }
-DecodePlan attn_plan(int B, int Hq, int Hkv, int Nq) { return cache4_plan(B, Hkv, Hq / Hkv * Nq, 152); }
+DecodePlan attn_plan(int B, int Hq, int Hkv, int Nq, int d, fa_dtype dt) {
+  return cache4_plan(B, Hkv, Hq / Hkv * Nq, d, dt, 152);
+}
 PartLayout attn_layout_tc(const DecodePlan& plan, int d) {
   return part_layout(1, 0, static_cast<long long>(decode_slots(plan)), d);
 }
@@ -97,7 +100,11 @@ fa_status fa_cache_fp4_read(const void* cache, const int* block_table, const int
 
 size_t fa_fwd_cache_fp4_workspace_bytes(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages, int d) {
   if (!attn_sizes_ok(B, Hq, Hkv, Nq, page_size, max_pages, d)) return 0;
-  if (tensor_cores(d)) return attn_layout_tc(attn_plan(B, Hq, Hkv, Nq), d).bytes;
+  if (tensor_cores(d)) {
+    const size_t f32 = attn_layout_tc(attn_plan(B, Hq, Hkv, Nq, d, FA_DTYPE_F32), d).bytes;
+    const size_t bf16 = attn_layout_tc(attn_plan(B, Hq, Hkv, Nq, d, FA_DTYPE_BF16), d).bytes;
+    return f32 > bf16 ? f32 : bf16;
+  }
   return attn_layout(B, Hq, Hkv, Nq, static_cast<int>(paged_keys(page_size, max_pages)), d).bytes;
 }
 
@@ -118,7 +125,7 @@ fa_status fa_fwd_cache_fp4(const void* q, const void* cache, const int* block_ta
   if (device_status_ptr(&c.status) != cudaSuccess) return FA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (tensor_cores(d)) {
-    const DecodePlan plan = attn_plan(B, Hq, Hkv, Nq);
+    const DecodePlan plan = attn_plan(B, Hq, Hkv, Nq, d, dt);
     SeqAttn a{};
     a.q = q;
     a.o = o;

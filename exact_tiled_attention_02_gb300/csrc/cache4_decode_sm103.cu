@@ -15,22 +15,22 @@
 // two that brings its largest entry to 2^14 .. 2^15, exact down to 2^-31 of that;
 // P is rounded to 11 bits where bf16 would keep 8.
 //
-// W teams of eight warps take the tiles in turn, each with operands, scores and
-// an O of its own in tensor memory and its own running reference, so that one's
-// products and waits overlap another's unpacking; they meet at the end of a
-// piece (a CTA's share of a sequence) only, where all O are added up.  Per tile
-// a team unpacks K (two threads a key), then V while S^T is computed (two a
-// channel), takes the softmax (two a key) and writes P.  One more warp issues
-// every product, told by mbarriers, so that no team waits for its own warps.
+// W teams of eight warps, each with a range of the tiles, a ring, operands,
+// scores and an O in tensor memory of its own: they share nothing, so that
+// one's waits (products, the end of a sequence) overlap another's unpacking.  Of
+// a team half unpacks K, a thread a key, half V, a thread a channel; the first
+// takes the softmax, or both a half of the columns where there are more than 16.
+// One more warp issues all products, told by mbarriers, so that the warps of a
+// team do not wait for one another around them.
 //
 // Statistics run down the columns, across lanes.  Per tile a thread (one key)
 // only checks whether any of its scores exceeds its column's reference by 2^8;
 // if no key's does (one barrier with an OR) the tile is exponentiated as it is.
 // Otherwise the column maxima are reduced across lanes and warps and O rescaled.
 //
-// One more warp loads: a tile's blocks, one bulk copy for each run of them in
-// a page, into a ring of as many tiles as fit.  The work is split as
-// seq_ranges.cuh says; a sequence that is one whole piece goes straight to o.
+// One more warp loads: a tile's blocks, one bulk copy for each run of them in a
+// page.  The work is split as seq_ranges.cuh says, a range a team; a sequence
+// that is one whole piece goes straight to o.
 #include <cmath>
 #include <type_traits>
 
@@ -69,25 +69,27 @@ struct Cfg {
   static constexpr int Q_BYTES = QC * NR * 128;      // a term
   static constexpr int P_BYTES = 128 * RB;           // a term of a team
   static constexpr int VS_BYTES = W * 4 * 512;       // a warp's value scales in fp16: [2 groups][128 keys]
-  static constexpr int STATS = (2 + 3 * W) * NR * 4  // lag, column scale; reference, sum and factor of each team
-                               + W * 4 * NR * 4;     // warps' column results
-  static constexpr int MISC = VS_BYTES + STATS + 512;
-  static constexpr int SLOTS_FIT = (227 * 1024 - 1024 - QT * Q_BYTES - W * PT * P_BYTES - MISC) / TILE;
-  static constexpr int SLOTS = SLOTS_FIT < 12 ? SLOTS_FIT : 12;
+  static constexpr int STATS = 6 * NR * 4                  // a team: lag, column scale, reference, factor
+                               + 4 * NR * 4;               // and warps' column results
+  static constexpr int MISC = VS_BYTES + W * STATS + 512;
+  static constexpr int FIT = (227 * 1024 - 1024 - W * (QT * Q_BYTES + PT * P_BYTES) - MISC) / TILE / W;
+  static constexpr int SL = FIT < 4 ? FIT : 4;             // ring slots of a team
+  static constexpr int SLOTS = W * SL;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_P = OFF_Q + QT * Q_BYTES;
+  static constexpr int OFF_P = OFF_Q + W * QT * Q_BYTES;
   static constexpr int OFF_RING = OFF_P + W * PT * P_BYTES;
   static constexpr int OFF_VS = OFF_RING + SLOTS * TILE;
   static constexpr int OFF_STAT = OFF_VS + VS_BYTES;
-  static constexpr int OFF_BAR = OFF_STAT + STATS;
+  static constexpr int OFF_BAR = OFF_STAT + W * STATS;
   static constexpr int NBAR = 2 * SLOTS + 4 * W + 1;
-  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tensor memory base, abort flag, start; teams' first-tile flags; slots' missing blocks
-  static constexpr int SMEM_USED = OFF_MISC + 24 + W * 4 + SLOTS * 4;
+  // tensor memory base, abort flag; teams' first sequence, its first tile, their tiles; first-tile flags; slots' missing blocks
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM_USED = OFF_MISC + 8 + W * 16 + SLOTS * 4;
   static constexpr int SMEM_BYTES = SMEM_USED + 1024;
   static constexpr int TM_K = 0, TM_V = KC, TM_S = KC + 64, TM_O = TM_S + NR;
-  static_assert(W >= 2 && SLOTS >= 2 * W, "two tiles a team in flight");
+  static_assert(W >= 2 && W <= 4 && SL >= 2, "two tiles a team in flight, eight lanes a team");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-  static_assert(OFF_P % 1024 == 0 && P_BYTES % 1024 == 0 && OFF_RING % 1024 == 0 && TILE % 16 == 0, "alignment");
+  static_assert(Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0 && OFF_RING % 1024 == 0 && TILE % 16 == 0, "alignment");
 };
 
 // fp16 operands: formats 0 in the bf16 descriptor's fields
@@ -159,7 +161,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
   using C = Cfg<D, NR, NA, F32>;
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
   constexpr int W = C::W, SLOTS = C::SLOTS, GROUPS = D / 16, NH = C::NH;
-  constexpr int kConsumers = W * 256;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t pad = (1024u - (raw & 1023u)) & 1023u;
@@ -171,12 +172,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
   uint8_t* smem = smem_raw + pad;
   const uint32_t sb = raw + pad;
   const uint32_t sQ = sb + C::OFF_Q, sRing = sb + C::OFF_RING;
-  int* s_lag = reinterpret_cast<int*>(smem + C::OFF_STAT);           // [NR]
-  float* s_cs = reinterpret_cast<float*>(s_lag + NR);                // [NR] log2-domain scale of a column
-  float* s_ref = s_cs + NR;                                          // [W][NR] negated references
-  float* s_sum = s_ref + W * NR;                                     // [W][NR]
-  float* s_fac = s_sum + W * NR;                                     // [W][NR] alpha, then the factor of an O
-  float* s_red = s_fac + W * NR;                                     // [W][4][NR]
   const uint32_t bars = sb + C::OFF_BAR;
   auto full = [&](int s) { return bars + 8 * s; };
   auto free_ = [&](int s) { return bars + 8 * (SLOTS + s); };
@@ -187,14 +182,16 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
   const uint32_t drain_bar = bars + 8 * (2 * SLOTS + 4 * W);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  int* s_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);  // first sequence, its first tile, tiles of this CTA
-  volatile int* s_first = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 24);  // [W] a team's tile is its first of a piece
-  volatile int* s_missing = s_first + W;                                             // [SLOTS] blocks without a page
+  int* s_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);    // [W][3] first sequence, its first tile, tiles of a team
+  volatile int* s_first = reinterpret_cast<volatile int*>(s_start + 3 * W);  // [W] a team's tile is its first of a piece
+  volatile int* s_missing = s_first + W;                                     // [SLOTS] blocks without a page
   const WaitCtl wc{p.status, abort_flag, p.wait_ns};
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
-  // this CTA: rows r0 .. of head `head` of every sequence (group b * heads + head), range `cut` of `cuts`
-  const int grp = blockIdx.x / plan.cuts, cut = blockIdx.x % plan.cuts;
+  // this CTA: rows r0 .. of head `head` of every sequence (group b * heads + head);
+  // team w takes range w * ctas + cta of plan.cuts, so that few ranges spread over the SMs
+  const int ctas = plan.cuts / W;
+  const int grp = blockIdx.x / ctas, cta = blockIdx.x % ctas;
   const int head = grp / plan.row_groups, r0 = (grp % plan.row_groups) * NR;
   const int n_rows = min(NR, p.rows - r0);
 
@@ -218,97 +215,110 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  if (warp == 8 * W + 1) {
+  if (warp < 8 * W && (warp & 7) == 0) {
     int b0, first, count;
-    find_range<BC>(p, plan, cut, b0, first, count);
+    find_range<BC>(p, plan, (warp >> 3) * ctas + cta, b0, first, count);
     if (lane == 0) {
-      s_start[0] = b0;
-      s_start[1] = first;
-      s_start[2] = count;
+      s_start[3 * (warp >> 3)] = b0;
+      s_start[3 * (warp >> 3) + 1] = first;
+      s_start[3 * (warp >> 3) + 2] = count;
     }
-  } else if (threadIdx.x < NR) {
-    s_lag[threadIdx.x] = p.n_new - 1 - (r0 + static_cast<int>(threadIdx.x)) % p.n_new;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  const int start_b = __shfl_sync(0xffffffffu, s_start[0], 0), start_t = __shfl_sync(0xffffffffu, s_start[1], 0),
-            n_tiles = __shfl_sync(0xffffffffu, s_start[2], 0);
-
-  // walks the pieces, a whole warp at a time: f(sequence, its keys, first tile, tiles, next sequence or -1)
-  auto pieces = [&](auto f) {
-    int b = start_b, t = start_t, left = n_tiles;
-    while (left > 0 && b < plan.n_seq) {
-      const int nk = __shfl_sync(0xffffffffu, seq_len(p, b, false), 0);
-      const int take = min(left, tiles_of<BC>(nk) - t);
-      if (take > 0) {
-        left -= take;
-        int next = -1;
-        if (left > 0) {  // the next sequence with keys
-          next = b + 1;
-          while (next + 1 < plan.n_seq && seq_len(p, next, false) == 0) ++next;
-        }
-        if (!f(b, nk, t, take, next)) return;
-      }
-      ++b;
-      t = 0;
-    }
-  };
 
   if (warp == 8 * W + 1) {
     // ---------------------------------------------------------------- loads
-    // Lane i (of 8) looks block i of a tile up; the first lane of every run of
-    // blocks that lie side by side in a page copies the run.
-    int g = 0;  // tiles issued
+    // Eight lanes a team walk its tiles, a block a lane; the first lane of every
+    // run of blocks that lie side by side in a page copies the run.
+    const int w = lane >> 3, i = lane & 7;
     const int per_page = cache.page_size / 16;
-    pieces([&](int b, int nk, int t0, int n, int) -> bool {
-      const int blocks = (nk + 15) / 16;
-      // this lane's block of a tile: its page as the table has it (-1: past the end, -2: no such page), its place there
-      auto place = [&](int tile, int& page, int& at) {
-        const int i = tile * 8 + lane;
-        page = at = -1;
-        if (lane >= 8 || i >= blocks) return;
-        const int q = i / per_page;
-        at = i - q * per_page;
-        page = cache.table != nullptr ? cache.table[static_cast<long long>(b) * cache.max_pages + q] : b;
-        if (page < 0 || page >= cache.n_pages) page = -2;
-      };
-      int page, at;
-      place(t0, page, at);
-      for (int i = 0; i < n; ++i, ++g) {
-        int page1 = -1, at1 = -1;
-        if (i + 1 < n) place(t0 + i + 1, page1, at1);  // the next tile's pages, while this one loads
-        const int slot = g % SLOTS;
-        if (g >= SLOTS && !warp_wait(free_(slot), (g / SLOTS - 1) & 1, wc)) return false;
-        const bool here = page >= 0;
-        if (page == -2) atomicOr(p.status, kStatusInput);
-        const unsigned missing = __ballot_sync(0xffffffffu, page == -2);
-        const unsigned have = __ballot_sync(0xffffffffu, here);
-        const int before = __shfl_up_sync(0xffffffffu, page, 1);
-        const bool starts = here && (lane == 0 || before != page || at == 0);
-        const unsigned heads = __ballot_sync(0xffffffffu, starts);
-        if (lane == 0) {
-          s_missing[slot] = static_cast<int>(missing);
-          mbar_arrive_expect_tx(full(slot), __popc(have) * 18 * D);
-        }
-        __syncwarp();
-        if (starts) {
-          const unsigned ends = (heads | ~have) & (0xfffffffeu << lane);  // never empty: lanes from 8 on have none
-          const int run = __ffs(ends) - 1 - lane;
-          const long long src = ((static_cast<long long>(page) * cache.Hkv + head) * per_page + at) * (18 * D);
-          bulk_load(sRing + slot * C::TILE + lane * 18 * D, cache.cache + src, run * 18 * D, full(slot));
-        }
-        page = page1;
-        at = at1;
+    int b = 0, t = 0, left = 0;  // the next tile's sequence and place there, tiles to go
+    if (w < W) {
+      b = s_start[3 * w];
+      t = s_start[3 * w + 1];
+      left = s_start[3 * w + 2];
+    }
+    int n = left > 0 ? seq_len(p, b, false) : 0;  // keys of sequence b
+    int page = -1, at = -1;  // of this lane's block: -1 past the end, -2 no such page
+    auto place = [&]() {
+      const int blk = t * 8 + i;
+      page = at = -1;
+      if (left <= 0 || blk * 16 >= n) return;
+      const int q = blk / per_page;
+      at = blk - q * per_page;
+      page = cache.table != nullptr ? cache.table[static_cast<long long>(b) * cache.max_pages + q] : b;
+      if (page < 0 || page >= cache.n_pages) page = -2;
+    };
+    place();
+    int slot = w * C::SL, used = 0;  // the next ring slot, tiles issued
+    uint32_t par = 1;                // of the slot's release: the first round waits for none
+    unsigned long long since = 0;
+    while (__any_sync(0xffffffffu, left > 0)) {
+      bool go = false;
+      if (left > 0) {
+        uint32_t ok;
+        asm volatile(
+            "{\n.reg .pred p;\n"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+            "selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(free_(slot)), "r"(par)
+            : "memory");
+        go = ok != 0;
       }
-      return true;
-    });
-    if (*abort_flag) {
+      go = (__ballot_sync(0xffffffffu, go) >> (8 * w) & 1) != 0;  // a team's lanes go together
+      const bool here = go && page >= 0, gone = go && page == -2;
+      if (gone) atomicOr(p.status, kStatusInput);
+      const unsigned missing = __ballot_sync(0xffffffffu, gone) >> (8 * w) & 0xffu;
+      const unsigned have = __ballot_sync(0xffffffffu, here) >> (8 * w) & 0xffu;
+      const int before = __shfl_up_sync(0xffffffffu, page, 1);
+      const bool starts = here && (i == 0 || before != page || at == 0);
+      const unsigned heads = __ballot_sync(0xffffffffu, starts) >> (8 * w) & 0xffu;
+      if (go && i == 0) {
+        s_missing[slot] = static_cast<int>(missing);
+        mbar_arrive_expect_tx(full(slot), __popc(have) * 18 * D);
+      }
+      __syncwarp();
+      if (starts) {
+        const unsigned ends = (heads | ~have) & (0xfffffffeu << i);  // never empty: bit 8 of ~have is set
+        const int run = __ffs(ends) - 1 - i;
+        const long long src = ((static_cast<long long>(page) * cache.Hkv + head) * per_page + at) * (18 * D);
+        bulk_load(sRing + slot * C::TILE + i * 18 * D, cache.cache + src, run * 18 * D, full(slot));
+      }
+      if (go) {
+        --left;
+        ++used;
+        if (++slot == (w + 1) * C::SL) {
+          slot = w * C::SL;
+          par ^= 1;
+        }
+        if (++t * BC >= n) {  // the next sequence with keys
+          t = 0;
+          n = 0;
+          while (left > 0 && b + 1 < plan.n_seq && n == 0) n = seq_len(p, ++b, false);
+        }
+        place();
+      }
+      __syncwarp();
+      if (__any_sync(0xffffffffu, go)) {
+        since = 0;
+      } else if (since == 0) {
+        since = globaltimer_ns();
+      } else {
+        // no slot has been released: the wait is bounded like every other
+        const bool late = __any_sync(0xffffffffu, globaltimer_ns() - since > wc.limit_ns);
+        if (late) record_timeout(wc);
+        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) break;
+      }
+    }
+    if (*abort_flag && i == 0 && w < W) {
       // let copies already in flight land before the CTA's shared memory is
       // released; a wait for copies that were never issued just runs out
       WaitCtl drain{nullptr, nullptr, wc.limit_ns};
-      for (int k = max(0, g - SLOTS); k < g; ++k) mbar_wait(full(k % SLOTS), (k / SLOTS) & 1, drain);
+      for (int k = max(0, used - C::SL); k < used; ++k) mbar_wait(full(w * C::SL + k % C::SL), (k / C::SL) & 1, drain);
     }
     __syncwarp();
   } else if (warp == 8 * W) {
@@ -317,7 +327,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     // once its K is in place, O^T once its V^T and P are, whichever is ready.
     constexpr uint32_t idesc_s = idesc_f16(128, NR, 0), idesc_o = idesc_f16(128, NR, 1);
     const Desc2 dq = desc_sw128(sQ, 16, 1024), dp = desc_p<C::RB>(sb + C::OFF_P);
-    int left = 2 * n_tiles;
+    int left = 0;  // products to issue
+#pragma unroll
+    for (int w = 0; w < W; ++w) left += 2 * __shfl_sync(0xffffffffu, s_start[3 * w + 2], 0);
     uint32_t s_par = 0, o_par = 0;  // a bit a team: the phase it waits for next
     unsigned long long since = 0;
     while (left > 0) {
@@ -332,7 +344,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ts_w(tw + C::TM_S, tw + C::TM_K + 8 * kk, dq,
-                       (t * C::Q_BYTES + (kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, t > 0 || kk > 0);
+                       ((w * C::QT + t) * C::Q_BYTES + (kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, t > 0 || kk > 0);
           mma_commit_w(s_done(w));
           s_par ^= 1u << w;
           moved = true;
@@ -381,28 +393,30 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     const uint32_t sP = sb + C::OFF_P + w * C::PT * C::P_BYTES;
     const uint32_t sVS = sb + C::OFF_VS + (w * 4 + quarter) * 512;
     const int c0 = C::SPLIT && !keys ? NH : 0;  // this thread's columns: c0 .. c0 + NH - 1
-    float* ref = s_ref + w * NR;
-    float* fac = s_fac + w * NR;
-    float* red = s_red + w * 4 * NR;
+    int* lag = reinterpret_cast<int*>(smem + C::OFF_STAT + w * C::STATS);  // [NR]
+    float* cscale = reinterpret_cast<float*>(lag + NR);  // [NR] log2-domain scale of a column
+    float* ref = cscale + NR;                            // [NR] negated reference
+    float* fac = ref + NR;                               // [NR] alpha, then 1 / sum
+    float* red = fac + NR;                               // [4][NR] warps' column results
     constexpr int kRows = C::SPLIT ? 256 : 128;   // threads of a team with columns
     constexpr int RCOLS = NH > 32 ? NH / 32 : 1;  // columns that a lane owns after a reduction
     const int my_col = c0 + first_col<NH>();
     const int tid = threadIdx.x & 255;  // within the team
     auto rows_sync = [&]() { named_bar_sync(1 + w, kRows); };
-    auto all_sync = [&]() { named_bar_sync(8, kConsumers); };
-    // the team's tiles are w, w + W, ... of the CTA's: the next one, its ring slot, and that slot's phase
-    int g0 = 0, next_tile = w, mine = 0, slot = w;
+    int mine = 0, slot = w * C::SL;  // tiles so far, the next ring slot
     uint32_t phase = 0;
+    if (tid < NR) lag[tid] = p.n_new - 1 - (r0 + tid) % p.n_new;
 
-    // Q rows of a sequence: a warp takes rows warp, warp + 8 W, ...; a lane 4 channels of one
-    constexpr int QR = (NR + 8 * W - 1) / (8 * W);
+    // Q rows of a sequence: a warp with columns takes every QW-th; a lane 4 channels of one
+    constexpr int QW = kRows / 32, QR = (NA + QW - 1) / QW;
+    const int qwarp = warp & (QW - 1);
     using Four = typename std::conditional<F32, uint4, uint2>::type;
     Four qv[QR];
     auto load_q = [&](int b) {
       const long long row0 = (b * plan.heads + head) / p.group_div * p.q_s1 + (b * plan.heads + head) % p.group_div * p.q_s2 + r0;
 #pragma unroll
       for (int i = 0; i < QR; ++i) {
-        const int r = warp + 8 * W * i;
+        const int r = qwarp + QW * i;
         qv[i] = Four{};
         if (r < n_rows && 4 * lane < D)
           qv[i] = *reinterpret_cast<const Four*>(static_cast<const T*>(p.q) + (row0 + r) * D + 4 * lane);
@@ -411,8 +425,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     auto put_q = [&]() {
 #pragma unroll
       for (int i = 0; i < QR; ++i) {
-        const int r = warp + 8 * W * i;
-        if (r >= NR) break;
+        const int r = qwarp + QW * i;
+        if (r >= NA) break;
         float x[4];
         if constexpr (F32) {
           x[0] = __uint_as_float(qv[i].x), x[1] = __uint_as_float(qv[i].y);
@@ -431,7 +445,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
 #pragma unroll
         for (int y = 0; y < 4; ++y) x[y] *= f;
         const int ch = 4 * lane, c16 = (ch & 63) >> 3;
-        const uint32_t at = sQ + (ch >> 6) * NR * 128 + r * 128 + ((c16 ^ (r & 7)) << 4) + (ch & 4) * 2;
+        const uint32_t at = sQ + w * C::QT * C::Q_BYTES + (ch >> 6) * NR * 128 + r * 128 + ((c16 ^ (r & 7)) << 4) + (ch & 4) * 2;
 #pragma unroll
         for (int t = 0; t < C::QT; ++t) {
           const uint32_t lo = pack_f16x2(x[0], x[1]), hi = pack_f16x2(x[2], x[3]);
@@ -440,33 +454,38 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
           x[0] -= a.x, x[1] -= a.y, x[2] -= b.x, x[3] -= b.y;
         }
         if (lane == 0)
-          s_cs[r] = fmaxf(p.scale * cache.k_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - up) << 23),
+          cscale[r] = fmaxf(p.scale * cache.k_scale * 1.4426950408889634f * __uint_as_float(static_cast<uint32_t>(127 - up) << 23),
                           1.5e-45f);  // not 0, for the masked scores' sake
       }
       fence_proxy_async_smem();
     };
 
-    bool begun = false;
-    pieces([&](int b, int nk, int t0, int n, int next) -> bool {
+    int b = __shfl_sync(0xffffffffu, s_start[3 * w], 0), t0 = __shfl_sync(0xffffffffu, s_start[3 * w + 1], 0);
+    int left = __shfl_sync(0xffffffffu, s_start[3 * w + 2], 0);
+    int nk = left > 0 ? __shfl_sync(0xffffffffu, seq_len(p, b, false), 0) : 0;
+    if (rows && left > 0) load_q(b);
+    // a piece at a time: tiles t0 .. t0 + n - 1 of sequence b
+    while (left > 0) {
+      const int n = min(left, tiles_of<BC>(nk) - t0);
+      left -= n;
+      int next = b, next_nk = 0;  // the next sequence with keys
+      while (left > 0 && next + 1 < plan.n_seq && next_nk == 0) next_nk = __shfl_sync(0xffffffffu, seq_len(p, ++next, false), 0);
+      if (next_nk == 0) left = 0;
       const int group = b * plan.heads + head;
-      if (!begun) {
-        begun = true;
-        load_q(b);
-        put_q();
-        all_sync();
-      }
-      if (next >= 0) load_q(next);  // lands while this piece goes on
       float l[NH];
 #pragma unroll
       for (int c = 0; c < NH; ++c) l[c] = 0.f;
-      if (tid < NR) ref[tid] = kUnset;
-      if (rows) rows_sync();
-      bool any = false;  // this team has had a tile of the piece
-      for (; next_tile < g0 + n; next_tile += W) {
+      if (rows) {
+        put_q();  // every product with the last piece's Q has completed
+        if (left > 0) load_q(next);  // lands while this piece goes on
+        if (tid < NR) ref[tid] = kUnset;
+        rows_sync();
+      }
+      for (int i = 0; i < n; ++i) {
         warp_wait(full(slot), phase, wc);
         const uint32_t base = sRing + slot * C::TILE;
         const int missing = s_missing[slot];
-        const int j0 = (t0 + next_tile - g0) * BC, valid = min(BC, nk - j0);
+        const int j0 = (t0 + i) * BC, valid = min(BC, nk - j0);
         // (the other half has read the last tile's scores, which S^T is to replace)
         if (C::SPLIT && !keys && lane == 0) mbar_arrive(k_ready(w));
         if (keys) {
@@ -572,14 +591,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
             for (int c = 0; c < NH; ++c) x[c] = __uint_as_float(r[c]);
             if (edge) {
 #pragma unroll
-              for (int c = 0; c < NH; ++c) x[c] = s_lag[c0 + c] < room ? x[c] : -INFINITY;
+              for (int c = 0; c < NH; ++c) x[c] = lag[c0 + c] < room ? x[c] : -INFINITY;
             }
           };
           auto against = [&]() {
 #pragma unroll
             for (int c = 0; c < NH; c += 4) {
               const float4 nr = *reinterpret_cast<const float4*>(ref + c0 + c);
-              const float4 cs = *reinterpret_cast<const float4*>(s_cs + c0 + c);
+              const float4 cs = *reinterpret_cast<const float4*>(cscale + c0 + c);
               x[c] = fmaf(x[c], cs.x, nr.x);
               x[c + 1] = fmaf(x[c + 1], cs.y, nr.y);
               x[c + 2] = fmaf(x[c + 2], cs.z, nr.z);
@@ -599,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
             tc_fence_after();
             scores();
 #pragma unroll
-            for (int c = 0; c < NH; ++c) x[c] *= s_cs[c0 + c];
+            for (int c = 0; c < NH; ++c) x[c] *= cscale[c0 + c];
             reduce_step<NH / 2, 16>(x, [](float a, float b) { return fmaxf(a, b); });
 #pragma unroll
             for (int y = 0; y < RCOLS; ++y) red[quarter * NR + my_col + y] = x[y];
@@ -617,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
             rows_sync();
 #pragma unroll
             for (int c = 0; c < NH; ++c) l[c] *= fac[c0 + c];
-            if (any) {
+            if (i > 0) {
 #pragma unroll 1
               for (int c = c0; c < c0 + NH; c += 8) {
                 uint32_t o[8];
@@ -657,97 +676,69 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
               st_shared_v4(at + t * C::P_BYTES, pk[0], pk[1], pk[2], pk[3]);
             }
           }
-          if (tid == 0) s_first[w] = !any;
+          if (tid == 0) s_first[w] = i == 0;
           fence_proxy_async_smem();
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(p_ready(w));
         }
-        any = true;
         ++mine;
-        slot += W;
-        if (slot >= SLOTS) {
-          slot -= SLOTS;
+        if (++slot == (w + 1) * C::SL) {
+          slot = w * C::SL;
           phase ^= 1;
         }
       }
       // ------------------------------------------------------------ output
-      if (any) warp_wait(o_done(w), (mine - 1) & 1, wc);
-      tc_fence_after();
       if (rows) {
         reduce_step<NH / 2, 16>(l, [](float x, float y) { return x + y; });
+        rows_sync();  // the last tile's column results have been read
 #pragma unroll
         for (int x = 0; x < RCOLS; ++x) red[quarter * NR + my_col + x] = l[x];
         rows_sync();
-        if (tid < NA) s_sum[w * NR + tid] = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
-      }
-      g0 += n;
-      tc_fence_before();
-      all_sync();
-      tc_fence_after();
-      const bool whole = t0 == 0 && n == tiles_of<BC>(nk);
-      const long long part = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + cut + b;
-      const long long orow0 = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r0;
-      if (threadIdx.x < NA) {  // the teams' O share one reference: the largest
-        const int c = threadIdx.x;
-        float m = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int y = 0; y < W; ++y)
-          if (s_ref[y * NR + c] != kUnset) m = fmaxf(m, -s_ref[y * NR + c]);
-        float f[W];
-#pragma unroll
-        for (int y = 0; y < W; ++y) {
-          f[y] = s_ref[y * NR + c] == kUnset ? 0.f : ex2_approx(-s_ref[y * NR + c] - m);
-          sum += f[y] == 0.f ? 0.f : f[y] * s_sum[y * NR + c];
-        }
-        const float inv = sum == 0.f ? 0.f : cache.v_scale / sum;
-#pragma unroll
-        for (int y = 0; y < W; ++y) s_fac[y * NR + c] = f[y] * inv;
-        const float lse = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * 0.69314718055994531f;
-        if (c < n_rows && !*abort_flag) {
-          if (!whole)
-            p.part_lse[part * NR + c] = lse;
-          else if (p.lse != nullptr)
-            p.lse[orow0 + c] = lse;
-        }
-      }
-      if (next >= 0) put_q();  // every product with this piece's Q has completed
-      all_sync();
-#pragma unroll 1
-      for (int c = 8 * (warp >> 2); c < n_rows; c += 16 * W) {
-        float acc[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) acc[x] = 0.f;
-#pragma unroll
-        for (int y = 0; y < W; ++y) {
-          __syncwarp();
-          if (n < W && (g0 - 1 - y + W * (n + W)) % W >= n) continue;  // team y had no tile
-          uint32_t o[8];
-          tmem_ld_32x32b_x8(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + y * C::COLS + C::TM_O + c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float f = s_fac[y * NR + c + x];
-            if (f != 0.f) acc[x] = fmaf(__uint_as_float(o[x]), f, acc[x]);
+        const bool whole = t0 == 0 && n == tiles_of<BC>(nk);
+        const long long part = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + w * ctas + cta + b;
+        const long long orow0 = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r0;
+        if (tid < NA) {
+          const float sum = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
+          fac[tid] = sum == 0.f ? 0.f : cache.v_scale / sum;
+          const float lse = sum == 0.f ? -INFINITY : (__log2f(sum) - ref[tid]) * 0.69314718055994531f;  // no key seen: -inf
+          if (tid < n_rows && !*abort_flag) {
+            if (!whole)
+              p.part_lse[part * NR + tid] = lse;
+            else if (p.lse != nullptr)
+              p.lse[orow0 + tid] = lse;
           }
         }
-        if (id >= D || *abort_flag) continue;
+        warp_wait(o_done(w), (mine - 1) & 1, wc);
+        tc_fence_after();
+        rows_sync();
+#pragma unroll 1
+        for (int c = c0; c < min(c0 + NH, n_rows); c += 8) {
+          uint32_t o[8];
+          __syncwarp();
+          tmem_ld_32x32b_x8(tl + C::TM_O + c, o);
+          tmem_wait_ld();
+          if (id >= D || *abort_flag) continue;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          if (c + x >= n_rows) break;
-          if (!whole)
-            p.part_o[(part * NR + c + x) * D + id] = acc[x];
-          else if constexpr (F32)
-            static_cast<float*>(p.o)[(orow0 + c + x) * D + id] = acc[x];
-          else
-            static_cast<__nv_bfloat16*>(p.o)[(orow0 + c + x) * D + id] = __float2bfloat16_rn(acc[x]);
+          for (int x = 0; x < 8; ++x) {
+            if (c + x >= n_rows) break;
+            const float f = fac[c + x], y = f == 0.f ? 0.f : __uint_as_float(o[x]) * f;
+            if (!whole)
+              p.part_o[(part * NR + c + x) * D + id] = y;
+            else if constexpr (F32)
+              static_cast<float*>(p.o)[(orow0 + c + x) * D + id] = y;
+            else
+              static_cast<__nv_bfloat16*>(p.o)[(orow0 + c + x) * D + id] = __float2bfloat16_rn(y);
+          }
         }
+        __syncwarp();
+        tc_fence_before();
       }
-      tc_fence_before();
-      all_sync();  // statistics and accumulators are free for the next piece
-      return true;
-    });
+      b = next;
+      t0 = 0;
+      nk = next_nk;
+    }
   }
 
   tc_fence_before();
@@ -764,14 +755,16 @@ cudaError_t launch_nr(const SeqAttn& p, const Cache4& c, const DecodePlan& plan,
   static SmemOnce once;
   const cudaError_t e = once(fa_cache4_decode_kernel<D, NR, NA, F32>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(plan.heads) * plan.row_groups * plan.cuts;
+  const unsigned grid = static_cast<unsigned>(plan.heads) * plan.row_groups * (plan.cuts / C::W);
   fa_cache4_decode_kernel<D, NR, NA, F32><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(p, c, plan);
   return cudaGetLastError();
 }
 template <int D, bool F32>
 cudaError_t launch_d(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s) {
   if (w.nr == 16) return p.rows <= 8 ? launch_nr<D, 16, 8, F32>(p, c, w, s) : launch_nr<D, 16, 16, F32>(p, c, w, s);
-  return w.nr == 32 ? launch_nr<D, 32, 32, F32>(p, c, w, s) : launch_nr<D, 64, 64, F32>(p, c, w, s);
+  if constexpr (!F32)
+    if (w.nr == 64) return launch_nr<D, 64, 64, F32>(p, c, w, s);
+  return launch_nr<D, 32, 32, F32>(p, c, w, s);
 }
 template <bool F32>
 cudaError_t launch_type(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s) {
@@ -783,14 +776,24 @@ cudaError_t launch_type(const SeqAttn& p, const Cache4& c, const DecodePlan& w, 
 
 }  // namespace
 
-DecodePlan cache4_plan(int n_seq, int heads, int rows, int sms) {
+// Teams of a CTA.
+template <bool F32>
+static int teams(int d, int nr) {
+  if (nr == 16) return d == 64 ? Cfg<64, 16, 16, F32>::W : d == 96 ? Cfg<96, 16, 16, F32>::W : Cfg<128, 16, 16, F32>::W;
+  if (nr == 32) return d == 64 ? Cfg<64, 32, 32, F32>::W : d == 96 ? Cfg<96, 32, 32, F32>::W : Cfg<128, 32, 32, F32>::W;
+  return 2;
+}
+
+DecodePlan cache4_plan(int n_seq, int heads, int rows, int d, fa_dtype dt, int sms) {
   DecodePlan w{};
   w.n_seq = n_seq;
   w.heads = heads;
-  w.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  // float32: at most 32 rows, whose terms of Q and P leave the ring its room
+  w.nr = rows <= 16 ? 16 : rows <= 32 || dt == FA_DTYPE_F32 ? 32 : 64;
   w.row_groups = (rows + w.nr - 1) / w.nr;
   const long long groups = static_cast<long long>(heads) * w.row_groups;
-  w.cuts = groups < sms ? static_cast<int>(sms / groups) : 1;  // a CTA an SM
+  const int ctas = groups < sms ? static_cast<int>(sms / groups) : 1;  // a CTA an SM
+  w.cuts = ctas * (dt == FA_DTYPE_F32 ? teams<true>(d, w.nr) : teams<false>(d, w.nr));
   w.direct = 1;
   return w;
 }
