@@ -43,7 +43,6 @@ namespace {
 using namespace seq;
 
 constexpr int BC = 128;  // keys per tile
-constexpr float kUnset = 3e38f;  // negated reference of a row that has seen no key
 // A row's reference is 2^7 below the largest score when it was set, and rises
 // once a score is 2^8 above that: P is at most 2^15, and fp16's least step at
 // least 2^-32 of the largest P.
@@ -460,6 +459,46 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
       fence_proxy_async_smem();
     };
 
+    auto next_slot = [&]() {
+      if (++slot == (w + 1) * C::SL) {
+        slot = w * C::SL;
+        phase ^= 1;
+      }
+    };
+    // K of the next tile, a thread a key: S^T of the tile before must have read
+    // the last one, and this thread have its scores
+    auto unpack_k = [&]() {
+      warp_wait(full(slot), phase, wc);
+      const uint32_t t = id & 15, blk = sRing + slot * C::TILE + (id >> 4) * (18 * D);
+      const bool gone = (s_missing[slot] >> (id >> 4)) & 1;  // no page: zeros
+      const uint32_t sa = blk + 8 * D + t * GROUPS, ka = blk + t * 8;
+#pragma unroll
+      for (int c = 0; c < GROUPS; c += 2) {
+        const uint2 a = ld_shared_v2(ka + c * 128), e = ld_shared_v2(ka + (c + 1) * 128);
+        uint32_t sc[2];
+        cache4::scales_f16(gone ? 0u : ld_shared_u16(sa + c), sc);
+        const uint32_t s0 = __byte_perm(sc[0], 0, 0x1010), s1 = __byte_perm(sc[0], 0, 0x3232);
+        uint32_t o[16];
+        cache4::codes_f16(a.x, o);
+        cache4::codes_f16(a.y, o + 4);
+        cache4::codes_f16(e.x, o + 8);
+        cache4::codes_f16(e.y, o + 12);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          o[x] = cache4::mul_f16x2(o[x], s0);
+          o[8 + x] = cache4::mul_f16x2(o[8 + x], s1);
+        }
+        tmem_st_32x32b_x16(tl + C::TM_K + 8 * c, o);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(k_ready(w));
+        mbar_arrive(free_(slot));
+      }
+      next_slot();
+    };
     int b = __shfl_sync(0xffffffffu, s_start[3 * w], 0), t0 = __shfl_sync(0xffffffffu, s_start[3 * w + 1], 0);
     int left = __shfl_sync(0xffffffffu, s_start[3 * w + 2], 0);
     int nk = left > 0 ? __shfl_sync(0xffffffffu, seq_len(p, b, false), 0) : 0;
@@ -478,51 +517,24 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
       if (rows) {
         put_q();  // every product with the last piece's Q has completed
         if (left > 0) load_q(next);  // lands while this piece goes on
-        if (tid < NR) ref[tid] = kUnset;
+        if (tid < NR) ref[tid] = 0.f;  // set by the piece's first tile
         rows_sync();
+        if (keys)
+          unpack_k();
+        else if (lane == 0)
+          mbar_arrive(k_ready(w));  // (split: this half has read the last scores, and its rows of Q are in place)
       }
       for (int i = 0; i < n; ++i) {
-        warp_wait(full(slot), phase, wc);
-        const uint32_t base = sRing + slot * C::TILE;
-        const int missing = s_missing[slot];
-        const int j0 = (t0 + i) * BC, valid = min(BC, nk - j0);
-        // (the other half has read the last tile's scores, which S^T is to replace)
-        if (C::SPLIT && !keys && lane == 0) mbar_arrive(k_ready(w));
+        const int j0 = (t0 + i) * BC;
         if (keys) {
-          // ---- K: a thread a key
-          const uint32_t t = id & 15, blk = base + (id >> 4) * (18 * D);
-          const bool gone = (missing >> (id >> 4)) & 1;  // no page: zeros
-          const uint32_t sa = blk + 8 * D + t * GROUPS, ka = blk + t * 8;
-#pragma unroll
-          for (int c = 0; c < GROUPS; c += 2) {
-            const uint2 a = ld_shared_v2(ka + c * 128), e = ld_shared_v2(ka + (c + 1) * 128);
-            uint32_t sc[2];
-            cache4::scales_f16(gone ? 0u : ld_shared_u16(sa + c), sc);
-            const uint32_t s0 = __byte_perm(sc[0], 0, 0x1010), s1 = __byte_perm(sc[0], 0, 0x3232);
-            uint32_t o[16];
-            cache4::codes_f16(a.x, o);
-            cache4::codes_f16(a.y, o + 4);
-            cache4::codes_f16(e.x, o + 8);
-            cache4::codes_f16(e.y, o + 12);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              o[x] = cache4::mul_f16x2(o[x], s0);
-              o[8 + x] = cache4::mul_f16x2(o[8 + x], s1);
-            }
-            tmem_st_32x32b_x16(tl + C::TM_K + 8 * c, o);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(k_ready(w));
-            mbar_arrive(free_(slot));
-          }
         } else if (quarter * 32 >= D) {
           if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);  // arrive for this tile, not for the last one
         } else {
           // ---- V: a thread a channel.  First the scales of the warp's two groups,
           // zeros past the sequence's end and in missing pages.
+          warp_wait(full(slot), phase, wc);
+          const uint32_t base = sRing + slot * C::TILE;
+          const int missing = s_missing[slot], valid = min(BC, nk - j0);
           {
             const int k = (lane & 15) >> 1, t = (lane & 1) * 8;  // block, first of eight keys
             uint32_t sc[4];
@@ -575,67 +587,76 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
             mbar_arrive(free_(slot));
             if (!C::SPLIT) mbar_arrive(p_ready(w));
           }
+          next_slot();
         }
         if (rows) {
           // ---- scores, in the log2 domain and against the row's reference
           warp_wait(s_done(w), mine & 1, wc);
           tc_fence_after();
-          const bool edge = j0 + BC > nk - (p.n_new - 1);  // some row does not see the whole tile
-          const int room = nk - (j0 + id);                 // > lag: the row sees this key
           float x[NH];
-          auto scores = [&]() {
+          {
             uint32_t r[NH];
             tmem_ld<NH>(tl + C::TM_S + c0, r);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < NH; ++c) x[c] = __uint_as_float(r[c]);
-            if (edge) {
-#pragma unroll
-              for (int c = 0; c < NH; ++c) x[c] = lag[c0 + c] < room ? x[c] : -INFINITY;
+          }
+          if (i + 1 < n) {  // the next tile's S^T goes on while this one's scores are dealt with
+            if (keys) {
+              unpack_k();
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(k_ready(w));
             }
-          };
-          auto against = [&]() {
+          }
+          if (j0 + BC > nk - (p.n_new - 1)) {  // some row does not see the whole tile
+            const int room = nk - (j0 + id);   // > lag: the row sees this key
 #pragma unroll
-            for (int c = 0; c < NH; c += 4) {
-              const float4 nr = *reinterpret_cast<const float4*>(ref + c0 + c);
-              const float4 cs = *reinterpret_cast<const float4*>(cscale + c0 + c);
-              x[c] = fmaf(x[c], cs.x, nr.x);
-              x[c + 1] = fmaf(x[c + 1], cs.y, nr.y);
-              x[c + 2] = fmaf(x[c + 2], cs.z, nr.z);
-              x[c + 3] = fmaf(x[c + 3], cs.w, nr.w);
-            }
-          };
-          scores();
-          against();
+            for (int c = 0; c < NH; ++c) x[c] = lag[c0 + c] < room ? x[c] : -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < NH; c += 4) {
+            const float4 nr = *reinterpret_cast<const float4*>(ref + c0 + c);
+            const float4 cs = *reinterpret_cast<const float4*>(cscale + c0 + c);
+            x[c] = fmaf(x[c], cs.x, nr.x);
+            x[c + 1] = fmaf(x[c + 1], cs.y, nr.y);
+            x[c + 2] = fmaf(x[c + 2], cs.z, nr.z);
+            x[c + 3] = fmaf(x[c + 3], cs.w, nr.w);
+          }
           float over = -INFINITY;
 #pragma unroll
           for (int c = 0; c < NH; c += 2) over = fmax3(over, x[c], x[c + 1]);
-          const bool rises = bar_any(1 + w, kRows, over > kRescaleThreshold);
+          const bool rises = bar_any(1 + w, kRows, i == 0 || over > kRescaleThreshold);
           // the last product of this team has read P (and O is complete)
           if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);
           if (rises) {
-            // some row's reference rises: column maxima over the 128 keys
+            // the piece's first tile sets the references (a row that sees any key of
+            // the piece sees its first one), in others some rise: column maxima over
+            // the 128 keys
             tc_fence_after();
-            scores();
+            {
+              float v[NH];
 #pragma unroll
-            for (int c = 0; c < NH; ++c) x[c] *= cscale[c0 + c];
-            reduce_step<NH / 2, 16>(x, [](float a, float b) { return fmaxf(a, b); });
+              for (int c = 0; c < NH; ++c) v[c] = x[c];
+              reduce_step<NH / 2, 16>(v, [](float a, float b) { return fmaxf(a, b); });
 #pragma unroll
-            for (int y = 0; y < RCOLS; ++y) red[quarter * NR + my_col + y] = x[y];
+              for (int y = 0; y < RCOLS; ++y) red[quarter * NR + my_col + y] = v[y];
+            }
             rows_sync();
             if (tid < NA) {
               const float mx = fmaxf(fmaxf(red[tid], red[NR + tid]), fmaxf(red[2 * NR + tid], red[3 * NR + tid]));
-              const float old = ref[tid];
-              float alpha = 1.f;
-              if (mx + old > kRescaleThreshold) {  // old = kUnset: the first key that the row sees
-                alpha = old == kUnset ? 0.f : ex2_approx(kBelow - old - mx);
-                ref[tid] = kBelow - mx;
-              }
-              fac[tid] = alpha;
+              const bool up = i == 0 ? mx != -INFINITY : mx > kRescaleThreshold;
+              fac[tid] = up ? kBelow - mx : 0.f;  // what the column's scores, and the logarithms of P and O, change by
+              ref[tid] += fac[tid];
             }
             rows_sync();
 #pragma unroll
-            for (int c = 0; c < NH; ++c) l[c] *= fac[c0 + c];
+            for (int c = 0; c < NH; ++c) {
+              const float f = fac[c0 + c];
+              x[c] += f;
+              l[c] *= ex2_approx(fminf(f, 0.f));  // (the first tile finds zeros)
+            }
             if (i > 0) {
 #pragma unroll 1
               for (int c = c0; c < c0 + NH; c += 8) {
@@ -643,12 +664,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
                 tmem_ld_32x32b_x8(tl + C::TM_O + c, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * fac[c + y]);
+                for (int y = 0; y < 8; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * ex2_approx(fac[c + y]));
                 tmem_st_32x32b_x8(tl + C::TM_O + c, o);
               }
             }
-            scores();
-            against();
           }
           // ---- P
 #pragma unroll
@@ -684,10 +703,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
           if (lane == 0) mbar_arrive(p_ready(w));
         }
         ++mine;
-        if (++slot == (w + 1) * C::SL) {
-          slot = w * C::SL;
-          phase ^= 1;
-        }
       }
       // ------------------------------------------------------------ output
       if (rows) {
