@@ -329,15 +329,28 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     int left = 0;  // products to issue
 #pragma unroll
     for (int w = 0; w < W; ++w) left += 2 * __shfl_sync(0xffffffffu, s_start[3 * w + 2], 0);
-    uint32_t s_par = 0, o_par = 0;  // a bit a team: the phase it waits for next
+    // lane l < W looks for K of team l, lane W + l for its P
+    const uint32_t my_bar = lane < W ? k_ready(lane) : p_ready(lane < 2 * W ? lane - W : 0);
+    uint32_t par = 0;
     unsigned long long since = 0;
     while (left > 0) {
-      bool moved = false;
+      uint32_t ok;
+      asm volatile(
+          "{\n.reg .pred p;\n"
+          "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+          "selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(ok)
+          : "r"(my_bar), "r"(par)
+          : "memory");
+      const unsigned ready = __ballot_sync(0xffffffffu, lane < 2 * W && ok != 0);
+      const bool moved = ready != 0;
+      if (ready >> lane & 1) par ^= 1;
+      left -= __popc(ready);
+      if (moved) tc_fence_after();
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         const uint32_t tw = tmem + w * C::COLS;
-        if (warp_test(k_ready(w), (s_par >> w) & 1)) {
-          tc_fence_after();
+        if (ready >> w & 1) {
 #pragma unroll
           for (int t = 0; t < C::QT; ++t)
 #pragma unroll
@@ -345,12 +358,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
               mma_ts_w(tw + C::TM_S, tw + C::TM_K + 8 * kk, dq,
                        ((w * C::QT + t) * C::Q_BYTES + (kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, t > 0 || kk > 0);
           mma_commit_w(s_done(w));
-          s_par ^= 1u << w;
-          moved = true;
-          --left;
         }
-        if (warp_test(p_ready(w), (o_par >> w) & 1)) {
-          tc_fence_after();
+        if (ready >> (W + w) & 1) {
           const uint32_t more = s_first[w] == 0;
 #pragma unroll
           for (int t = 0; t < C::PT; ++t)
@@ -359,9 +368,6 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
               mma_ts_w(tw + C::TM_O, tw + C::TM_V + 8 * kk, dp,
                        ((w * C::PT + t) * C::P_BYTES + kk * 16 * C::RB) >> 4, idesc_o, t > 0 || kk > 0 ? 1u : more);
           mma_commit_w(o_done(w));
-          o_par ^= 1u << w;
-          moved = true;
-          --left;
         }
       }
       if (moved) {
@@ -472,17 +478,22 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
       const uint32_t t = id & 15, blk = sRing + slot * C::TILE + (id >> 4) * (18 * D);
       const bool gone = (s_missing[slot] >> (id >> 4)) & 1;  // no page: zeros
       const uint32_t sa = blk + 8 * D + t * GROUPS, ka = blk + t * 8;
+      uint2 code[GROUPS];
+      uint32_t s2[GROUPS / 2];
+#pragma unroll
+      for (int c = 0; c < GROUPS / 2; ++c) s2[c] = gone ? 0u : ld_shared_u16(sa + 2 * c);
+#pragma unroll
+      for (int c = 0; c < GROUPS; ++c) code[c] = ld_shared_v2(ka + c * 128);
 #pragma unroll
       for (int c = 0; c < GROUPS; c += 2) {
-        const uint2 a = ld_shared_v2(ka + c * 128), e = ld_shared_v2(ka + (c + 1) * 128);
         uint32_t sc[2];
-        cache4::scales_f16(gone ? 0u : ld_shared_u16(sa + c), sc);
+        cache4::scales_f16(s2[c / 2], sc);
         const uint32_t s0 = __byte_perm(sc[0], 0, 0x1010), s1 = __byte_perm(sc[0], 0, 0x3232);
         uint32_t o[16];
-        cache4::codes_f16(a.x, o);
-        cache4::codes_f16(a.y, o + 4);
-        cache4::codes_f16(e.x, o + 8);
-        cache4::codes_f16(e.y, o + 12);
+        cache4::codes_f16(code[c].x, o);
+        cache4::codes_f16(code[c].y, o + 4);
+        cache4::codes_f16(code[c + 1].x, o + 8);
+        cache4::codes_f16(code[c + 1].y, o + 12);
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           o[x] = cache4::mul_f16x2(o[x], s0);
@@ -549,22 +560,24 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
             }
             st_shared_v4(sVS + lane * 16, sc[0], sc[1], sc[2], sc[3]);
           }
+          const uint32_t cb = base + 9 * D + id * 8, cs = sVS + (lane >> 4) * 256;
+          uint2 code[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) code[k] = ld_shared_v2(cb + k * 18 * D);
           __syncwarp();
           // the last product of this team has read V^T
           if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);
           tc_fence_after();
-          const uint32_t cb = base + 9 * D + id * 8, cs = sVS + (lane >> 4) * 256;
+          uint4 sa = ld_shared_v4(cs), se = ld_shared_v4(cs + 16);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             uint32_t o[16];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int k = 2 * x + h;
-              const uint2 a = ld_shared_v2(cb + k * 18 * D);
-              const uint4 sa = ld_shared_v4(cs + k * 32), se = ld_shared_v4(cs + k * 32 + 16);
               uint32_t* y = o + 8 * h;
-              cache4::codes_f16(a.x, y);
-              cache4::codes_f16(a.y, y + 4);
+              cache4::codes_f16(code[k].x, y);
+              cache4::codes_f16(code[k].y, y + 4);
               y[0] = cache4::mul_f16x2(y[0], sa.x);
               y[1] = cache4::mul_f16x2(y[1], sa.y);
               y[2] = cache4::mul_f16x2(y[2], sa.z);
@@ -573,6 +586,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
               y[5] = cache4::mul_f16x2(y[5], se.y);
               y[6] = cache4::mul_f16x2(y[6], se.z);
               y[7] = cache4::mul_f16x2(y[7], se.w);
+              if (k < 7) {
+                sa = ld_shared_v4(cs + (k + 1) * 32);
+                se = ld_shared_v4(cs + (k + 1) * 32 + 16);
+              }
             }
             tmem_st_32x32b_x16(tl + C::TM_V + 16 * x, o);
           }
