@@ -173,6 +173,10 @@ ATTENDS = [
     ("bf16", 1, 8, 8, 1, 64, 128, [30001], 2),                      # one long sequence
     ("bf16", 40, 4, 1, 1, 16, 64, [7 * i % 331 for i in range(40)], 1),  # many pieces a CTA
     ("bf16", 33, 8, 8, 2, 32, 96, [(19 * i + 3) % 401 for i in range(33)], 1),
+    ("bf16", 150, 8, 1, 4, 16, 128, [(37 * i + 5) % 700 for i in range(150)], 1),   # 32 rows, several sequences a CTA
+    ("bf16", 150, 4, 1, 12, 16, 64, [(41 * i + 9) % 700 for i in range(150)], 1),   # 48 rows
+    ("f32", 150, 8, 1, 4, 32, 96, [(43 * i + 2) % 600 for i in range(150)], 1),
+    ("f32", 150, 4, 1, 1, 32, 128, [(43 * i + 2) % 600 for i in range(150)], 1),
     ("bf16", 3, 6, 2, 2, 16, 80, [5, 90, 200], 1),                  # widths without a tensor-core form
     ("bf16", 2, 4, 2, 1, 32, 256, [65, 400], 1),
     ("bf16", 2, 3, 3, 5, 16, 16, [4, 100], 1),
