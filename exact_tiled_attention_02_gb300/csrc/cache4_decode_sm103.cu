@@ -139,18 +139,46 @@ __device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
-  uint32_t v;
-  asm volatile("{\n.reg .u16 t;\nld.shared.u16 t, [%1];\ncvt.u32.u16 %0, t;\n}" : "=r"(v) : "r"(addr) : "memory");
+// The N scales (4, 6 or 8) of a key, the first in the lowest byte.
+template <int N>
+__device__ __forceinline__ uint2 ld_scales(uint32_t addr) {
+  uint2 v = make_uint2(0, 0);
+  if constexpr (N == 8) {
+    v = ld_shared_v2(addr);
+  } else if constexpr (N == 4) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v.x) : "r"(addr) : "memory");
+  } else {
+    asm volatile("{\n.reg .b16 a, b, c;\nld.shared.b16 a, [%2];\nld.shared.b16 b, [%2+2];\nld.shared.b16 c, [%2+4];\n"
+                 "mov.b32 %0, {a, b};\ncvt.u32.u16 %1, c;\n}"
+                 : "=r"(v.x), "=r"(v.y)
+                 : "r"(addr)
+                 : "memory");
+  }
   return v;
 }
 __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
+__device__ __forceinline__ void tmem_ld_x4(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
+}
+
+// A whole warp's wait.  The first try is where the warp goes on at once; what
+// follows is kept out of line, and out of the instruction cache.
+__device__ __noinline__ void wait_longer(uint32_t bar, uint32_t parity, unsigned int* status, volatile int* abort_flag,
+                                         unsigned long long limit_ns) {
+  mbar_wait(bar, parity, WaitCtl{status, abort_flag, limit_ns});
+}
+__device__ __forceinline__ void wait_for(uint32_t bar, uint32_t parity, const WaitCtl& w) {
+  if (!mbar_try_wait(bar, parity)) wait_longer(bar, parity, w.status, w.abort_flag, w.limit_ns);
+  __syncwarp();
 }
 
 template <int D, int NR, int NA, bool F32>
@@ -474,21 +502,21 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     // K of the next tile, a thread a key: S^T of the tile before must have read
     // the last one, and this thread have its scores
     auto unpack_k = [&]() {
-      warp_wait(full(slot), phase, wc);
+      wait_for(full(slot), phase, wc);
       const uint32_t t = id & 15, blk = sRing + slot * C::TILE + (id >> 4) * (18 * D);
       const bool gone = (s_missing[slot] >> (id >> 4)) & 1;  // no page: zeros
       const uint32_t sa = blk + 8 * D + t * GROUPS, ka = blk + t * 8;
       uint2 code[GROUPS];
-      uint32_t s2[GROUPS / 2];
-#pragma unroll
-      for (int c = 0; c < GROUPS / 2; ++c) s2[c] = gone ? 0u : ld_shared_u16(sa + 2 * c);
+      uint2 s8 = ld_scales<GROUPS>(sa);
+      if (gone) s8 = make_uint2(0, 0);
 #pragma unroll
       for (int c = 0; c < GROUPS; ++c) code[c] = ld_shared_v2(ka + c * 128);
+      uint32_t sc[4];
+      cache4::scales_f16(s8.x, sc);
+      if (GROUPS > 4) cache4::scales_f16(s8.y, sc + 2);
 #pragma unroll
       for (int c = 0; c < GROUPS; c += 2) {
-        uint32_t sc[2];
-        cache4::scales_f16(s2[c / 2], sc);
-        const uint32_t s0 = __byte_perm(sc[0], 0, 0x1010), s1 = __byte_perm(sc[0], 0, 0x3232);
+        const uint32_t s0 = __byte_perm(sc[c / 2], 0, 0x1010), s1 = __byte_perm(sc[c / 2], 0, 0x3232);
         uint32_t o[16];
         cache4::codes_f16(code[c].x, o);
         cache4::codes_f16(code[c].y, o + 4);
@@ -522,6 +550,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
       while (left > 0 && next + 1 < plan.n_seq && next_nk == 0) next_nk = __shfl_sync(0xffffffffu, seq_len(p, ++next, false), 0);
       if (next_nk == 0) left = 0;
       const int group = b * plan.heads + head;
+      const int all_seen = nk - (p.n_new - 1);  // keys that every row sees
       float l[NH];
 #pragma unroll
       for (int c = 0; c < NH; ++c) l[c] = 0.f;
@@ -539,11 +568,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         const int j0 = (t0 + i) * BC;
         if (keys) {
         } else if (quarter * 32 >= D) {
-          if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);  // arrive for this tile, not for the last one
+          if (mine > 0) wait_for(o_done(w), (mine - 1) & 1, wc);  // arrive for this tile, not for the last one
         } else {
           // ---- V: a thread a channel.  First the scales of the warp's two groups,
           // zeros past the sequence's end and in missing pages.
-          warp_wait(full(slot), phase, wc);
+          wait_for(full(slot), phase, wc);
           const uint32_t base = sRing + slot * C::TILE;
           const int missing = s_missing[slot], valid = min(BC, nk - j0);
           {
@@ -566,7 +595,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
           for (int k = 0; k < 8; ++k) code[k] = ld_shared_v2(cb + k * 18 * D);
           __syncwarp();
           // the last product of this team has read V^T
-          if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);
+          if (mine > 0) wait_for(o_done(w), (mine - 1) & 1, wc);
           tc_fence_after();
           uint4 sa = ld_shared_v4(cs), se = ld_shared_v4(cs + 16);
 #pragma unroll
@@ -608,12 +637,15 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         }
         if (rows) {
           // ---- scores, in the log2 domain and against the row's reference
-          warp_wait(s_done(w), mine & 1, wc);
+          wait_for(s_done(w), mine & 1, wc);
           tc_fence_after();
           float x[NH];
           {
             uint32_t r[NH];
-            tmem_ld<NH>(tl + C::TM_S + c0, r);
+            if constexpr (NH == 4)
+              tmem_ld_x4(tl + C::TM_S, r);
+            else
+              tmem_ld<NH>(tl + C::TM_S + c0, r);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < NH; ++c) x[c] = __uint_as_float(r[c]);
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
               if (lane == 0) mbar_arrive(k_ready(w));
             }
           }
-          if (j0 + BC > nk - (p.n_new - 1)) {  // some row does not see the whole tile
+          if (j0 + BC > all_seen) {  // some row does not see the whole tile
             const int room = nk - (j0 + id);   // > lag: the row sees this key
 #pragma unroll
             for (int c = 0; c < NH; ++c) x[c] = lag[c0 + c] < room ? x[c] : -INFINITY;
@@ -644,9 +676,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
           float over = -INFINITY;
 #pragma unroll
           for (int c = 0; c < NH; c += 2) over = fmax3(over, x[c], x[c + 1]);
+          const bool o_ready = mine == 0 || mbar_try_wait(o_done(w), (mine - 1) & 1);  // (asked ahead of the barrier)
           const bool rises = bar_any(1 + w, kRows, i == 0 || over > kRescaleThreshold);
           // the last product of this team has read P (and O is complete)
-          if (mine > 0) warp_wait(o_done(w), (mine - 1) & 1, wc);
+          if (!o_ready) wait_longer(o_done(w), (mine - 1) & 1, wc.status, wc.abort_flag, wc.limit_ns);
+          __syncwarp();
           if (rises) {
             // the piece's first tile sets the references (a row that sees any key of
             // the piece sees its first one), in others some rise: column maxima over
@@ -687,10 +721,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
             }
           }
           // ---- P
+          constexpr int PW = NH < 8 ? NH : 8;  // columns of a store
 #pragma unroll
-          for (int c = 0; c < NH; c += 8) {
+          for (int c = 0; c < NH; c += PW) {
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
+            for (int y = 0; y < PW; ++y) {
               x[c + y] = ex2_approx(x[c + y]);
               l[c + y] += x[c + y];
             }
@@ -699,9 +734,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
             const uint32_t at = sP + id * C::RB + p_chunk<C::RB>(id, (c0 + c) / 8) * 16;
 #pragma unroll
             for (int t = 0; t < C::PT; ++t) {
-              uint32_t pk[4];
+              uint32_t pk[PW / 2];
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
+              for (int y = 0; y < PW / 2; ++y) {
                 pk[y] = pack_f16x2(x[c + 2 * y], x[c + 2 * y + 1]);
                 if (t + 1 < C::PT) {
                   const float2 h = cache4::floats(pk[y]);
@@ -709,7 +744,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
                   x[c + 2 * y + 1] -= h.y;
                 }
               }
-              st_shared_v4(at + t * C::P_BYTES, pk[0], pk[1], pk[2], pk[3]);
+              if constexpr (PW == 8)
+                st_shared_v4(at + t * C::P_BYTES, pk[0], pk[1], pk[2], pk[3]);
+              else
+                st_shared_v2(at + t * C::P_BYTES, pk[0], pk[1]);
             }
           }
           if (tid == 0) s_first[w] = i == 0;
@@ -742,7 +780,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
               p.lse[orow0 + tid] = lse;
           }
         }
-        warp_wait(o_done(w), (mine - 1) & 1, wc);
+        wait_for(o_done(w), (mine - 1) & 1, wc);
         tc_fence_after();
         rows_sync();
 #pragma unroll 1
@@ -793,7 +831,10 @@ cudaError_t launch_nr(const SeqAttn& p, const Cache4& c, const DecodePlan& plan,
 }
 template <int D, bool F32>
 cudaError_t launch_d(const SeqAttn& p, const Cache4& c, const DecodePlan& w, cudaStream_t s) {
-  if (w.nr == 16) return p.rows <= 8 ? launch_nr<D, 16, 8, F32>(p, c, w, s) : launch_nr<D, 16, 16, F32>(p, c, w, s);
+  if (w.nr == 16) {
+    if (p.rows <= 4) return launch_nr<D, 16, 4, F32>(p, c, w, s);
+    return p.rows <= 8 ? launch_nr<D, 16, 8, F32>(p, c, w, s) : launch_nr<D, 16, 16, F32>(p, c, w, s);
+  }
   if constexpr (!F32)
     if (w.nr == 64) return launch_nr<D, 64, 64, F32>(p, c, w, s);
   return launch_nr<D, 32, 32, F32>(p, c, w, s);
