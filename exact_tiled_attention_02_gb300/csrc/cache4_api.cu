@@ -46,7 +46,8 @@ bool attn_sizes_ok(int B, int Hq, int Hkv, int Nq, int page_size, int max_pages,
   const long long keys = paged_keys(page_size, max_pages);
   return sizes_ok(B, Hq, Nq, d) && sizes_ok(B, max_pages) && keys > 0 &&
          static_cast<long long>(B) * Hq * Nq <= 0x7fffffffLL / 8 &&
-         B * ((keys + 127) / 128) * 457 <= 0x7fffffffLL;  // tiles of 128 times the most ranges they are cut into
+         tiles_ok(B, keys) &&  // and a CTA's tiles of 128, at least 304 ranges sharing those of all groups of rows
+         B * ((keys + 127) / 128) * Hkv / 304 < 0x7fffffffLL / ((static_cast<long long>(Hq / Hkv) * Nq + 15) / 16);
 }
 PartLayout attn_layout(int B, int Hq, int Hkv, int Nq, int n_keys, int d) {
   return part_layout(cache4_simt_splits(B, Hq, Hkv, Nq, n_keys, d), 0, static_cast<long long>(B) * Hq * Nq, d);
@@ -57,7 +58,8 @@ DecodePlan attn_plan(int B, int Hq, int Hkv, int Nq, int d, fa_dtype dt) {
   return cache4_plan(B, Hkv, Hq / Hkv * Nq, d, dt, 152);
 }
 PartLayout attn_layout_tc(const DecodePlan& plan, int d) {
-  return part_layout(1, 0, static_cast<long long>(decode_slots(plan)), d);
+  const long long pieces = static_cast<long long>(plan.heads) * plan.row_groups * plan.n_seq + plan.cuts;
+  return part_layout(1, 0, pieces * plan.nr, d);
 }
 
 }  // namespace

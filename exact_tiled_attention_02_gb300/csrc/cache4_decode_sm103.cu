@@ -83,7 +83,7 @@ struct Cfg {
   static constexpr int NBAR = 2 * SLOTS + 4 * W + 1;
   // tensor memory base, abort flag; teams' first sequence, its first tile, their tiles; first-tile flags; slots' missing blocks
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM_USED = OFF_MISC + 8 + W * 16 + SLOTS * 4;
+  static constexpr int SMEM_USED = OFF_MISC + 8 + W * 28 + SLOTS * 4;
   static constexpr int SMEM_BYTES = SMEM_USED + 1024;
   static constexpr int TM_K = 0, TM_V = KC, TM_S = KC + 64, TM_O = TM_S + NR;
   static_assert(W >= 2 && W <= 4 && SL >= 2, "two tiles a team in flight, eight lanes a team");
@@ -209,19 +209,13 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
   const uint32_t drain_bar = bars + 8 * (2 * SLOTS + 4 * W);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
-  int* s_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);    // [W][3] first sequence, its first tile, tiles of a team
-  volatile int* s_first = reinterpret_cast<volatile int*>(s_start + 3 * W);  // [W] a team's tile is its first of a piece
+  int* s_start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);    // [W][6] a team's first head, row group, sequence and tile, its tiles, range
+  volatile int* s_first = reinterpret_cast<volatile int*>(s_start + 6 * W);  // [W] a team's tile is its first of a piece
   volatile int* s_missing = s_first + W;                                     // [SLOTS] blocks without a page
   const WaitCtl wc{p.status, abort_flag, p.wait_ns};
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
 
-  // this CTA: rows r0 .. of head `head` of every sequence (group b * heads + head);
-  // team w takes range w * ctas + cta of plan.cuts, so that few ranges spread over the SMs
-  const int ctas = plan.cuts / W;
-  const int grp = blockIdx.x / ctas, cta = blockIdx.x % ctas;
-  const int head = grp / plan.row_groups, r0 = (grp % plan.row_groups) * NR;
-  const int n_rows = min(NR, p.rows - r0);
-
+  // A group of rows is rows NR rg .. of key/value head `head`.
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(full(s), 1);
@@ -243,12 +237,16 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     tmem_relinquish();
   }
   if (warp < 8 * W && (warp & 7) == 0) {
-    int b0, first, count;
-    find_range<BC>(p, plan, (warp >> 3) * ctas + cta, b0, first, count);
+    int r, grp, b0, first, count;
+    find_flat<BC>(p, plan, warp >> 3, W, r, grp, b0, first, count);
     if (lane == 0) {
-      s_start[3 * (warp >> 3)] = b0;
-      s_start[3 * (warp >> 3) + 1] = first;
-      s_start[3 * (warp >> 3) + 2] = count;
+      int* at = s_start + 6 * (warp >> 3);
+      at[0] = grp / plan.row_groups;
+      at[1] = grp % plan.row_groups;
+      at[2] = b0;
+      at[3] = first;
+      at[4] = count;
+      at[5] = r;
     }
   }
   tc_fence_before();
@@ -256,17 +254,36 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
+  // Steps to the next sequence with keys, of the next group of rows past the
+  // last one; its keys.
+  auto next_seq = [&](int& head, int& rg, int& b) -> int {
+    for (int i = 0; i < plan.n_seq; ++i) {
+      if (++b == plan.n_seq) {
+        b = 0;
+        if (++rg == plan.row_groups) {
+          rg = 0;
+          ++head;
+        }
+      }
+      const int n = seq_len(p, b, false);
+      if (n > 0) return n;
+    }
+    return 0;
+  };
+
   if (warp == 8 * W + 1) {
     // ---------------------------------------------------------------- loads
     // Eight lanes a team walk its tiles, a block a lane; the first lane of every
     // run of blocks that lie side by side in a page copies the run.
     const int w = lane >> 3, i = lane & 7;
     const int per_page = cache.page_size / 16;
-    int b = 0, t = 0, left = 0;  // the next tile's sequence and place there, tiles to go
+    int head = 0, rg = 0, b = 0, t = 0, left = 0;  // the next tile's head, row group, sequence and place there; tiles to go
     if (w < W) {
-      b = s_start[3 * w];
-      t = s_start[3 * w + 1];
-      left = s_start[3 * w + 2];
+      head = s_start[6 * w];
+      rg = s_start[6 * w + 1];
+      b = s_start[6 * w + 2];
+      t = s_start[6 * w + 3];
+      left = s_start[6 * w + 4];
     }
     int n = left > 0 ? seq_len(p, b, false) : 0;  // keys of sequence b
     int page = -1, at = -1;  // of this lane's block: -1 past the end, -2 no such page
@@ -324,8 +341,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         }
         if (++t * BC >= n) {  // the next sequence with keys
           t = 0;
-          n = 0;
-          while (left > 0 && b + 1 < plan.n_seq && n == 0) n = seq_len(p, ++b, false);
+          n = left > 0 ? next_seq(head, rg, b) : 0;
         }
         place();
       }
@@ -356,7 +372,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     const Desc2 dq = desc_sw128(sQ, 16, 1024), dp = desc_p<C::RB>(sb + C::OFF_P);
     int left = 0;  // products to issue
 #pragma unroll
-    for (int w = 0; w < W; ++w) left += 2 * __shfl_sync(0xffffffffu, s_start[3 * w + 2], 0);
+    for (int w = 0; w < W; ++w) left += 2 * __shfl_sync(0xffffffffu, s_start[6 * w + 4], 0);
     // lane l < W looks for K of team l, lane W + l for its P
     const uint32_t my_bar = lane < W ? k_ready(lane) : p_ready(lane < 2 * W ? lane - W : 0);
     uint32_t par = 0;
@@ -438,15 +454,18 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     auto rows_sync = [&]() { named_bar_sync(1 + w, kRows); };
     int mine = 0, slot = w * C::SL;  // tiles so far, the next ring slot
     uint32_t phase = 0;
-    if (tid < NR) lag[tid] = p.n_new - 1 - (r0 + tid) % p.n_new;
 
     // Q rows of a sequence: a warp with columns takes every QW-th; a lane 4 channels of one
     constexpr int QW = kRows / 32, QR = (NA + QW - 1) / QW;
     const int qwarp = warp & (QW - 1);
     using Four = typename std::conditional<F32, uint4, uint2>::type;
     Four qv[QR];
-    auto load_q = [&](int b) {
-      const long long row0 = (b * plan.heads + head) / p.group_div * p.q_s1 + (b * plan.heads + head) % p.group_div * p.q_s2 + r0;
+    auto row_of = [&](int head, int rg, int b) {  // the group's first row of q, o and lse
+      return b * p.q_s1 + head * p.q_s2 + rg * NR;
+    };
+    auto load_q = [&](int head, int rg, int b) {
+      const long long row0 = row_of(head, rg, b);
+      const int n_rows = min(NR, p.rows - rg * NR);
 #pragma unroll
       for (int i = 0; i < QR; ++i) {
         const int r = qwarp + QW * i;
@@ -538,26 +557,32 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
       }
       next_slot();
     };
-    int b = __shfl_sync(0xffffffffu, s_start[3 * w], 0), t0 = __shfl_sync(0xffffffffu, s_start[3 * w + 1], 0);
-    int left = __shfl_sync(0xffffffffu, s_start[3 * w + 2], 0);
+    const int* start = s_start + 6 * w;
+    int head = __shfl_sync(0xffffffffu, start[0], 0), rg = __shfl_sync(0xffffffffu, start[1], 0);
+    int b = __shfl_sync(0xffffffffu, start[2], 0), t0 = __shfl_sync(0xffffffffu, start[3], 0);
+    int left = __shfl_sync(0xffffffffu, start[4], 0), lag_of = -1;  // the row group that lag[] is of
+    const int range = __shfl_sync(0xffffffffu, start[5], 0);
     int nk = left > 0 ? __shfl_sync(0xffffffffu, seq_len(p, b, false), 0) : 0;
-    if (rows && left > 0) load_q(b);
+    if (rows && left > 0) load_q(head, rg, b);
     // a piece at a time: tiles t0 .. t0 + n - 1 of sequence b
     while (left > 0) {
       const int n = min(left, tiles_of<BC>(nk) - t0);
       left -= n;
-      int next = b, next_nk = 0;  // the next sequence with keys
-      while (left > 0 && next + 1 < plan.n_seq && next_nk == 0) next_nk = __shfl_sync(0xffffffffu, seq_len(p, ++next, false), 0);
+      int next_head = head, next_rg = rg, next = b, next_nk = 0;
+      if (left > 0) next_nk = __shfl_sync(0xffffffffu, next_seq(next_head, next_rg, next), 0);
       if (next_nk == 0) left = 0;
-      const int group = b * plan.heads + head;
+      const int n_rows = min(NR, p.rows - rg * NR);
       const int all_seen = nk - (p.n_new - 1);  // keys that every row sees
       float l[NH];
 #pragma unroll
       for (int c = 0; c < NH; ++c) l[c] = 0.f;
       if (rows) {
         put_q();  // every product with the last piece's Q has completed
-        if (left > 0) load_q(next);  // lands while this piece goes on
-        if (tid < NR) ref[tid] = 0.f;  // set by the piece's first tile
+        if (left > 0) load_q(next_head, next_rg, next);  // lands while this piece goes on
+        if (tid < NA) {
+          ref[tid] = 0.f;  // set by the piece's first tile
+          if (rg != lag_of) lag[tid] = p.n_new - 1 - (rg * NR + tid) % p.n_new;
+        }
         rows_sync();
         if (keys)
           unpack_k();
@@ -767,8 +792,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         for (int x = 0; x < RCOLS; ++x) red[quarter * NR + my_col + x] = l[x];
         rows_sync();
         const bool whole = t0 == 0 && n == tiles_of<BC>(nk);
-        const long long part = static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + w * ctas + cta + b;
-        const long long orow0 = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r0;
+        const long long part = static_cast<long long>(head * plan.row_groups + rg) * plan.n_seq + b + range;
+        const long long orow0 = row_of(head, rg, b);
         if (tid < NA) {
           const float sum = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
           fac[tid] = sum == 0.f ? 0.f : cache.v_scale / sum;
@@ -805,6 +830,9 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         __syncwarp();
         tc_fence_before();
       }
+      lag_of = rg;
+      head = next_head;
+      rg = next_rg;
       b = next;
       t0 = 0;
       nk = next_nk;
@@ -825,7 +853,7 @@ cudaError_t launch_nr(const SeqAttn& p, const Cache4& c, const DecodePlan& plan,
   static SmemOnce once;
   const cudaError_t e = once(fa_cache4_decode_kernel<D, NR, NA, F32>, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(plan.heads) * plan.row_groups * (plan.cuts / C::W);
+  const unsigned grid = static_cast<unsigned>(plan.cuts / C::W);
   fa_cache4_decode_kernel<D, NR, NA, F32><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(p, c, plan);
   return cudaGetLastError();
 }
@@ -864,26 +892,23 @@ DecodePlan cache4_plan(int n_seq, int heads, int rows, int d, fa_dtype dt, int s
   // float32: at most 32 rows, whose terms of Q and P leave the ring its room
   w.nr = rows <= 16 ? 16 : rows <= 32 || dt == FA_DTYPE_F32 ? 32 : 64;
   w.row_groups = (rows + w.nr - 1) / w.nr;
-  const long long groups = static_cast<long long>(heads) * w.row_groups;
-  const int ctas = groups < sms ? static_cast<int>(sms / groups) : 1;  // a CTA an SM
-  w.cuts = ctas * (dt == FA_DTYPE_F32 ? teams<true>(d, w.nr) : teams<false>(d, w.nr));
+  w.cuts = sms * (dt == FA_DTYPE_F32 ? teams<true>(d, w.nr) : teams<false>(d, w.nr));  // a CTA an SM, a range a team
   w.direct = 1;
   return w;
 }
 
 cudaError_t launch_cache4_decode(const SeqAttn& p, const Cache4& c, const DecodePlan& w, fa_dtype dt, cudaStream_t s) {
-  if (static_cast<long long>(w.heads) * w.row_groups * w.cuts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  // tile counts are summed, and multiplied by the number of cuts, in 32 bits
-  if (static_cast<long long>(w.n_seq) * tiles_of<BC>(p.n_keys) * (w.cuts + 1LL) > 0x7fffffffLL)
-    return cudaErrorInvalidConfiguration;
+  // the sequences' tiles are summed in 32 bits, a range's tiles are counted in 31
+  const long long tiles = static_cast<long long>(w.n_seq) * tiles_of<BC>(p.n_keys);
+  if (tiles > 0x7fffffffLL || tiles * w.heads * w.row_groups / w.cuts >= 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return dt == FA_DTYPE_F32 ? launch_type<true>(p, c, w, s) : launch_type<false>(p, c, w, s);
 }
 
 template <typename T>
 static cudaError_t merge_of(const SeqAttn& p, const DecodePlan& w, cudaStream_t s) {
-  if (w.nr == 16) return launch_merge<BC, 16, T>(p, w, nullptr, nullptr, 0, true, s);
-  if (w.nr == 32) return launch_merge<BC, 32, T>(p, w, nullptr, nullptr, 0, true, s);
-  return launch_merge<BC, 64, T>(p, w, nullptr, nullptr, 0, true, s);
+  if (w.nr == 16) return launch_merge<BC, 16, T, true>(p, w, nullptr, nullptr, 0, true, s);
+  if (w.nr == 32) return launch_merge<BC, 32, T, true>(p, w, nullptr, nullptr, 0, true, s);
+  return launch_merge<BC, 64, T, true>(p, w, nullptr, nullptr, 0, true, s);
 }
 cudaError_t launch_cache4_merge(const SeqAttn& p, const DecodePlan& w, fa_dtype dt, cudaStream_t s) {
   return dt == FA_DTYPE_F32 ? merge_of<float>(p, w, s) : merge_of<__nv_bfloat16>(p, w, s);

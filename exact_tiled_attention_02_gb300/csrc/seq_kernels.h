@@ -132,6 +132,7 @@ int cache4_simt_splits(int B, int Hq, int Hkv, int n_new, int n_keys, int d);
 
 // On the tensor cores, d = 64, 96 or 128 (cache4_decode_sm103.cu).  p: as for
 // launch_seq_decode, groups (sequence, key/value head), page fields and k1, v unused.
+// Ranges are flat (seq_ranges.cuh): plan.cuts of them over all groups of rows; slot = range + row group * n_seq + sequence.
 DecodePlan cache4_plan(int n_seq, int heads, int rows, int d, fa_dtype dt, int sms);
 cudaError_t launch_cache4_decode(const SeqAttn& p, const Cache4& c, const DecodePlan& w, fa_dtype dt, cudaStream_t s);
 cudaError_t launch_cache4_merge(const SeqAttn& p, const DecodePlan& w, fa_dtype dt, cudaStream_t s);

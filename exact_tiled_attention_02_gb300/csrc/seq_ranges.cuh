@@ -1,7 +1,9 @@
 // seq_ranges.cuh -- work split of the decoding kernels: the tiles of BC keys of
 // all sequences, laid end to end, cut into equal ranges, one a CTA (per group
 // of rows), and the kernel that merges the pieces of sequences that several
-// CTAs share.  The cut depends on the lengths alone.
+// CTAs share.  The cut depends on the lengths alone.  The flat form lays the
+// tiles of all groups of rows end to end too: any number of groups fills the
+// GPU, at the price of 64-bit products.
 #pragma once
 
 #include <cmath>
@@ -82,6 +84,82 @@ __device__ __forceinline__ void find_range(const SeqAttn& p, const DecodePlan& p
   }
 }
 
+// The flat form: plan.cuts ranges of all groups' tiles, none of them empty, the
+// first `rem` a tile longer than the others.  U: 32 bits where they hold the tiles.
+template <typename U>
+struct FlatCut {
+  U n, q, rem;
+  __device__ __forceinline__ FlatCut(U all, unsigned cuts) {
+    n = all < cuts ? all : cuts;
+    q = n > 0 ? all / n : 0;
+    rem = all - q * n;
+  }
+  __device__ __forceinline__ U start(U r) const { return r * q + (r < rem ? r : rem); }
+  __device__ __forceinline__ int owner(U x) const {
+    return static_cast<int>(x < rem * (q + 1) ? x / (q + 1) : rem + (x - rem * (q + 1)) / q);
+  }
+};
+// f(all groups' tiles, in 32 bits where they fit)
+template <typename F>
+__device__ __forceinline__ void flat_tiles(const DecodePlan& plan, unsigned total, F f) {
+  const unsigned long long all = static_cast<unsigned long long>(plan.heads) * plan.row_groups * total;
+  if (all >> 32 == 0)
+    f(static_cast<unsigned>(all));
+  else
+    f(all);
+}
+// The range r of team `team` (of `teams`) of this CTA: where it begins (group of
+// rows, sequence, tile) and its tiles.  Where every team has some, the CTAs are
+// dealt out among the groups, and within a group to its first teams first: CTAs
+// of all heads then walk the same pages at the same time (152 CTAs of three
+// teams, 64 sequences of 4096 to 32768 tokens, 8 heads: 222 us, 230 with teams
+// in the order of the ranges).  Fewer tiles spread over the CTAs.
+template <int BC>
+__device__ __forceinline__ void find_flat(const SeqAttn& p, const DecodePlan& plan, int team, int teams, int& r, int& grp,
+                                          int& b0, int& first, int& count) {
+  const int lane = threadIdx.x & 31;
+  unsigned before, total;
+  tile_sums<BC>(p, plan.n_seq, 0, before, total);
+  grp = b0 = first = count = 0;
+  unsigned t0 = 0;
+  const unsigned cta = blockIdx.x, ctas = gridDim.x, groups = static_cast<unsigned>(plan.heads) * plan.row_groups;
+  flat_tiles(plan, total, [&](auto all) {
+    using U = decltype(all);
+    const FlatCut<U> cut(all, plan.cuts);
+    r = team * ctas + cta;
+    if (groups <= ctas && all > static_cast<U>(plan.cuts)) {
+      const unsigned per = ctas / groups, g = cta / per, dealt = groups * per;
+      r = g < groups ? (g * teams + team) * per + (cta - g * per) : dealt * teams + team * (ctas - dealt) + (cta - dealt);
+    }
+    if (static_cast<U>(r) >= cut.n) return;
+    const U x0 = cut.start(r);
+    grp = static_cast<int>(x0 / total);
+    t0 = static_cast<unsigned>(x0 - static_cast<U>(grp) * total);
+    count = static_cast<int>(cut.start(r + 1) - x0);
+  });
+  if (count == 0) return;
+  unsigned base = 0;
+  for (int i0 = 0; i0 < plan.n_seq; i0 += 32) {
+    const int i = i0 + lane;
+    const unsigned t = i < plan.n_seq ? tiles_of<BC>(seq_len(p, i, true)) : 0;
+    unsigned inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const unsigned end = base + inc;
+    const unsigned hit = __ballot_sync(0xffffffffu, end > t0);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      b0 = i0 + l;
+      first = static_cast<int>(t0 - __shfl_sync(0xffffffffu, end - t, l));
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, inc, 31);
+  }
+}
+
 __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool x) {
   uint32_t r;
   asm volatile(
@@ -101,7 +179,7 @@ __device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool x) {
 // slices (all of them where there are rows enough to fill the GPU); lane i
 // holds the weight of part i, so that the parts' loads do not wait for one
 // another.  Rows of a sequence that was written directly are left alone.
-template <int BC, int NR, int W, typename T>
+template <int BC, int NR, int W, typename T, bool FLAT>
 __global__ void __launch_bounds__(128)
     fa_seq_decode_merge_kernel(const __grid_constant__ SeqAttn p, const DecodePlan plan, const float* __restrict__ pre_o,
                                const float* __restrict__ pre_lse, int pre) {
@@ -119,16 +197,27 @@ __global__ void __launch_bounds__(128)
   unsigned before, total;
   tile_sums<BC>(p, plan.n_seq, b, before, total);
   const int nt = tiles_of<BC>(seq_len(p, b, true));
+  const int grp = head * plan.row_groups + r / NR;
   int c0 = 0, n = 0;
   if (nt > 0) {
-    const unsigned ranges = range_count(total, plan.cuts);
-    c0 = owner(total, before, ranges);
-    n = owner(total, before + nt - 1, ranges) - c0 + 1;
+    if constexpr (FLAT) {
+      flat_tiles(plan, total, [&](auto all) {
+        using U = decltype(all);
+        const FlatCut<U> cut(all, plan.cuts);
+        const U at = static_cast<U>(grp) * total + before;
+        c0 = cut.owner(at);
+        n = cut.owner(at + nt - 1) - c0 + 1;
+      });
+    } else {
+      const unsigned ranges = range_count(total, plan.cuts);
+      c0 = owner(total, before, ranges);
+      n = owner(total, before + nt - 1, ranges) - c0 + 1;
+    }
   }
   pdl_wait();
   if (plan.direct && n == 1) return;
-  const int grp = head * plan.row_groups + r / NR;
-  const long long slot0 = (static_cast<long long>(grp) * (plan.cuts + plan.n_seq) + c0 + b) * NR + r % NR;
+  const long long slot0 =
+      (static_cast<long long>(grp) * (FLAT ? plan.n_seq : plan.cuts + plan.n_seq) + c0 + b) * NR + r % NR;
   const long long row = (group / p.group_div) * p.q_s1 + (group % p.group_div) * p.q_s2 + r;
   n += pre;
   auto part_lse = [&](int i) {
@@ -146,6 +235,7 @@ __global__ void __launch_bounds__(128)
   for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int c = slice * 128 * W + 4 * lane;
+  constexpr int U = W == 1 ? 4 : 2;
   float4 acc[W];
 #pragma unroll
   for (int w = 0; w < W; ++w) acc[w] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -153,21 +243,32 @@ __global__ void __launch_bounds__(128)
     const float ls = i0 == 0 ? mine : (i0 + lane < n ? part_lse(i0 + lane) : -INFINITY);
     const float wl = expf(ls - ref) * inv;
     const int k = min(32, n - i0);
-#pragma unroll 8
-    for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, wl, i);
-      const int part = i0 + i;
-      const float* src = (part < pre ? pre_o + (part * p.total + row) * p.dv
-                                     : p.part_o + (slot0 + static_cast<long long>(part - pre) * NR) * p.dv) + c;
-      if (wi == 0.f) continue;  // a part without keys holds zeros or nothing
+#pragma unroll 1
+    for (int i = 0; i < k; i += U) {  // the loads of U parts do not wait for one another
+      float wi[U];
+      float4 v[U][W];
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (c + 128 * w >= p.dv) break;
-        const float4 v = *reinterpret_cast<const float4*>(src + 128 * w);
-        acc[w].x = fmaf(wi, v.x, acc[w].x);
-        acc[w].y = fmaf(wi, v.y, acc[w].y);
-        acc[w].z = fmaf(wi, v.z, acc[w].z);
-        acc[w].w = fmaf(wi, v.w, acc[w].w);
+      for (int u = 0; u < U; ++u) {
+        wi[u] = __shfl_sync(0xffffffffu, wl, (i + u) & 31);
+        if (i + u >= k) wi[u] = 0.f;
+        const int part = i0 + i + u;
+        const float* src = (part < pre ? pre_o + (part * p.total + row) * p.dv
+                                       : p.part_o + (slot0 + static_cast<long long>(part - pre) * NR) * p.dv) + c;
+#pragma unroll
+        for (int w = 0; w < W; ++w)  // a part without keys holds zeros or nothing
+          v[u][w] = wi[u] != 0.f && c + 128 * w < p.dv ? *reinterpret_cast<const float4*>(src + 128 * w)
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (wi[u] == 0.f) continue;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          acc[w].x = fmaf(wi[u], v[u][w].x, acc[w].x);
+          acc[w].y = fmaf(wi[u], v[u][w].y, acc[w].y);
+          acc[w].z = fmaf(wi[u], v[u][w].z, acc[w].z);
+          acc[w].w = fmaf(wi[u], v[u][w].w, acc[w].w);
+        }
       }
     }
   }
@@ -183,7 +284,7 @@ __global__ void __launch_bounds__(128)
   if (slice == 0 && lane == 0 && p.lse != nullptr) p.lse[row] = m + logf(sum);
 }
 
-template <int BC, int NR, typename T = __nv_bfloat16>
+template <int BC, int NR, typename T = __nv_bfloat16, bool FLAT = false>
 cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre_o, const float* pre_lse, int pre,
                          bool after, cudaStream_t s) {
   // A warp takes a whole row of 512 where the rows alone give every SM 32 warps
@@ -195,12 +296,12 @@ cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre
   if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
   if (!after) {  // no kernel of this call before it: the lengths may only now be complete
-    fa_seq_decode_merge_kernel<BC, NR, 1, T><<<static_cast<unsigned>((rows * ((p.dv + 127) / 128) + 3) / 4), 128, 0, s>>>(
+    fa_seq_decode_merge_kernel<BC, NR, 1, T, FLAT><<<static_cast<unsigned>((rows * ((p.dv + 127) / 128) + 3) / 4), 128, 0, s>>>(
         p, w, pre_o, pre_lse, pre);
     return cudaGetLastError();
   }
-  return wide ? launch_after(fa_seq_decode_merge_kernel<BC, NR, 4, T>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre)
-              : launch_after(fa_seq_decode_merge_kernel<BC, NR, 1, T>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
+  return wide ? launch_after(fa_seq_decode_merge_kernel<BC, NR, 4, T, FLAT>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre)
+              : launch_after(fa_seq_decode_merge_kernel<BC, NR, 1, T, FLAT>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
 }
 
 }  // namespace seq
