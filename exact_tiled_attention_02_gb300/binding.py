@@ -345,6 +345,7 @@ def fa_cache_fp4_bytes(n_pages: int, Hkv: int, page_size: int, d: int) -> int:
     return lib.fa_cache_fp4_bytes(n_pages, Hkv, page_size, d)
 
 
+@functools.lru_cache(maxsize=1024)  # a server asks for the same sizes at every step
 def fa_fwd_cache_fp4_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, page_size: int, max_pages: int, d: int) -> int:
     return lib.fa_fwd_cache_fp4_workspace_bytes(B, Hq, Hkv, Nq, page_size, max_pages, d)
 

@@ -237,8 +237,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     tmem_relinquish();
   }
   if (warp < 8 * W && (warp & 7) == 0) {
-    int r, grp, b0, first, count;
-    find_flat<BC>(p, plan, warp >> 3, W, r, grp, b0, first, count);
+    // (teams in the order of the ranges: few tiles spread over the SMs)
+    const int r = (warp >> 3) * gridDim.x + blockIdx.x;
+    int grp, b0, first, count;
+    find_flat<BC>(p, plan, r, grp, b0, first, count);
     if (lane == 0) {
       int* at = s_start + 6 * (warp >> 3);
       at[0] = grp / plan.row_groups;

@@ -66,10 +66,10 @@ __host__ __device__ __forceinline__ int blocks_of(int n) { return (n + kBlock - 
 // holds the tokens of a channel together.  Tokens of the block that are not
 // new keep their codes and scales: where a byte of value codes is shared with
 // one of them it is read and put together again.
-template <typename T>
+template <typename T, Quotient Q>
 __global__ void __launch_bounds__(kWarps * 32)
     fa_cache4_write_kernel(const __grid_constant__ Cache4 c, const T* __restrict__ k, const T* __restrict__ v,
-                           const int* __restrict__ n_new, int Nn, float inv_k, float inv_v, bool pow2_k, bool pow2_v) {
+                           const int* __restrict__ n_new, int Nn, float k_scale, float v_scale) {
   extern __shared__ uint2 smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = c.d, groups = d / 16;
@@ -106,30 +106,41 @@ __global__ void __launch_bounds__(kWarps * 32)
     float x[16];
     uint2 w;
     load16(k + (row0 + t) * d + g * 16, x);
-    uint8_t s = quantise16(x, inv_k, pow2_k, w);
+    uint8_t s = quantise16<Q>(x, k_scale, w);
     *reinterpret_cast<uint2*>(dst + (g * 16 + t) * 8) = w;
     dst[off_k_scale(d) + t * groups + g] = s;
     load16(v + (row0 + t) * d + g * 16, x);
-    s = quantise16(x, inv_v, pow2_v, w);
+    s = quantise16<Q>(x, v_scale, w);
     codes[i] = w;
     dst[off_v_scale(d) + g * 16 + t] = s;
   }
   __syncwarp();
-  // a lane takes the 16 tokens of a channel
+  // a lane takes the 16 tokens of eight channels
   unsigned long long keep = 0;  // nibbles of the tokens that stay
   if (t0 > 0) keep |= (1ull << (4 * t0)) - 1;
   if (t1 < kBlock) keep |= ~0ull << (4 * t1);
-  const uint8_t* nib = reinterpret_cast<const uint8_t*>(codes);
-  for (int ch = lane; ch < d; ch += 32) {
-    unsigned long long* out = reinterpret_cast<unsigned long long*>(dst + off_v(d)) + ch;
-    unsigned long long w = 0;
+  const uint32_t keep_lo = static_cast<uint32_t>(keep), keep_hi = static_cast<uint32_t>(keep >> 32);
+  const uint32_t* rows = reinterpret_cast<const uint32_t*>(codes);  // [16 tokens][d/8]
+  for (int i = lane; i < d / 8; i += 32) {
+    uint32_t lo[8], hi[8];
 #pragma unroll
-    for (int t = 0; t < kBlock; ++t) {
-      const unsigned x = (nib[t * (d / 2) + ch / 2] >> (4 * (ch & 1))) & 15u;
-      w |= static_cast<unsigned long long>(x) << (4 * t);
+    for (int t = 0; t < 8; ++t) {
+      lo[t] = rows[t * (d / 8) + i];
+      hi[t] = rows[(t + 8) * (d / 8) + i];
     }
-    if (keep != 0) w = (*out & keep) | (w & ~keep);
-    *out = w;
+    transpose_codes(lo);
+    transpose_codes(hi);
+    uint4* out = reinterpret_cast<uint4*>(dst + off_v(d) + i * 64);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint4 w = make_uint4(lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1]);
+      if (keep != 0) {
+        const uint4 o = out[j];
+        w = make_uint4((o.x & keep_lo) | (w.x & ~keep_lo), (o.y & keep_hi) | (w.y & ~keep_hi),
+                       (o.z & keep_lo) | (w.z & ~keep_lo), (o.w & keep_hi) | (w.w & ~keep_hi));
+      }
+      out[j] = w;
+    }
   }
 }
 
@@ -219,7 +230,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// A power of two whose reciprocal can stand for the division by it.
+// A power of two whose reciprocal is a normal number, and so can stand for the division by it.
 bool power_of_two(float x) {
   int e;
   return std::frexp(x, &e) == 0.5f && e > -100 && e < 100;
@@ -230,10 +241,14 @@ cudaError_t launch_write(const Cache4& c, const void* k, const void* v, const in
   const long long warps = static_cast<long long>(c.B) * c.Hkv * blocks_of(Nn);
   const long long blocks = (warps + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const bool pk = power_of_two(c.k_scale), pv = power_of_two(c.v_scale);
-  fa_cache4_write_kernel<T><<<static_cast<unsigned>(blocks), kWarps * 32, kWarps * c.d * 16, s>>>(
-      c, static_cast<const T*>(k), static_cast<const T*>(v), n_new, Nn, pk ? 1.f / c.k_scale : c.k_scale,
-      pv ? 1.f / c.v_scale : c.v_scale, pk, pv);
+  const unsigned grid = static_cast<unsigned>(blocks);
+  const int smem = kWarps * c.d * 16;
+  const T *kt = static_cast<const T*>(k), *vt = static_cast<const T*>(v);
+  constexpr Quotient kFast = sizeof(T) == 2 ? kShort : kMultiply;
+  if (power_of_two(c.k_scale) && power_of_two(c.v_scale))
+    fa_cache4_write_kernel<T, kFast><<<grid, kWarps * 32, smem, s>>>(c, kt, vt, n_new, Nn, 1.f / c.k_scale, 1.f / c.v_scale);
+  else
+    fa_cache4_write_kernel<T, kDivide><<<grid, kWarps * 32, smem, s>>>(c, kt, vt, n_new, Nn, c.k_scale, c.v_scale);
   return cudaGetLastError();
 }
 template <typename T>

@@ -108,29 +108,18 @@ __device__ __forceinline__ void flat_tiles(const DecodePlan& plan, unsigned tota
   else
     f(all);
 }
-// The range r of team `team` (of `teams`) of this CTA: where it begins (group of
-// rows, sequence, tile) and its tiles.  Where every team has some, the CTAs are
-// dealt out among the groups, and within a group to its first teams first: CTAs
-// of all heads then walk the same pages at the same time (152 CTAs of three
-// teams, 64 sequences of 4096 to 32768 tokens, 8 heads: 222 us, 230 with teams
-// in the order of the ranges).  Fewer tiles spread over the CTAs.
+// Of range r: where it begins (group of rows, sequence, tile) and its tiles.
 template <int BC>
-__device__ __forceinline__ void find_flat(const SeqAttn& p, const DecodePlan& plan, int team, int teams, int& r, int& grp,
-                                          int& b0, int& first, int& count) {
+__device__ __forceinline__ void find_flat(const SeqAttn& p, const DecodePlan& plan, int r, int& grp, int& b0, int& first,
+                                          int& count) {
   const int lane = threadIdx.x & 31;
   unsigned before, total;
   tile_sums<BC>(p, plan.n_seq, 0, before, total);
   grp = b0 = first = count = 0;
   unsigned t0 = 0;
-  const unsigned cta = blockIdx.x, ctas = gridDim.x, groups = static_cast<unsigned>(plan.heads) * plan.row_groups;
   flat_tiles(plan, total, [&](auto all) {
     using U = decltype(all);
     const FlatCut<U> cut(all, plan.cuts);
-    r = team * ctas + cta;
-    if (groups <= ctas && all > static_cast<U>(plan.cuts)) {
-      const unsigned per = ctas / groups, g = cta / per, dealt = groups * per;
-      r = g < groups ? (g * teams + team) * per + (cta - g * per) : dealt * teams + team * (ctas - dealt) + (cta - dealt);
-    }
     if (static_cast<U>(r) >= cut.n) return;
     const U x0 = cut.start(r);
     grp = static_cast<int>(x0 / total);
