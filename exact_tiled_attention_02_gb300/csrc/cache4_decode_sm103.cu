@@ -1,5 +1,6 @@
 // cache4_decode_sm103.cu -- attention of few query rows over the 4-bit key/value
-// cache, bf16 in / fp32 accumulate, on the tensor cores of GB300 (sm_103a).
+// cache, bf16 or float32 in / fp32 accumulate, on the tensor cores of GB300
+// (sm_103a).
 //
 //   S_ij = scale k_scale (q_i . K_j) over the keys j < len - lag(i),
 //   O_i = v_scale sum_j softmax_j(S_i) V_j,   K, V = code * scale
@@ -31,6 +32,17 @@
 // One more warp loads: a tile's blocks, one bulk copy for each run of them in a
 // page.  The work is split as seq_ranges.cuh says, a range a team; a sequence
 // that is one whole piece goes straight to o.
+//
+// Unpacking costs two instructions a pair of codes (a conversion and a product, in
+// pipes that take 2.6 cycles for both), 330 cycles a tile of d = 128 for the 830
+// that its 18 KB take at the copy rate; at 4 rows the whole tile is 600
+// instructions a scheduler.  64 sequences of 4096 to 32768 tokens, 32 / 8 heads,
+// d = 128: 224 us, 6.1 TB/s (90% of the copy rate).  500 to 8200 tokens: 67.5 us,
+// 63 of them this kernel; 7 go by before its first tile has come (length, page,
+// tile: three dependent loads) and after its last.  With 32 rows two teams fit
+// tensor memory instead of three, and the warps there are keep the schedulers busy
+// 59% of the time: 32 sequences, 64 / 8 heads x 4 tokens, 1000 to 16384: 104 us.
+// 512 tokens, 64 rows a group: 125 us, 568 TFLOP/s, 66% of the issue slots.
 #include <cmath>
 #include <type_traits>
 
@@ -48,8 +60,12 @@ constexpr int BC = 128;  // keys per tile
 // least 2^-32 of the largest P.
 constexpr float kBelow = 7.0f, kRescaleThreshold = kBelow + 8.0f;
 
-// F32: float32 q and o.  Q is then three fp16 terms and P two, which the
-// products take one after the other: 2^-33 and 2^-22 relative.
+// F32: float32 q and o.  Q is then three fp16 terms and P two, 2^-33 and 2^-22
+// relative, which the products take one after the other, the smallest first.  A
+// product that adds to what an accumulator holds drops bits of it, to the same
+// side each time, so O^T is of one tile only, and the tiles are added up in
+// registers (6 x 32 heads x 3 tokens, up to 3001 tokens, d = 96: 4e-7 of O,
+// 1.1e-6 with O^T kept on and the largest terms first; float32 sums 6.6e-7).
 template <int D, int NR, int NA, bool F32>
 struct Cfg {
   static constexpr int QT = F32 ? 3 : 1, PT = F32 ? 2 : 1;
@@ -68,7 +84,7 @@ struct Cfg {
   static constexpr int Q_BYTES = QC * NR * 128;      // a term
   static constexpr int P_BYTES = 128 * RB;           // a term of a team
   static constexpr int VS_BYTES = W * 4 * 512;       // a warp's value scales in fp16: [2 groups][128 keys]
-  static constexpr int STATS = 6 * NR * 4                  // a team: lag, column scale, reference, factor
+  static constexpr int STATS = 4 * NR * 4                  // a team: lag, column scale, reference, factor
                                + 4 * NR * 4;               // and warps' column results
   static constexpr int MISC = VS_BYTES + W * STATS + 512;
   static constexpr int FIT = (227 * 1024 - 1024 - W * (QT * Q_BYTES + PT * P_BYTES) - MISC) / TILE / W;
@@ -81,7 +97,7 @@ struct Cfg {
   static constexpr int OFF_STAT = OFF_VS + VS_BYTES;
   static constexpr int OFF_BAR = OFF_STAT + W * STATS;
   static constexpr int NBAR = 2 * SLOTS + 4 * W + 1;
-  // tensor memory base, abort flag; teams' first sequence, its first tile, their tiles; first-tile flags; slots' missing blocks
+  // tensor memory base, abort flag; where the teams begin (6 words each), first-tile flags; slots' missing blocks
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_USED = OFF_MISC + 8 + W * 28 + SLOTS * 4;
   static constexpr int SMEM_BYTES = SMEM_USED + 1024;
@@ -402,17 +418,19 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
               mma_ts_w(tw + C::TM_S, tw + C::TM_K + 8 * kk, dq,
-                       ((w * C::QT + t) * C::Q_BYTES + (kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s, t > 0 || kk > 0);
+                       ((w * C::QT + C::QT - 1 - t) * C::Q_BYTES + (kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s,
+                       t > 0 || kk > 0);
           mma_commit_w(s_done(w));
         }
         if (ready >> (W + w) & 1) {
-          const uint32_t more = s_first[w] == 0;
+          const uint32_t more = !F32 && s_first[w] == 0;
 #pragma unroll
           for (int t = 0; t < C::PT; ++t)
 #pragma unroll
             for (int kk = 0; kk < BC / 16; ++kk)
               mma_ts_w(tw + C::TM_O, tw + C::TM_V + 8 * kk, dp,
-                       ((w * C::PT + t) * C::P_BYTES + kk * 16 * C::RB) >> 4, idesc_o, t > 0 || kk > 0 ? 1u : more);
+                       ((w * C::PT + C::PT - 1 - t) * C::P_BYTES + kk * 16 * C::RB) >> 4, idesc_o,
+                       t > 0 || kk > 0 ? 1u : more);
           mma_commit_w(o_done(w));
         }
       }
@@ -578,6 +596,21 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
       float l[NH];
 #pragma unroll
       for (int c = 0; c < NH; ++c) l[c] = 0.f;
+      float acc[F32 ? NH : 1];  // float32: O of the tiles so far, this thread's channel
+#pragma unroll
+      for (int c = 0; c < (F32 ? NH : 1); ++c) acc[c] = 0.f;
+      auto add_tile = [&]() {
+        if constexpr (F32) {
+          uint32_t o[NH];
+          if constexpr (NH == 4)
+            tmem_ld_x4(tl + C::TM_O, o);
+          else
+            tmem_ld<NH>(tl + C::TM_O + c0, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < NH; ++c) acc[c] += __uint_as_float(o[c]);
+        }
+      };
       if (rows) {
         put_q();  // every product with the last piece's Q has completed
         if (left > 0) load_q(next_head, next_rg, next);  // lands while this piece goes on
@@ -708,6 +741,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
           // the last product of this team has read P (and O is complete)
           if (!o_ready) wait_longer(o_done(w), (mine - 1) & 1, wc.status, wc.abort_flag, wc.limit_ns);
           __syncwarp();
+          if (F32 && i > 0) {
+            tc_fence_after();
+            add_tile();
+          }
           if (rises) {
             // the piece's first tile sets the references (a row that sees any key of
             // the piece sees its first one), in others some rise: column maxima over
@@ -733,9 +770,11 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
             for (int c = 0; c < NH; ++c) {
               const float f = fac[c0 + c];
               x[c] += f;
-              l[c] *= ex2_approx(fminf(f, 0.f));  // (the first tile finds zeros)
+              const float alpha = ex2_approx(fminf(f, 0.f));  // (the first tile finds zeros)
+              l[c] *= alpha;
+              if constexpr (F32) acc[c] *= alpha;
             }
-            if (i > 0) {
+            if (!F32 && i > 0) {
 #pragma unroll 1
               for (int c = c0; c < c0 + NH; c += 8) {
                 uint32_t o[8];
@@ -799,7 +838,8 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         if (tid < NA) {
           const float sum = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
           fac[tid] = sum == 0.f ? 0.f : cache.v_scale / sum;
-          const float lse = sum == 0.f ? -INFINITY : (__log2f(sum) - ref[tid]) * 0.69314718055994531f;  // no key seen: -inf
+          // (one product in 64 bits: the reference may be large beside the logarithm; no key seen: -inf)
+          const float lse = sum == 0.f ? -INFINITY : static_cast<float>(logf(sum) - ref[tid] * 0.69314718055994531);
           if (tid < n_rows && !*abort_flag) {
             if (!whole)
               p.part_lse[part * NR + tid] = lse;
@@ -810,23 +850,35 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         wait_for(o_done(w), (mine - 1) & 1, wc);
         tc_fence_after();
         rows_sync();
-#pragma unroll 1
-        for (int c = c0; c < min(c0 + NH, n_rows); c += 8) {
-          uint32_t o[8];
-          __syncwarp();
-          tmem_ld_32x32b_x8(tl + C::TM_O + c, o);
-          tmem_wait_ld();
-          if (id >= D || *abort_flag) continue;
+        auto put_o = [&](int row, float y) {
+          if (!whole)
+            p.part_o[(part * NR + row) * D + id] = y;
+          else if constexpr (F32)
+            static_cast<float*>(p.o)[(orow0 + row) * D + id] = y;
+          else
+            static_cast<__nv_bfloat16*>(p.o)[(orow0 + row) * D + id] = __float2bfloat16_rn(y);
+        };
+        if constexpr (F32) {
+          add_tile();
+          if (id < D && !*abort_flag) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            if (c + x >= n_rows) break;
-            const float f = fac[c + x], y = f == 0.f ? 0.f : __uint_as_float(o[x]) * f;
-            if (!whole)
-              p.part_o[(part * NR + c + x) * D + id] = y;
-            else if constexpr (F32)
-              static_cast<float*>(p.o)[(orow0 + c + x) * D + id] = y;
-            else
-              static_cast<__nv_bfloat16*>(p.o)[(orow0 + c + x) * D + id] = __float2bfloat16_rn(y);
+            for (int c = 0; c < NH; ++c)
+              if (c0 + c < n_rows) put_o(c0 + c, fac[c0 + c] == 0.f ? 0.f : acc[c] * fac[c0 + c]);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = c0; c < min(c0 + NH, n_rows); c += 8) {
+            uint32_t o[8];
+            __syncwarp();
+            tmem_ld_32x32b_x8(tl + C::TM_O + c, o);
+            tmem_wait_ld();
+            if (id >= D || *abort_flag) continue;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              if (c + x >= n_rows) break;
+              const float f = fac[c + x];
+              put_o(c + x, f == 0.f ? 0.f : __uint_as_float(o[x]) * f);
+            }
           }
         }
         __syncwarp();

@@ -391,7 +391,14 @@ fa_status fa_cache_fp4_read(const void* cache, const int* block_table, const int
  *   q, o         [B,Hq,Nq,d], bf16 or float32.   lse  float32 [B,Hq,Nq] or NULL.
  *   workspace    at least fa_fwd_cache_fp4_workspace_bytes() bytes, 256-byte
  *                aligned, as above.
- * Hq must be a multiple of Hkv.  Forward only: a serving call.
+ * Hq must be a multiple of Hkv; Hkv ceil(Hq / Hkv Nq / 16) B tiles of 128
+ * tokens / 304 must stay below 2^31 too.  Forward only: a serving call.
+ * d = 64, 96 and 128 run on the tensor cores, with fp32 accumulation: code * s
+ * is exact in fp16, a row of q is brought to fp16 by a power of two (bf16: exact
+ * down to 2^-31 of its largest entry; float32: as three terms), and P, rounded
+ * to fp16 (float32: as two terms), multiplies the values: 2^-11 relative
+ * (2^-22), and 2^-32 of the largest P at the least.  Other d run on CUDA cores
+ * in plain fp32.
  */
 fa_status fa_fwd_cache_fp4(const void* q, const void* cache, const int* block_table, const int* lens, void* o,
                            float* lse, int B, int Hq, int Hkv, int Nq, int n_pages, int page_size, int max_pages,

@@ -242,3 +242,60 @@ def test_without_a_table(fa):
         ref, lr, tol, tol_l = cc.forward(sb.f64(q[b]), k, v, d ** -0.5, "bf16")
         sb.check("o", sb.f64(o[b]), ref, tol)
         sb.check("lse", sb.f64(lse[b]), lr, tol_l)
+
+
+@pytest.mark.parametrize("dtype,d,Nq", [("bf16", 128, 1), ("bf16", 64, 20), ("f32", 96, 2), ("bf16", 80, 1)])
+def test_a_batch_without_any_token(fa, dtype, d, Nq):
+    q = torch.randn(3, 4, Nq, d).to(TYPES[dtype]).cuda()
+    cache = torch.full((2, 2, 16, 9 * d // 8), 0xFF, dtype=torch.uint8, device="cuda")
+    kw = dict(block_table=i32([[-1, 7]] * 3))
+    o, lse = fa.fa_fwd_cache_fp4(q, cache, i32([0, 0, 0]), **kw)
+    k, v = fa.fa_cache_fp4_read(cache, i32([0, 0, 0]), 5, **kw)
+    fa.fa_cache_fp4_write(q[:, :2].contiguous(), q[:, :2].contiguous(), cache, i32([0, 0, 0]), n_new=i32([0, 0, 0]), **kw)
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_status() == fa.FA_OK
+    assert (o == 0).all() and (lse == -float("inf")).all() and (k == 0).all() and (v == 0).all() and (cache == 0xFF).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq,d", [(8, 8, 1, 128), (16, 4, 1, 64), (40, 8, 1, 96), (24, 3, 1, 128), (64, 4, 1, 128),
+                                         (48, 16, 1, 64), (10, 2, 4, 128), (6, 1, 9, 96), (4, 1, 33, 64), (2, 1, 97, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_every_row_count(fa, dtype, Hq, Hkv, Nq, d):
+    """1 to 194 rows a key head: every width of the products, and groups of rows."""
+    rng = np.random.default_rng(Hq + Nq)
+    lens, page = [Nq + 3, 0, 517, 128, 2], 32
+    table, pages = cc.place(rng, 5, 20, lens, page)
+    cache = cc.random_cache(rng, pages, Hkv, page, d)
+    cc.poison(cache, table, lens, page, d)
+    q = torch.from_numpy(rng.standard_normal((5, Hq, Nq, d))).to(TYPES[dtype])
+    o, lse = fa.fa_fwd_cache_fp4(q.cuda(), torch.from_numpy(cache).cuda(), i32(lens), scale=0.02, block_table=i32(table))
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_status() == fa.FA_OK
+    for b, n in enumerate(lens):
+        k, v = cc.dense(cache, table, b, n, d, page, 1.0, 1.0)
+        ref, lr, tol, tol_l = cc.forward(sb.f64(q[b]), k, v, float(np.float32(0.02)), dtype)
+        sb.check(f"lse {b}", sb.f64(lse[b]), lr, tol_l)
+        sb.check(f"o {b}", sb.f64(o[b]), ref, tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_scores_that_rise_and_fall(fa, dtype):
+    """Keys that grow along a sequence (references rise tile after tile, O is
+    rescaled), fall, or jump by thousands; scores of 2^40 and of 2^-40."""
+    d, n, page = 128, 1000, 16
+    rng = np.random.default_rng(6)
+    blocks = cc.random_cache(rng, 63, 1, page, d).reshape(63, 1, 1, 18 * d)
+    table = np.arange(63, dtype=np.int32)[None]
+    for grow in (lambda i: i // 2, lambda i: 62 - i, lambda i: 60 * (i % 2), lambda i: 55 if i == 40 else 5):
+        for i in range(63):
+            blocks[i, ..., 8 * d:9 * d] = 0x10 + grow(i)
+        cache = blocks.reshape(63, 1, page, 144)
+        for scale in (0.01, 0.5, 2.0 ** 20, 2.0 ** -60):
+            q = torch.from_numpy(rng.standard_normal((1, 4, 2, d))).to(TYPES[dtype])
+            o, lse = fa.fa_fwd_cache_fp4(q.cuda(), torch.from_numpy(cache).cuda(), i32([n]), scale=scale, block_table=i32(table))
+            k, v = cc.dense(cache, table, 0, n, d, page, 1.0, 1.0)
+            ref, lr, tol, tol_l = cc.forward(sb.f64(q[0]), k, v, scale, dtype)
+            sb.check("lse", sb.f64(lse[0]), lr, tol_l)
+            if scale < 2:  # past that the bound on a score's error allows any softmax
+                sb.check("o", sb.f64(o[0]), ref, tol)
+            assert torch.isfinite(o).all()
