@@ -186,6 +186,41 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Four or two products in a row, K steps of 16: A steps 8 columns, B's start STEP
+// units of 16 bytes.  One election for all of them: the issuing warp shares its
+// scheduler with a quarter of the others.
+template <int N, int STEP>
+__device__ __forceinline__ void mma_ts_steps(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                             uint32_t acc) {
+  static_assert(N == 2 || N == 4, "steps");
+  if constexpr (N == 4)
+    asm volatile(
+        "{\n.reg .pred p, q, e;\n.reg .b64 b0, b1, b2, b3;\n.reg .b32 x;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p, %5, 0;\nsetp.eq.b32 q, %5, %5;\n"
+        "mov.b64 b0, {%2, %3};\n"
+        "add.u32 x, %2, %6;\nmov.b64 b1, {x, %3};\n"
+        "add.u32 x, %2, %7;\nmov.b64 b2, {x, %3};\n"
+        "add.u32 x, %2, %8;\nmov.b64 b3, {x, %3};\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, p;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1 + 8], b1, %4, q;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1 + 16], b2, %4, q;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1 + 24], b3, %4, q;\n}\n" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "n"(STEP), "n"(2 * STEP), "n"(3 * STEP)
+        : "memory");
+  else
+    asm volatile(
+        "{\n.reg .pred p, q, e;\n.reg .b64 b0, b1;\n.reg .b32 x;\n"
+        "elect.sync _|e, 0xffffffff;\n"
+        "setp.ne.b32 p, %5, 0;\nsetp.eq.b32 q, %5, %5;\n"
+        "mov.b64 b0, {%2, %3};\n"
+        "add.u32 x, %2, %6;\nmov.b64 b1, {x, %3};\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b0, %4, p;\n"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1 + 8], b1, %4, q;\n}\n" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "n"(STEP)
+        : "memory");
+}
+
 // A whole warp's wait.  The first try is where the warp goes on at once; what
 // follows is kept out of line, and out of the instruction cache.
 __device__ __noinline__ void wait_longer(uint32_t bar, uint32_t parity, unsigned int* status, volatile int* abort_flag,
@@ -416,10 +451,14 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
 #pragma unroll
           for (int t = 0; t < C::QT; ++t)
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_ts_w(tw + C::TM_S, tw + C::TM_K + 8 * kk, dq,
-                       ((w * C::QT + C::QT - 1 - t) * C::Q_BYTES + (kk >> 2) * NR * 128 + (kk & 3) * 32) >> 4, idesc_s,
-                       t > 0 || kk > 0);
+            for (int c = 0; c < C::QC; ++c) {  // 64 channels, or what is left of them
+              constexpr int LAST = D / 16 - (C::QC - 1) * 4;
+              const uint32_t at = dq.lo + (((w * C::QT + C::QT - 1 - t) * C::Q_BYTES + c * NR * 128) >> 4);
+              if (c < C::QC - 1)
+                mma_ts_steps<4, 2>(tw + C::TM_S, tw + C::TM_K + 32 * c, at, dq.hi, idesc_s, t > 0 || c > 0);
+              else
+                mma_ts_steps<LAST, 2>(tw + C::TM_S, tw + C::TM_K + 32 * c, at, dq.hi, idesc_s, t > 0 || c > 0);
+            }
           mma_commit_w(s_done(w));
         }
         if (ready >> (W + w) & 1) {
@@ -427,10 +466,10 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
 #pragma unroll
           for (int t = 0; t < C::PT; ++t)
 #pragma unroll
-            for (int kk = 0; kk < BC / 16; ++kk)
-              mma_ts_w(tw + C::TM_O, tw + C::TM_V + 8 * kk, dp,
-                       ((w * C::PT + C::PT - 1 - t) * C::P_BYTES + kk * 16 * C::RB) >> 4, idesc_o,
-                       t > 0 || kk > 0 ? 1u : more);
+            for (int c = 0; c < 2; ++c)
+              mma_ts_steps<4, C::RB>(tw + C::TM_O, tw + C::TM_V + 32 * c,
+                                     dp.lo + (((w * C::PT + C::PT - 1 - t) * C::P_BYTES + c * 64 * C::RB) >> 4), dp.hi, idesc_o,
+                                     t > 0 || c > 0 ? 1u : more);
           mma_commit_w(o_done(w));
         }
       }
