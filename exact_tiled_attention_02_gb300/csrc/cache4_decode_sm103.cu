@@ -29,8 +29,10 @@
 // if no key's does (one barrier with an OR) the tile is exponentiated as it is.
 // Otherwise the column maxima are reduced across lanes and warps and O rescaled.
 //
-// One more warp loads: a tile's blocks, one bulk copy for each run of them in a
-// page.  The work is split as seq_ranges.cuh says, a range a team; a sequence
+// A warp a team loads: a tile's blocks, one bulk copy for each run of them in a
+// page.  (One warp for all teams waited for each tile's pages before it turned to
+// the next team: with pages of 16 tokens, where every tile's are in a sector of
+// their own, 64 sequences of 500 to 8200 took 79 us, with pages of 64 64.)  The work is split as seq_ranges.cuh says, a range a team; a sequence
 // that is one whole piece goes straight to o.
 //
 // Unpacking costs two instructions a pair of codes (a conversion and a product, in
@@ -77,7 +79,7 @@ struct Cfg {
   // half of the softmax, else the half that unpacks K takes all of it.
   static constexpr bool SPLIT = NR > 16;
   static constexpr int NH = SPLIT ? NR / 2 : NA;     // columns of a thread
-  static constexpr int THREADS = W * 256 + 64;
+  static constexpr int THREADS = W * 256 + 32 + W * 32;
   static constexpr int QC = (D + 63) / 64;           // 64-channel chunks of Q
   static constexpr int RB = NR * 2;                  // bytes of a key's row of P
   static constexpr int TILE = 144 * D;               // bytes: 8 blocks of 18 D
@@ -102,7 +104,7 @@ struct Cfg {
   static constexpr int SMEM_USED = OFF_MISC + 8 + W * 28 + SLOTS * 4;
   static constexpr int SMEM_BYTES = SMEM_USED + 1024;
   static constexpr int TM_K = 0, TM_V = KC, TM_S = KC + 64, TM_O = TM_S + NR;
-  static_assert(W >= 2 && W <= 4 && SL >= 2, "two tiles a team in flight, eight lanes a team");
+  static_assert(W >= 2 && SL >= 2, "two tiles a team in flight");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
   static_assert(Q_BYTES % 1024 == 0 && P_BYTES % 1024 == 0 && OFF_RING % 1024 == 0 && TILE % 16 == 0, "alignment");
 };
@@ -324,26 +326,20 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     return 0;
   };
 
-  if (warp == 8 * W + 1) {
+  if (warp > 8 * W) {
     // ---------------------------------------------------------------- loads
-    // Eight lanes a team walk its tiles, a block a lane; the first lane of every
-    // run of blocks that lie side by side in a page copies the run.
-    const int w = lane >> 3, i = lane & 7;
+    // A warp a team: lane i (of 8) looks block i of a tile up, and the first lane
+    // of every run of blocks that lie side by side in a page copies the run.
+    const int w = warp - 8 * W - 1;
     const int per_page = cache.page_size / 16;
-    int head = 0, rg = 0, b = 0, t = 0, left = 0;  // the next tile's head, row group, sequence and place there; tiles to go
-    if (w < W) {
-      head = s_start[6 * w];
-      rg = s_start[6 * w + 1];
-      b = s_start[6 * w + 2];
-      t = s_start[6 * w + 3];
-      left = s_start[6 * w + 4];
-    }
+    const int* start = s_start + 6 * w;  // the next tile's head, row group, sequence and place there; tiles to go
+    int head = start[0], rg = start[1], b = start[2], t = start[3], left = start[4];
     int n = left > 0 ? seq_len(p, b, false) : 0;  // keys of sequence b
     int page = -1, at = -1;  // of this lane's block: -1 past the end, -2 no such page
     auto place = [&]() {
-      const int blk = t * 8 + i;
+      const int blk = t * 8 + lane;
       page = at = -1;
-      if (left <= 0 || blk * 16 >= n) return;
+      if (left <= 0 || lane >= 8 || blk * 16 >= n) return;
       const int q = blk / per_page;
       at = blk - q * per_page;
       page = cache.table != nullptr ? cache.table[static_cast<long long>(b) * cache.max_pages + q] : b;
@@ -352,65 +348,40 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
     place();
     int slot = w * C::SL, used = 0;  // the next ring slot, tiles issued
     uint32_t par = 1;                // of the slot's release: the first round waits for none
-    unsigned long long since = 0;
-    while (__any_sync(0xffffffffu, left > 0)) {
-      bool go = false;
-      if (left > 0) {
-        uint32_t ok;
-        asm volatile(
-            "{\n.reg .pred p;\n"
-            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-            "selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(free_(slot)), "r"(par)
-            : "memory");
-        go = ok != 0;
-      }
-      go = (__ballot_sync(0xffffffffu, go) >> (8 * w) & 1) != 0;  // a team's lanes go together
-      const bool here = go && page >= 0, gone = go && page == -2;
-      if (gone) atomicOr(p.status, kStatusInput);
-      const unsigned missing = __ballot_sync(0xffffffffu, gone) >> (8 * w) & 0xffu;
-      const unsigned have = __ballot_sync(0xffffffffu, here) >> (8 * w) & 0xffu;
+    while (left > 0) {
+      if (!warp_wait(free_(slot), par, wc)) break;
+      const bool here = page >= 0;
+      if (page == -2) atomicOr(p.status, kStatusInput);
+      const unsigned missing = __ballot_sync(0xffffffffu, page == -2);
+      const unsigned have = __ballot_sync(0xffffffffu, here);
       const int before = __shfl_up_sync(0xffffffffu, page, 1);
-      const bool starts = here && (i == 0 || before != page || at == 0);
-      const unsigned heads = __ballot_sync(0xffffffffu, starts) >> (8 * w) & 0xffu;
-      if (go && i == 0) {
+      const bool starts = here && (lane == 0 || before != page || at == 0);
+      const unsigned heads = __ballot_sync(0xffffffffu, starts);
+      if (lane == 0) {
         s_missing[slot] = static_cast<int>(missing);
         mbar_arrive_expect_tx(full(slot), __popc(have) * 18 * D);
       }
       __syncwarp();
       if (starts) {
-        const unsigned ends = (heads | ~have) & (0xfffffffeu << i);  // never empty: bit 8 of ~have is set
-        const int run = __ffs(ends) - 1 - i;
+        const unsigned ends = (heads | ~have) & (0xfffffffeu << lane);  // never empty: lanes from 8 on have none
+        const int run = __ffs(ends) - 1 - lane;
         const long long src = ((static_cast<long long>(page) * cache.Hkv + head) * per_page + at) * (18 * D);
-        bulk_load(sRing + slot * C::TILE + i * 18 * D, cache.cache + src, run * 18 * D, full(slot));
+        bulk_load(sRing + slot * C::TILE + lane * 18 * D, cache.cache + src, run * 18 * D, full(slot));
       }
-      if (go) {
-        --left;
-        ++used;
-        if (++slot == (w + 1) * C::SL) {
-          slot = w * C::SL;
-          par ^= 1;
-        }
-        if (++t * BC >= n) {  // the next sequence with keys
-          t = 0;
-          n = left > 0 ? next_seq(head, rg, b) : 0;
-        }
-        place();
+      --left;
+      ++used;
+      if (++slot == (w + 1) * C::SL) {
+        slot = w * C::SL;
+        par ^= 1;
       }
+      if (++t * BC >= n) {  // the next sequence with keys
+        t = 0;
+        n = left > 0 ? next_seq(head, rg, b) : 0;
+      }
+      place();  // the next tile's pages, while this one loads
       __syncwarp();
-      if (__any_sync(0xffffffffu, go)) {
-        since = 0;
-      } else if (since == 0) {
-        since = globaltimer_ns();
-      } else {
-        // no slot has been released: the wait is bounded like every other
-        const bool late = __any_sync(0xffffffffu, globaltimer_ns() - since > wc.limit_ns);
-        if (late) record_timeout(wc);
-        if (__any_sync(0xffffffffu, late || *abort_flag != 0)) break;
-      }
     }
-    if (*abort_flag && i == 0 && w < W) {
+    if (*abort_flag && lane == 0) {
       // let copies already in flight land before the CTA's shared memory is
       // released; a wait for copies that were never issued just runs out
       WaitCtl drain{nullptr, nullptr, wc.limit_ns};
