@@ -39,12 +39,14 @@
 // pipes that take 2.6 cycles for both), 330 cycles a tile of d = 128 for the 830
 // that its 18 KB take at the copy rate; at 4 rows the whole tile is 600
 // instructions a scheduler.  64 sequences of 4096 to 32768 tokens, 32 / 8 heads,
-// d = 128: 224 us, 6.1 TB/s (90% of the copy rate).  500 to 8200 tokens: 67.5 us,
-// 63 of them this kernel; 7 go by before its first tile has come (length, page,
-// tile: three dependent loads) and after its last.  With 32 rows two teams fit
-// tensor memory instead of three, and the warps there are keep the schedulers busy
-// 59% of the time: 32 sequences, 64 / 8 heads x 4 tokens, 1000 to 16384: 104 us.
-// 512 tokens, 64 rows a group: 125 us, 568 TFLOP/s, 66% of the issue slots.
+// d = 128: 216 us, 6.3 TB/s (93% of the copy rate).  500 to 8200 tokens: 66 us, 7
+// of them before its first tile has come (length, page, tile: three dependent
+// loads), after its last, and for the merge.  With 32 rows two teams fit tensor
+// memory instead of three, and the softmax's instructions come to 300 a tile more:
+// 32 sequences, 64 / 8 heads x 4 tokens, 1000 to 16384: 99 us.  (S^T in columns of
+// V^T made room for three teams, whose S^T then waited for the last O^T: 107 for
+// 96.)  512 tokens, 64 rows a group: 125 us, 565 TFLOP/s, two thirds of the issue
+// slots.
 #include <cmath>
 #include <type_traits>
 
@@ -953,7 +955,11 @@ DecodePlan cache4_plan(int n_seq, int heads, int rows, int d, fa_dtype dt, int s
   DecodePlan w{};
   w.n_seq = n_seq;
   w.heads = heads;
-  // float32: at most 32 rows, whose terms of Q and P leave the ring its room
+  // The narrowest product that holds the rows (32 sequences of 1000 to 16384
+  // tokens, 8 heads, d = 128: 4 rows 61, 92, 119 us with 16, 32, 64 columns; 16
+  // rows 73, 93, 121; 24 rows, in two groups of 16, 130, 95, 125; 32 rows 132, 96,
+  // 126; 64 rows 247, 178, 133).  float32: at most 32, whose terms of Q and P leave
+  // the ring its room.
   w.nr = rows <= 16 ? 16 : rows <= 32 || dt == FA_DTYPE_F32 ? 32 : 64;
   w.row_groups = (rows + w.nr - 1) / w.nr;
   w.cuts = sms * (dt == FA_DTYPE_F32 ? teams<true>(d, w.nr) : teams<false>(d, w.nr));  // a CTA an SM, a range a team
