@@ -299,3 +299,21 @@ def test_scores_that_rise_and_fall(fa, dtype):
             if scale < 2:  # past that the bound on a score's error allows any softmax
                 sb.check("o", sb.f64(o[0]), ref, tol)
             assert torch.isfinite(o).all()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64), ("bf16", 80)])
+def test_a_token_that_is_no_number(fa, dtype, d):
+    """A NaN among a sequence's keys or values is not lost, and stays with its sequence and head."""
+    rng = np.random.default_rng(8)
+    k, v = tokens(rng, dtype, 3, 2, 200, d), tokens(rng, dtype, 3, 2, 200, d)
+    k[0, 1, 150, 7], v[2, 0, 3, 20] = float("nan"), float("nan")
+    cache = torch.zeros((3, 2, 208, 9 * d // 8), dtype=torch.uint8, device="cuda")
+    lens = i32([200, 200, 200])
+    fa.fa_cache_fp4_write(k.cuda(), v.cuda(), cache, lens)
+    q = torch.from_numpy(rng.standard_normal((3, 8, 1, d))).to(TYPES[dtype]).cuda()
+    o, lse = fa.fa_fwd_cache_fp4(q, cache, lens)
+    o, lse = torch.isnan(o[:, :, 0]).cpu(), torch.isnan(lse[:, :, 0]).cpu()
+    want_o, want_l = torch.zeros(3, 8, d, dtype=torch.bool), torch.zeros(3, 8, dtype=torch.bool)
+    want_o[0, 4:] = want_l[0, 4:] = True
+    want_o[2, :4, 16:32] = True
+    assert torch.equal(o, want_o) and torch.equal(lse, want_l)
