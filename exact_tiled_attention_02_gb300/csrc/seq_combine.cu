@@ -47,11 +47,12 @@ __global__ void __launch_bounds__(kWarps * 32)
   for (int s0 = 0; s0 < splits; s0 += 32) {
     const float ls = s0 == 0 ? mine : (s0 + lane < splits ? part_lse[(s0 + lane) * total + row] : -INFINITY);
     const float w = expf(ls - ref) * inv;
+    const unsigned holds = __ballot_sync(0xffffffffu, ls != -INFINITY);
     const int k = min(32, splits - s0);
 #pragma unroll 8
     for (int i = 0; i < k; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      if (wi != 0.f && c < dv) acc = fmaf(wi, part_o[((s0 + i) * total + row) * dv + c], acc);
+      if ((holds >> i & 1) && c < dv) acc = fmaf(wi, part_o[((s0 + i) * total + row) * dv + c], acc);
     }
   }
   if (c < dv) {

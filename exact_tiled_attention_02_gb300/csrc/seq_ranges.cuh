@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(128)
   for (int i0 = 0; i0 < n; i0 += 32) {
     const float ls = i0 == 0 ? mine : (i0 + lane < n ? part_lse(i0 + lane) : -INFINITY);
     const float wl = expf(ls - ref) * inv;
+    const unsigned holds = __ballot_sync(0xffffffffu, ls != -INFINITY);  // a part without keys holds zeros or nothing
     const int k = min(32, n - i0);
 #pragma unroll 1
     for (int i = 0; i < k; i += U) {  // the loads of U parts do not wait for one another
@@ -239,18 +240,18 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         wi[u] = __shfl_sync(0xffffffffu, wl, (i + u) & 31);
-        if (i + u >= k) wi[u] = 0.f;
+        const bool on = i + u < k && (holds >> ((i + u) & 31) & 1);
         const int part = i0 + i + u;
         const float* src = (part < pre ? pre_o + (part * p.total + row) * p.dv
                                        : p.part_o + (slot0 + static_cast<long long>(part - pre) * NR) * p.dv) + c;
 #pragma unroll
-        for (int w = 0; w < W; ++w)  // a part without keys holds zeros or nothing
-          v[u][w] = wi[u] != 0.f && c + 128 * w < p.dv ? *reinterpret_cast<const float4*>(src + 128 * w)
+        for (int w = 0; w < W; ++w)
+          v[u][w] = on && c + 128 * w < p.dv ? *reinterpret_cast<const float4*>(src + 128 * w)
                                                        : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (wi[u] == 0.f) continue;
+        if (i + u >= k) break;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           acc[w].x = fmaf(wi[u], v[u][w].x, acc[w].x);
