@@ -37,7 +37,7 @@
 //
 // Unpacking costs two instructions a pair of codes (a conversion and a product, in
 // pipes that take 2.6 cycles for both), 330 cycles a tile of d = 128 for the 830
-// that its 18 KB take at the copy rate; at 4 rows the whole tile is 600
+// that its 18 KB take at the copy rate; at 4 rows the whole tile is 640
 // instructions a scheduler.  64 sequences of 4096 to 32768 tokens, 32 / 8 heads,
 // d = 128: 216 us, 6.3 TB/s (93% of the copy rate).  500 to 8200 tokens: 66 us, 7
 // of them before its first tile has come (length, page, tile: three dependent
