@@ -281,17 +281,21 @@ cudaError_t launch_merge(const SeqAttn& p, const DecodePlan& w, const float* pre
   // (the whole call at 16384 rows: 105 us, 117 with a warp a slice; at 1024
   // rows 71 and 68; at 16 rows 18.9 and 15.4).
   const long long rows = static_cast<long long>(w.n_seq) * w.heads * p.rows;
-  const bool wide = p.dv > 128 && rows >= 152 * 32;
+  const bool wide = !FLAT && p.dv > 128 && rows >= 152 * 32;  // (the flat form's rows are of 128 at most)
   const long long warps = rows * (wide ? (p.dv + 511) / 512 : (p.dv + 127) / 128);
   if (warps > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
-  if (!after) {  // no kernel of this call before it: the lengths may only now be complete
-    fa_seq_decode_merge_kernel<BC, NR, 1, T, FLAT><<<static_cast<unsigned>((rows * ((p.dv + 127) / 128) + 3) / 4), 128, 0, s>>>(
-        p, w, pre_o, pre_lse, pre);
-    return cudaGetLastError();
+  if constexpr (FLAT) {
+    return launch_after(fa_seq_decode_merge_kernel<BC, NR, 1, T, true>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
+  } else {
+    if (!after) {  // no kernel of this call before it: the lengths may only now be complete
+      fa_seq_decode_merge_kernel<BC, NR, 1, T, false><<<static_cast<unsigned>((rows * ((p.dv + 127) / 128) + 3) / 4), 128, 0, s>>>(
+          p, w, pre_o, pre_lse, pre);
+      return cudaGetLastError();
+    }
+    return wide ? launch_after(fa_seq_decode_merge_kernel<BC, NR, 4, T, false>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre)
+                : launch_after(fa_seq_decode_merge_kernel<BC, NR, 1, T, false>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
   }
-  return wide ? launch_after(fa_seq_decode_merge_kernel<BC, NR, 4, T, FLAT>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre)
-              : launch_after(fa_seq_decode_merge_kernel<BC, NR, 1, T, FLAT>, blocks, 128, 0, s, p, w, pre_o, pre_lse, pre);
 }
 
 }  // namespace seq
