@@ -31,9 +31,10 @@
 //
 // A warp a team loads: a tile's blocks, one bulk copy for each run of them in a
 // page.  (One warp for all teams waited for each tile's pages before it turned to
-// the next team: with pages of 16 tokens, where every tile's are in a sector of
-// their own, 64 sequences of 500 to 8200 took 79 us, with pages of 64 64.)  The work is split as seq_ranges.cuh says, a range a team; a sequence
-// that is one whole piece goes straight to o.
+// the next team; with pages of 16 tokens, where every tile's entries are in a
+// sector of their own, 64 sequences of 500 to 8200 took 79 us for 64 now.)  The
+// work is split as seq_ranges.cuh says, a range a team; a sequence that is one
+// whole piece goes straight to o.
 //
 // Unpacking costs two instructions a pair of codes (a conversion and a product, in
 // pipes that take 2.6 cycles for both), 330 cycles a tile of d = 128 for the 830
@@ -60,8 +61,8 @@ using namespace seq;
 
 constexpr int BC = 128;  // keys per tile
 // A row's reference is 2^7 below the largest score when it was set, and rises
-// once a score is 2^8 above that: P is at most 2^15, and fp16's least step at
-// least 2^-32 of the largest P.
+// once a score is 2^8 above that: P is at most 2^15, and fp16's smallest half
+// step, 2^-25, at most 2^-32 of the largest P.
 constexpr float kBelow = 7.0f, kRescaleThreshold = kBelow + 8.0f;
 
 // F32: float32 q and o.  Q is then three fp16 terms and P two, 2^-33 and 2^-22

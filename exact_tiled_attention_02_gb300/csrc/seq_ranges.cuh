@@ -3,7 +3,7 @@
 // of rows), and the kernel that merges the pieces of sequences that several
 // CTAs share.  The cut depends on the lengths alone.  The flat form lays the
 // tiles of all groups of rows end to end too: any number of groups fills the
-// GPU, at the price of 64-bit products.
+// GPU, at the price of a few divisions (in 64 bits only where tiles pass 32).
 #pragma once
 
 #include <cmath>
