@@ -317,3 +317,20 @@ def test_a_token_that_is_no_number(fa, dtype, d):
     want_o[0, 4:] = want_l[0, 4:] = True
     want_o[2, :4, 16:32] = True
     assert torch.equal(o, want_o) and torch.equal(lse, want_l)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("power", [100, -100])
+def test_queries_far_from_one(fa, dtype, power):
+    """Queries of 2^100 and 2^-100 with a scale that brings the scores back."""
+    rng = np.random.default_rng(12)
+    d, n, page = 96, 250, 32
+    cache = cc.random_cache(rng, 8, 2, page, d)
+    table = np.arange(8, dtype=np.int32)[None]
+    q = torch.from_numpy(rng.standard_normal((1, 6, 3, d)) * 2.0 ** power).to(TYPES[dtype])
+    scale = 0.1 * 2.0 ** -power
+    o, lse = fa.fa_fwd_cache_fp4(q.cuda(), torch.from_numpy(cache).cuda(), i32([n]), scale=scale, block_table=i32(table))
+    k, v = cc.dense(cache, table, 0, n, d, page, 1.0, 1.0)
+    ref, lr, tol, tol_l = cc.forward(sb.f64(q[0]), k, v, float(np.float32(scale)), dtype)
+    sb.check("lse", sb.f64(lse[0]), lr, tol_l)
+    sb.check("o", sb.f64(o[0]), ref, tol)
