@@ -39,7 +39,7 @@ __device__ __forceinline__ int length(const Cache4& c, int b, bool report) {
 }
 // The page of block i of sequence b, or -1 (reported) where the table has none.
 __device__ __forceinline__ int page_of(const Cache4& c, int b, int i) {
-  const int at = i * kBlock / c.page_size;
+  const int at = i / (c.page_size / kBlock);
   const int page = c.table != nullptr ? c.table[static_cast<long long>(b) * c.max_pages + at] : b;
   if (page >= 0 && page < c.n_pages) return page;
   atomicOr(c.status, kStatusInput);

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   const int p0 = max(len - n, 0);  // positions p0 .. len - 1 are written
   const int blk = p0 / kBlock + rest % per;
-  if (blk * kBlock >= len) return;
+  if (blk >= (len + kBlock - 1) / kBlock) return;  // (in blocks: a position past the end may pass 32 bits)
   const int page = page_of(c, b, blk);
   if (page < 0) return;
   uint8_t* dst = c.cache + block_at(c, page, h, blk);

@@ -1,0 +1,56 @@
+"""The 4-bit cache's calls at their borders: capacities near 2^31 tokens,
+pages that sequences share, numbers on the borders of the format, bytes around
+what a call writes."""
+
+import numpy as np
+import pytest
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def fa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from exact_tiled_attention_02_gb300 import binding
+    return binding
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def quantised(x, scale):
+    """What float64 ``x`` is held as, its division by the tensor's scale float32's."""
+    y = (torch.from_numpy(x).float() / torch.tensor(scale, dtype=torch.float32)).double().numpy()
+    return oracle.cache4_quantise(y, 1.0)
+
+
+def test_more_rows_than_positions_are_left(fa):
+    """A sequence of 2^31 - 2^20 tokens (its table repeats one page) and 2^21
+    rows, of which one is new: of the blocks that so many rows could touch, those
+    past the end would begin beyond 2^31."""
+    page, max_pages, Nn, d = 1 << 20, 2047, 1 << 21, 16
+    rng = np.random.default_rng(0)
+    cache = torch.full((1, 1, page, 9 * d // 8), 0x11, dtype=torch.uint8, device="cuda")
+    k = torch.full((1, 1, Nn, d), float("nan"), dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    new = [torch.from_numpy(rng.standard_normal(d)).bfloat16() for _ in range(2)]
+    k[0, 0, -1], v[0, 0, -1] = new[0].cuda(), new[1].cuda()
+    fa.fa_cache_fp4_write(k, v, cache, i32([page * max_pages]), block_table=i32([[0] * max_pages]), n_new=i32([1]))
+    torch.cuda.synchronize()
+    assert fa.fa_last_device_status() == fa.FA_OK
+    got = cache.view(-1, 18 * d)
+    assert (got[:-1] == 0x11).all()
+    parts = [x.copy() for x in oracle.cache4_unpack(np.full(18 * d, 0x11), d)]
+    for i, x in enumerate(new):
+        parts[2 * i][15], parts[2 * i + 1][15] = oracle.cache4_quantise(x.double().numpy(), 1.0)
+    have = oracle.cache4_unpack(got[-1].cpu().numpy(), d)
+    for a, b in zip(have, parts):
+        assert (np.where(a == 8, 0, a) == np.where(b == 8, 0, b)).all()
