@@ -19,10 +19,11 @@ fa_status cache_check(const void* cache, const int* table, const int* lens, int 
   if (page_size % 16 != 0 || d % 16 != 0 || d > kMaxD) return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
-// a warp a block of 16 tokens and head, four a CTA
+// a warp a block of 16 tokens and head, four a CTA; a sequence's are counted in 31 bits
 bool blocks_ok(int B, int Hkv, int n) {
-  return sizes_ok(B, Hkv, n) && n <= 0x3fffffff &&
-         static_cast<double>(B) * Hkv * ((n + 14) / 16 + 1) < 4.0 * 0x7ffffff0;
+  if (!sizes_ok(B, Hkv, n) || n > 0x3fffffff) return false;
+  const long long per = static_cast<long long>(Hkv) * ((n + 14) / 16 + 1);
+  return per <= 0x7fffffffLL && static_cast<double>(B) * per < 4.0 * 0x7ffffff0;
 }
 Cache4 cache_of(const void* cache, const int* table, const int* lens, int B, int Hkv, int n_pages, int page_size,
                 int max_pages, int d, float k_scale, float v_scale) {

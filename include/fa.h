@@ -349,7 +349,9 @@ size_t fa_bwd_latent_workspace_bytes(int B, int H, int Nq, int Nk, int dn, int d
  *              and pages, uncovered positions (any bytes), workspaces and sizes
  *              hold here too, with Nq for new queries, unless stated otherwise.
  *   Sizes      page_size and d multiples of 16, d <= 256 (others return
- *              FA_ERR_UNSUPPORTED).
+ *              FA_ERR_UNSUPPORTED).  Rows written or read, n a sequence: n <
+ *              2^30, Hkv (floor((n + 14) / 16) + 1) < 2^31, and B times that
+ *              below 2^33 - 64 (the blocks that they can touch).
  */
 
 /* Bytes of a cache, or 0 for sizes that the calls refuse. */
