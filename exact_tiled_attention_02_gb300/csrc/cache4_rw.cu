@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     n = min(max(n_new[b], 0), Nn);
     if (n != n_new[b] && lane == 0) atomicOr(c.status, kStatusInput);
   }
+  if (n == 0) return;  // not even its last block's own bits are put back: another sequence may be writing to that page
   const int p0 = max(len - n, 0);  // positions p0 .. len - 1 are written
   const int blk = p0 / kBlock + rest % per;
   if (blk >= (len + kBlock - 1) / kBlock) return;  // (in blocks: a position past the end may pass 32 bits)

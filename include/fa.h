@@ -369,7 +369,8 @@ size_t fa_cache_fp4_bytes(int n_pages, int Hkv, int page_size, int d);
  *                sequence written.
  * Other tokens of the cache keep their bits.  A byte holds codes of two
  * neighbouring tokens: calls that write to one page must run in order, and a
- * page must not appear twice among those that a call writes to.
+ * page must not appear twice among those that a call writes to (a sequence
+ * writes to the pages of its new tokens' positions, and to none without any).
  */
 fa_status fa_cache_fp4_write(const void* k, const void* v, void* cache, const int* block_table, const int* lens,
                              const int* n_new, int B, int Hkv, int Nn, int n_pages, int page_size, int max_pages,

@@ -54,3 +54,26 @@ def test_more_rows_than_positions_are_left(fa):
     have = oracle.cache4_unpack(got[-1].cpu().numpy(), d)
     for a, b in zip(have, parts):
         assert (np.where(a == 8, 0, a) == np.where(b == 8, 0, b)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_sequence_without_new_tokens_leaves_its_page_alone(fa, dtype):
+    """One sequence of 200 writes to a page that all of them hold; the others'
+    lengths end in the block that it writes to.  Nothing it wrote is lost, and a
+    table without pages is not looked at where there is nothing to write."""
+    B, Hkv, page, d = 200, 4, 64, 128
+    rng = np.random.default_rng(1)
+    lens, n_new = [25] * B, [0] * B
+    lens[100], n_new[100] = 30, 6
+    table = np.zeros((B, 2), dtype=np.int32)
+    table[7] = table[150] = -1
+    for seed in range(30):
+        k, v = (torch.from_numpy(rng.standard_normal((B, Hkv, 6, d))).to(TYPES[dtype]).cuda() for _ in range(2))
+        alone = torch.full((3, Hkv, page, 9 * d // 8), 0x11, dtype=torch.uint8, device="cuda")
+        cache = alone.clone()
+        one = slice(100, 101)
+        fa.fa_cache_fp4_write(k[one], v[one], alone, i32(lens[one]), block_table=i32(table[one]))
+        fa.fa_cache_fp4_write(k, v, cache, i32(lens), block_table=i32(table), n_new=i32(n_new))
+        torch.cuda.synchronize()
+        assert fa.fa_last_device_status() == fa.FA_OK
+        assert torch.equal(cache, alone) and not (cache[0] == 0x11).all()
