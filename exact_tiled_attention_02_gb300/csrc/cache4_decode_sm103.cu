@@ -850,7 +850,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         const long long orow0 = row_of(head, rg, b);
         if (tid < NA) {
           const float sum = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
-          fac[tid] = sum == 0.f ? 0.f : cache.v_scale / sum;
+          fac[tid] = sum == 0.f ? 0.f : 1.f / sum;
           // (one product in 64 bits: the reference may be large beside the logarithm; no key seen: -inf)
           const float lse = sum == 0.f ? -INFINITY : static_cast<float>(logf(sum) - ref[tid] * 0.69314718055994531);
           if (tid < n_rows && !*abort_flag) {
@@ -864,6 +864,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         tc_fence_after();
         rows_sync();
         auto put_o = [&](int row, float y) {
+          y *= cache.v_scale;  // (not part of fac: v_scale / sum may be too small a number where O is not)
           if (!whole)
             p.part_o[(part * NR + row) * D + id] = y;
           else if constexpr (F32)

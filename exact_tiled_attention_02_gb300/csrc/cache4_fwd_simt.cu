@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads) fa_cache4_fwd_simt_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = 2 * warp + i;
-      alpha[r] = l[i] == 0.f ? 0.f : c.v_scale / l[i];
+      alpha[r] = l[i] == 0.f ? 0.f : 1.f / l[i];
       if (r0 + r >= rows) continue;
       const float lse = m[i] + logf(l[i]);  // no key: -inf
       if (p.splits > 1)
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) fa_cache4_fwd_simt_kernel(const __gr
 #pragma unroll
     for (int r = 0; r < TR; ++r) {
       if (r0 + r >= rows) break;
-      const float y = alpha[r] == 0.f ? 0.f : acc[x][r] * alpha[r];
+      const float y = alpha[r] == 0.f ? 0.f : acc[x][r] * alpha[r] * c.v_scale;  // (v_scale / l may be too small a number)
       if (p.splits > 1)
         p.part_o[(split * total + row0 + r) * d + ch] = y;
       else if constexpr (sizeof(T) == 2)

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 import oracle
+from tests import cache4_common as cc
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +78,25 @@ def test_a_sequence_without_new_tokens_leaves_its_page_alone(fa, dtype):
         torch.cuda.synchronize()
         assert fa.fa_last_device_status() == fa.FA_OK
         assert torch.equal(cache, alone) and not (cache[0] == 0x11).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 80])
+@pytest.mark.parametrize("power", [-124, -60, 110])
+def test_values_scale_of_any_magnitude(fa, d, power):
+    """O is proportional to v_scale, far from 1 too: a power of two moves it as a
+    whole.  What may differ: O is a float32 number of its own (2^-24), a piece of a
+    sequence is one before pieces are merged (2^-24 again, and the merge's sums are
+    of numbers scaled alike), and below 2^-126 each of at most 64 pieces and the
+    result is rounded to 2^-149."""
+    rng = np.random.default_rng(2)
+    B, Hq, Hkv, page, lens = 3, 8, 2, 32, [1000, 5, 129]
+    table, pages = cc.place(rng, B, 32, lens, page)
+    cache = torch.from_numpy(cc.random_cache(rng, pages, Hkv, page, d)).cuda()
+    q = torch.from_numpy(rng.standard_normal((B, Hq, 1, d))).float().cuda()
+    kw = dict(block_table=i32(table), k_scale=0.25)
+    one, lse = fa.fa_fwd_cache_fp4(q, cache, i32(lens), v_scale=1.0, **kw)
+    far, lse2 = fa.fa_fwd_cache_fp4(q, cache, i32(lens), v_scale=2.0 ** power, **kw)
+    assert fa.fa_last_device_status() == fa.FA_OK and torch.equal(lse, lse2)
+    want = one.double() * 2.0 ** power
+    assert ((far.double() - want).abs() <= 2.0 ** -21 * want.abs() + 65 * 2.0 ** -150).all()
+    assert (want != 0).any()
