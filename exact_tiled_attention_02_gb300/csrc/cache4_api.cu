@@ -121,7 +121,8 @@ fa_status fa_fwd_cache_fp4(const void* q, const void* cache, const int* block_ta
   const fa_status st =
       cache_check(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale, dt);
   if (st != FA_OK) return st;
-  if (!scale_ok(scale) || !scale_ok(scale * k_scale)) return FA_ERR_INVALID;
+  if (!scale_ok(scale) || !std::isnormal(scale * k_scale) || !std::isfinite(scale * k_scale * 1.4426950408889634f))
+    return FA_ERR_INVALID;  // scores are multiplied with these in float32
   if (workspace_bytes < fa_fwd_cache_fp4_workspace_bytes(B, Hq, Hkv, Nq, page_size, max_pages, d))
     return FA_ERR_INVALID;
   Cache4 c = cache_of(cache, block_table, lens, B, Hkv, n_pages, page_size, max_pages, d, k_scale, v_scale);

@@ -396,6 +396,8 @@ fa_status fa_cache_fp4_read(const void* cache, const int* block_table, const int
  *                aligned, as above.
  * Hq must be a multiple of Hkv; Hkv ceil(Hq / Hkv Nq / 16) B tiles of 128
  * tokens / 304 must stay below 2^31 too.  Forward only: a serving call.
+ * scale k_scale and scale k_scale / ln 2 must be normal float32 numbers (others
+ * return FA_ERR_INVALID).
  * d = 64, 96 and 128 run on the tensor cores, with fp32 accumulation: code * s
  * is exact in fp16, a row of q is brought to fp16 by a power of two (bf16: exact
  * down to 2^-31 of its largest entry; float32: as three terms), and P, rounded
