@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   extern __shared__ uint2 smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int d = c.d, groups = d / 16;
-  uint2* codes = smem + warp * 2 * d;  // [16 tokens][d/16]
+  uint2* codes = smem + warp * d;  // [16 tokens][d/16]
   const int per = blocks_of(Nn);
   const long long at = static_cast<long long>(blockIdx.x) * kWarps + warp;
   const int b = static_cast<int>(at / (static_cast<long long>(per) * c.Hkv));
@@ -257,7 +257,7 @@ cudaError_t launch_write(const Cache4& c, const void* k, const void* v, const in
   const long long blocks = (warps + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned grid = static_cast<unsigned>(blocks);
-  const int smem = kWarps * c.d * 16;
+  const int smem = kWarps * c.d * 8;
   const T *kt = static_cast<const T*>(k), *vt = static_cast<const T*>(v);
   constexpr Quotient kFast = sizeof(T) == 2 ? kShort : kMultiply;
   if (power_of_two(c.k_scale) && power_of_two(c.v_scale))
