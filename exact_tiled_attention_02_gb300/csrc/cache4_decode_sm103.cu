@@ -979,8 +979,9 @@ cudaError_t launch_cache4_decode(const SeqAttn& p, const Cache4& c, const Decode
 template <typename T>
 static cudaError_t merge_of(const SeqAttn& p, const DecodePlan& w, cudaStream_t s) {
   if (w.nr == 16) return launch_merge<BC, 16, T, true>(p, w, nullptr, nullptr, 0, true, s);
-  if (w.nr == 32) return launch_merge<BC, 32, T, true>(p, w, nullptr, nullptr, 0, true, s);
-  return launch_merge<BC, 64, T, true>(p, w, nullptr, nullptr, 0, true, s);
+  if constexpr (sizeof(T) == 2)  // (float32 has at most 32: cache4_plan)
+    if (w.nr == 64) return launch_merge<BC, 64, T, true>(p, w, nullptr, nullptr, 0, true, s);
+  return launch_merge<BC, 32, T, true>(p, w, nullptr, nullptr, 0, true, s);
 }
 cudaError_t launch_cache4_merge(const SeqAttn& p, const DecodePlan& w, fa_dtype dt, cudaStream_t s) {
   return dt == FA_DTYPE_F32 ? merge_of<float>(p, w, s) : merge_of<__nv_bfloat16>(p, w, s);
