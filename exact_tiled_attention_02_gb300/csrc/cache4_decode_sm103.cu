@@ -25,8 +25,9 @@
 // team do not wait for one another around them.
 //
 // Statistics run down the columns, across lanes.  Per tile a thread (one key)
-// only checks whether any of its scores exceeds its column's reference by 2^8;
-// if no key's does (one barrier with an OR) the tile is exponentiated as it is.
+// only checks whether any P of it would exceed 2^15, that is whether a score is
+// 15 above its column's reference (log2 domain), 8 above the score that set it;
+// if no key's is (one barrier with an OR) the tile is exponentiated as it is.
 // Otherwise the column maxima are reduced across lanes and warps and O rescaled.
 //
 // A warp a team loads: a tile's blocks, one bulk copy for each run of them in a
@@ -60,9 +61,9 @@ namespace {
 using namespace seq;
 
 constexpr int BC = 128;  // keys per tile
-// A row's reference is 2^7 below the largest score when it was set, and rises
-// once a score is 2^8 above that: P is at most 2^15, and fp16's smallest half
-// step, 2^-25, at most 2^-32 of the largest P.
+// A row's reference is 7 (log2 domain: a factor 2^7) below the largest score when
+// it was set, and rises once a score is 8 above that one: P is at most 2^15, and
+// fp16's smallest half step, 2^-25, at most 2^-32 of the largest P.
 constexpr float kBelow = 7.0f, kRescaleThreshold = kBelow + 8.0f;
 
 // F32: float32 q and o.  Q is then three fp16 terms and P two, 2^-33 and 2^-22

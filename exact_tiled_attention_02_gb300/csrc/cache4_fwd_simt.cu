@@ -1,6 +1,6 @@
 // cache4_fwd_simt.cu -- attention of a sequence's last tokens over the 4-bit
-// cache, fp32 on CUDA cores: float32 tensors, and bf16 ones of head widths
-// that the tensor-core kernel does not take.
+// cache, fp32 on CUDA cores: bf16 and float32 tensors of the head widths that
+// the tensor-core kernel does not take (all but 64, 96 and 128).
 //
 //   S_ij = scale k_scale (q_i . K_j),  O_i = v_scale sum_j softmax_j(S_i) V_j
 //
