@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(Cfg<D, NR, NA, F32>::THREADS, 1)
         const long long orow0 = row_of(head, rg, b);
         if (tid < NA) {
           const float sum = (red[tid] + red[NR + tid]) + (red[2 * NR + tid] + red[3 * NR + tid]);
-          fac[tid] = sum == 0.f ? 0.f : 1.f / sum;
+          fac[tid] = sum == 0.f ? 0.f : __frcp_rn(sum);
           // (one product in 64 bits: the reference may be large beside the logarithm; no key seen: -inf)
           const float lse = sum == 0.f ? -INFINITY : static_cast<float>(logf(sum) - ref[tid] * 0.69314718055994531);
           if (tid < n_rows && !*abort_flag) {
