@@ -10,6 +10,12 @@
 //
 // One CTA of 128 threads per 8 query rows of a key/value head and split of its
 // keys; tiles of 64 keys are unpacked to shared memory.
+//
+// For completeness of widths, not for speed: every CTA unpacks its keys for 8
+// rows at most (4 in use at 4 query heads a key head), four CTAs of four warps an
+// SM at d = 80 and one at 256, with five barriers a tile.  64 sequences of 500 to
+// 8200 tokens, 32 / 8 heads, either type: d = 80 1100 us, 112 1520, 256 6160, where
+// the bytes take 30, 42 and 95 and the tensor-core kernel 67 at d = 128.
 #include <cmath>
 
 #include "cache4.cuh"
