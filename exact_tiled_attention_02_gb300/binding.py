@@ -610,7 +610,7 @@ def fa_cache_fp4_write(k, v, cache, lens, block_table=None, n_new=None, k_scale:
     max_pages], or None when sequence b is page b; ``n_new``: int32 [B], how
     many of the last rows are tokens of sequence b, or None for all.
     ``k_scale, v_scale``: what the stored numbers are multiples of (the header
-    has the format).
+    has the format); powers of two, both, are written fastest.
     """
     torch = _torch()
     code = _first("k", k, 4)
